@@ -397,6 +397,110 @@ ls_status segmented_scan_offsets(const void *in, void *out, int64_t n, ls_dtype 
                                  int exclusive, const int64_t *offsets, int64_t nseg, void *total,
                                  void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * A decoding step: one token from each row of logits, and the books of a paged
+ * cache (which pages a request holds, where its new tokens go).  The same common
+ * rules hold: asynchronous on `stream`, arguments checked on the host before
+ * anything is enqueued, kernels only (so calls can be captured in a graph), no
+ * library call.  Results are the same bits on every run.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the logits. */
+typedef enum ls_logits {
+    LS_LOGITS_FLOAT32 = 0,
+    LS_LOGITS_FLOAT16 = 1,
+    LS_LOGITS_BFLOAT16 = 2
+} ls_logits;
+
+/* Workspace size for sample_tokens.  Errors: LS_ERR_INVALID_ARG for bytes == NULL,
+ * rows or vocab outside [0, 2^31 - 1]. */
+ls_status ls_sample_workspace_bytes(int64_t rows, int64_t vocab, size_t *bytes);
+
+/* One token from each row, by given random numbers.  For a row x with largest
+ * value M and temperature T > 0, token i has the weight w_i = exp((x_i - M) / T);
+ * NaN counts as -infinity, and -infinity (a masked token) has no weight.  With the
+ * tokens in order of x, largest first, equal ones by index:
+ *   top_k  keeps the first k of the order (k <= 0: all);
+ *   top_p  keeps of those each token whose weight before it is below p times
+ *          their sum, and always the first (p <= 0 or NaN: only the first);
+ *   min_p  keeps of those each token with w_i >= min(1, min_p) (<= 0 or NaN: all).
+ * The token is the first index whose running sum of kept weights, in index order,
+ * exceeds u times their sum Z.  Weights and sums are in 64 bits (weights to a
+ * relative 2^-50; below exp(-745) they are 0).
+ *   logits       rows x vocab elements of type t; row r starts at element
+ *                r * row_stride.  Any alignment to the element.
+ *   rows, vocab  0 <= rows, vocab < 2^31; row_stride >= vocab when rows > 1, or 0
+ *                (every row the same).
+ *   uniforms     rows float32 in [0, 1).  1 and above take the last kept token,
+ *                negative ones and NaN count as 0.
+ *   temperature  rows float32.  T <= 0 or NaN: the lowest index of M, with
+ *                log-probability 0; the cuts and the random number do not matter.
+ *   top_k, top_p, min_p  rows int32 / float32 / float32 each, or NULL: no such cut.
+ *   tokens       rows int64: the index, or -1 where no token is left (every logit
+ *                -infinity or NaN, or vocab == 0).
+ *   logprobs     rows float32 or NULL: ln(w / Z) of the token after the cuts;
+ *                -infinity where no token is left.
+ *   ws           >= ls_sample_workspace_bytes(rows, vocab) bytes, 16-byte aligned,
+ *                zero-filled once by ls_workspace_init before its first use; each
+ *                call leaves it ready for the next.  It serves sample_tokens only.
+ * Outputs overlap no input and not each other (else LS_ERR_INVALID_ARG, as for
+ * NULL, misaligned buffers, sizes and types outside the above). */
+ls_status sample_tokens(const void *logits, int64_t rows, int64_t vocab, int64_t row_stride, ls_logits t,
+                        const float *uniforms, const float *temperature, const int32_t *top_k,
+                        const float *top_p, const float *min_p, int64_t *tokens, float *logprobs, void *ws,
+                        size_t ws_bytes, void *stream);
+
+/* Pages for the tokens that each request is about to add.  A request of len tokens
+ * holds the ceil(len / page_size) pages at the front of its row of the table; with
+ * new_len more it needs ceil((len + new_len) / page_size).  Requests are served in
+ * order, each its missing pages from the end of the free list (the last free page
+ * goes to the first missing column).  A request that needs more columns than the
+ * table has gets nothing and is passed over; from the first request that the free
+ * list cannot serve in full, only requests that miss no page are granted.
+ *   lens, new_lens  requests int32 each; negative ones count as 0.  A request
+ *                   whose len + new_len passes 2^31 - 1 gets nothing.
+ *   tables          requests x columns int32, row r at element r * table_stride;
+ *                   only the granted missing columns are written.
+ *   free_pages      free_capacity int32, of which the first *free_count are free
+ *                   (*free_count is taken as at least 0 and at most free_capacity).
+ *   page_size       1 .. 2^31 - 1 tokens.
+ *   count_out       device int64_t: free pages left.  Not free_count itself:
+ *                   blocks that start late still read that.
+ *   granted         requests bytes: 1 where the request has its pages, else 0.
+ * No workspace.  Errors: LS_ERR_INVALID_ARG for negative or too large sizes
+ * (requests, columns < 2^31; table_stride >= columns when requests > 1), NULL or
+ * misaligned buffers, and outputs that overlap any other buffer. */
+ls_status pages_append(const int32_t *lens, const int32_t *new_lens, int64_t requests, int32_t *tables,
+                       int64_t columns, int64_t table_stride, const int32_t *free_pages, int64_t free_capacity,
+                       const int64_t *free_count, int64_t page_size, int64_t *count_out, uint8_t *granted,
+                       void *stream);
+
+/* Where the new tokens of this step go in the cache.  Token j of the step, in order
+ * of the requests and of their positions, belongs to request r with
+ * offsets[r] <= j < offsets[r + 1], has position lens[r] + j - offsets[r] and slot
+ * table[r][position / page_size] * page_size + position % page_size, or -1 where
+ * the table has no such column or a negative page there.
+ *   n          room in the outputs; tokens past it are left out, and entries past
+ *              the last token get slot -1, position 0, request -1.
+ *   slots      n int64; positions, request_ids: n int32.
+ *   offsets    requests + 1 int64: the running sum of new_lens from 0.
+ * Other arguments and errors as for pages_append; len + new_len of each request is
+ * at most 2^31 - 1 (a token past that gets slot -1 and no defined position). */
+ls_status slot_map(const int32_t *lens, const int32_t *new_lens, int64_t requests, const int32_t *tables,
+                   int64_t columns, int64_t table_stride, int64_t page_size, int64_t n, int64_t *slots,
+                   int32_t *positions, int32_t *request_ids, int64_t *offsets, void *stream);
+
+/* The pages of finished requests go back on the free list: for each request with
+ * finished[r] != 0, in order, the first min(ceil(lens[r] / page_size), columns)
+ * entries of its table row are written behind the *free_count free pages.  Pages
+ * past free_capacity are counted and not written.
+ *   count_out  device int64_t: *free_count plus the pages of the finished
+ *              requests.  Not free_count itself.
+ * Other arguments and errors as for pages_append. */
+ls_status pages_release(const int32_t *lens, const uint8_t *finished, int64_t requests, const int32_t *tables,
+                        int64_t columns, int64_t table_stride, int32_t *free_pages, int64_t free_capacity,
+                        const int64_t *free_count, int64_t page_size, int64_t *count_out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,8 @@ __all__ = [
     "select_indices_if", "select_indices_flags",
     "segmented_scan", "ls_segmented_workspace_bytes", "scan_noalloc", "SCAN_NOALLOC_MAX_N",
     "ls_workspace_init", "ls_workspace_check", "set_checked", "workspace_error_flags",
-    "release_workspaces",
+    "release_workspaces", "sample_tokens", "ls_sample_workspace_bytes", "pages_append", "slot_map",
+    "pages_release",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +47,7 @@ OP_CODES = {"sum": 0, "max": 1, "xor": 2, "min": 3, "and": 4, "or": 5, "prod": 6
 CMP_CODES = {"lt": 0, "le": 1, "gt": 2, "ge": 3, "eq": 4, "ne": 5}
 SCHEME_CODES = {"single_pass": 0, "reduce_then_scan": 1, "scan_then_propagate": 2,
                 "deterministic": 3}
+LOGITS_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 BLOCK_SCAN_CODES = {"wave_dpp": 0, "hillis_steele": 1, "hillis_steele_double": 2, "blelloch": 3}
 _TORCH_DTYPES = {torch.int32: "int32", torch.float32: "float32"}
 if hasattr(torch, "uint32"):
@@ -130,6 +132,16 @@ def load_library():
         lib.compact_if.restype = I
         lib.batched_row_scan.argtypes = [P, P, I64, I64, I, I, I, P]
         lib.batched_row_scan.restype = I
+        lib.ls_sample_workspace_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+        lib.ls_sample_workspace_bytes.restype = I
+        lib.sample_tokens.argtypes = [P, I64, I64, I64, I, P, P, P, P, P, P, P, P, SZ, P]
+        lib.sample_tokens.restype = I
+        lib.pages_append.argtypes = [P, P, I64, P, I64, I64, P, I64, P, I64, P, P, P]
+        lib.pages_append.restype = I
+        lib.slot_map.argtypes = [P, P, I64, P, I64, I64, I64, I64, P, P, P, P, P]
+        lib.slot_map.restype = I
+        lib.pages_release.argtypes = [P, P, I64, P, I64, I64, P, I64, P, I64, P, P]
+        lib.pages_release.restype = I
         _lib = lib
         return lib
 
@@ -602,3 +614,188 @@ def radix_sort(keys: torch.Tensor, values: torch.Tensor | None = None,
     _after_call(ws, stream, "radix_sort")
     return out_keys, (out_values if values is not None else None)
 
+
+# ------------------------------------------------------------ a decoding step
+
+def _need(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(f"libscan: {what}")
+
+
+def _vector(t, name: str, dtypes: tuple, n: int, device) -> int:
+    """Address of a contiguous vector of n elements on `device`."""
+    if t.device != device:
+        _require_gpu(t)
+        raise ValueError(f"libscan: {name} is on {t.device}, not on {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"libscan: {name} must be {' / '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"libscan: {name} must be a contiguous vector of {n} elements")
+    return t.data_ptr()
+
+
+def _matrix(t, name: str, rows, overlapping: bool) -> tuple:
+    """(rows, columns, row stride) of a matrix whose rows are contiguous.  Rows may be
+    one and the same (stride 0) only where `overlapping`."""
+    _require_gpu(t)
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"libscan: {name} must be a matrix" + ("" if rows is None else f" of {rows} rows"))
+    n, columns = t.shape
+    stride = t.stride(0)
+    if columns > 1 and n > 0 and t.stride(1) != 1:
+        raise ValueError(f"libscan: the rows of {name} must be contiguous")
+    if n > 1 and stride < columns and not (overlapping and stride == 0):
+        raise ValueError(f"libscan: the rows of {name} overlap")
+    return n, columns, stride if n > 1 else columns
+
+
+def _on(device, call, *args) -> int:
+    """call(*args, stream) on `device`'s current stream."""
+    index = device.index
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == index:
+        return call(*args, stream)
+    with torch.cuda.device(index):
+        return call(*args, stream)
+
+
+_I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
+_BYTES = (torch.bool, torch.uint8)
+
+
+def ls_sample_workspace_bytes(rows: int, vocab: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().ls_sample_workspace_bytes(rows, vocab, ctypes.byref(out)), "ls_sample_workspace_bytes")
+    return out.value
+
+
+def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature: torch.Tensor,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  logprobs: torch.Tensor | None = None):
+    """One token from each row of logits (rows x vocab; float32, float16 or bfloat16;
+    rows contiguous, at any stride), by the row's random number in [0, 1).
+
+    A token's weight is exp((x - max) / temperature).  top_k keeps the k largest logits
+    (equal ones: the lower index first; k <= 0 keeps all), top_p of those the smallest
+    number whose weights reach top_p of their sum, min_p of those the ones that have at
+    least min_p of the largest weight.  The token is the first index at which the running
+    sum of the kept weights exceeds uniform * their sum; sums are in 64 bits.
+    temperature <= 0 takes the first largest logit.  -inf and NaN are masked; a row with
+    nothing left gives token -1 and log-probability -inf.
+
+    uniforms, temperature, top_p, min_p are float32 and top_k int32 vectors of one entry
+    a row; a cut that is None is not made.  Returns (tokens int64, logprobs float32),
+    written into `out` and `logprobs` where given."""
+    lib = load_library()
+    rows, vocab, stride = _matrix(logits, "logits", None, True)
+    code = LOGITS_CODES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"libscan: unsupported dtype {logits.dtype} (float32, float16, bfloat16)")
+    device = logits.device
+    if out is None:
+        out = torch.empty(rows, dtype=torch.int64, device=device)
+    if logprobs is None:
+        logprobs = torch.empty(rows, dtype=torch.float32, device=device)
+    u = _vector(uniforms, "uniforms", _F32, rows, device)
+    t = _vector(temperature, "temperature", _F32, rows, device)
+    k = None if top_k is None else _vector(top_k, "top_k", _I32, rows, device)
+    p = None if top_p is None else _vector(top_p, "top_p", _F32, rows, device)
+    m = None if min_p is None else _vector(min_p, "min_p", _F32, rows, device)
+    o = _vector(out, "out", _I64, rows, device)
+    lp = _vector(logprobs, "logprobs", _F32, rows, device)
+    stream = torch.cuda.current_stream(device)
+    ws = workspace_for(device, stream, ls_sample_workspace_bytes(rows, vocab), "sample")
+    st = _on(device, lib.sample_tokens, logits.data_ptr(), rows, vocab, stride, code, u, t, k, p, m, o, lp,
+             ws.data_ptr(), ws.numel())
+    _check(st, "sample_tokens")
+    return out, logprobs
+
+
+def _page_size(page_size) -> int:
+    page_size = int(page_size)
+    _need(1 <= page_size < 1 << 31, "page_size must be in [1, 2^31)")
+    return page_size
+
+
+def pages_append(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tensor, free_pages: torch.Tensor,
+                 free_count: torch.Tensor, page_size: int, count_out: torch.Tensor | None = None,
+                 granted: torch.Tensor | None = None):
+    """Gives each request the pages that new_lens more tokens need, into its row of
+    `tables` (int32, requests x columns), from the end of the free list (the first
+    free_count entries of free_pages).  Requests are served in order; from the first one
+    that the free list cannot serve, only requests that need no page are granted, and a
+    request that needs more columns than the table has is passed over.
+
+    Returns (count_out, granted): free pages left (one int64) and a bool for each
+    request.  count_out may not be free_count itself."""
+    lib = load_library()
+    requests, columns, stride = _matrix(tables, "tables", None, False)
+    device = tables.device
+    if count_out is None:
+        count_out = torch.empty(1, dtype=torch.int64, device=device)
+    if granted is None:
+        granted = torch.empty(requests, dtype=torch.bool, device=device)
+    if tables.dtype != torch.int32:
+        raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
+    capacity = free_pages.numel()
+    st = _on(device, lib.pages_append, _vector(lens, "lens", _I32, requests, device),
+             _vector(new_lens, "new_lens", _I32, requests, device), requests, tables.data_ptr(), columns, stride,
+             _vector(free_pages, "free_pages", _I32, capacity, device), capacity,
+             _vector(free_count, "free_count", _I64, 1, device), _page_size(page_size),
+             _vector(count_out, "count_out", _I64, 1, device), _vector(granted, "granted", _BYTES, requests, device))
+    _check(st, "pages_append")
+    return count_out, granted
+
+
+def slot_map(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tensor, page_size: int, capacity: int,
+             out: tuple | None = None):
+    """Where this step's new tokens go in a paged cache: for each of `capacity` entries
+    (tokens in order of request and position) its slot page * page_size + offset (int64;
+    -1 where the table holds no page), its position and its request (int32), and the
+    requests' offsets (int64, one more than requests).  Entries past the last token get
+    slot -1, position 0, request -1.
+
+    Returns (slots, positions, requests, offsets), written into the tensors of `out`
+    where given."""
+    lib = load_library()
+    requests, columns, stride = _matrix(tables, "tables", None, True)
+    device = tables.device
+    n = int(capacity)
+    _need(n >= 0, "capacity must not be negative")
+    if tables.dtype != torch.int32:
+        raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
+    if out is None:
+        out = (torch.empty(n, dtype=torch.int64, device=device), torch.empty(n, dtype=torch.int32, device=device),
+               torch.empty(n, dtype=torch.int32, device=device),
+               torch.empty(requests + 1, dtype=torch.int64, device=device))
+    slots, positions, ids, offsets = out
+    st = _on(device, lib.slot_map, _vector(lens, "lens", _I32, requests, device),
+             _vector(new_lens, "new_lens", _I32, requests, device), requests, tables.data_ptr(), columns, stride,
+             _page_size(page_size), n, _vector(slots, "slots", _I64, n, device),
+             _vector(positions, "positions", _I32, n, device), _vector(ids, "requests", _I32, n, device),
+             _vector(offsets, "offsets", _I64, requests + 1, device))
+    _check(st, "slot_map")
+    return slots, positions, ids, offsets
+
+
+def pages_release(lens: torch.Tensor, finished: torch.Tensor, tables: torch.Tensor, free_pages: torch.Tensor,
+                  free_count: torch.Tensor, page_size: int, count_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Puts the pages of the finished requests (a bool each) back on the free list, behind
+    its free_count entries, in order of request and column.  Returns count_out: the new
+    number of free pages (one int64; not free_count itself)."""
+    lib = load_library()
+    requests, columns, stride = _matrix(tables, "tables", None, True)
+    device = tables.device
+    if count_out is None:
+        count_out = torch.empty(1, dtype=torch.int64, device=device)
+    if tables.dtype != torch.int32:
+        raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
+    capacity = free_pages.numel()
+    st = _on(device, lib.pages_release, _vector(lens, "lens", _I32, requests, device),
+             _vector(finished, "finished", _BYTES, requests, device), requests, tables.data_ptr(), columns, stride,
+             _vector(free_pages, "free_pages", _I32, capacity, device), capacity,
+             _vector(free_count, "free_count", _I64, 1, device), _page_size(page_size),
+             _vector(count_out, "count_out", _I64, 1, device))
+    _check(st, "pages_release")
+    return count_out

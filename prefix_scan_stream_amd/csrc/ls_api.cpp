@@ -178,6 +178,49 @@ ls_status segmented_common(const void* in, void* out, int64_t n, ls_dtype t, ls_
                                          nseg, total, ws, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// The operators of a decoding step index rows, columns and requests in 31 bits.
+constexpr int64_t MAX_ROWS = INT32_MAX;
+bool count_ok(int64_t n) { return n >= 0 && n <= MAX_ROWS; }
+
+// A buffer of an entry point: address, bytes, required alignment, whether it is
+// written.  NULL is refused when bytes > 0.
+struct Buffer {
+    const void* p;
+    size_t bytes, align;
+    bool written;
+};
+
+// Present, aligned, and no written buffer overlapping any other.
+template <int N>
+bool buffers_ok(const Buffer (&b)[N])
+{
+    for (int i = 0; i < N; ++i) {
+        if (b[i].bytes > 0 && (b[i].p == nullptr || !aligned(b[i].p, b[i].align)))
+            return false;
+        for (int j = 0; j < i; ++j)
+            if ((b[i].written || b[j].written) && overlaps(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
+                return false;
+    }
+    return true;
+}
+
+// Bytes from the first to the last element of `rows` rows of `columns` elements.
+size_t matrix_bytes(int64_t rows, int64_t columns, int64_t stride, size_t size)
+{
+    return rows == 0 || columns == 0 ? 0 : (size_t(rows - 1) * size_t(stride) + size_t(columns)) * size;
+}
+
+// Rows of a matrix at a stride in elements that lie apart (or are all one row, where
+// `broadcast` allows it), within the address range.
+bool matrix_ok(int64_t rows, int64_t columns, int64_t stride, bool broadcast)
+{
+    if (!count_ok(rows) || !count_ok(columns) || stride < 0 || stride > LS_MAX_N)
+        return false;
+    return rows <= 1 || stride >= columns || (broadcast && stride == 0);
+}
+
+bool page_size_ok(int64_t page_size) { return page_size >= 1 && page_size <= INT32_MAX; }
+
 }  // namespace
 
 extern "C" {
@@ -402,6 +445,112 @@ ls_status segmented_scan_offsets(const void* in, void* out, int64_t n, ls_dtype 
 {
     return segmented_common(in, out, n, t, op, exclusive, nullptr, offsets, nseg, true, total, ws,
                             ws_bytes, stream);
+}
+
+ls_status ls_sample_workspace_bytes(int64_t rows, int64_t vocab, size_t* bytes)
+{
+    if (bytes == nullptr || !count_ok(rows) || !count_ok(vocab))
+        return LS_ERR_INVALID_ARG;
+    *bytes = ls::sample_workspace_bytes(rows, vocab);
+    return LS_OK;
+}
+
+ls_status sample_tokens(const void* logits, int64_t rows, int64_t vocab, int64_t row_stride, ls_logits t,
+                        const float* uniforms, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, int64_t* tokens, float* logprobs, void* ws,
+                        size_t ws_bytes, void* stream)
+{
+    if (t != LS_LOGITS_FLOAT32 && t != LS_LOGITS_FLOAT16 && t != LS_LOGITS_BFLOAT16)
+        return LS_ERR_INVALID_ARG;
+    if (!matrix_ok(rows, vocab, row_stride, true))
+        return LS_ERR_INVALID_ARG;
+    const size_t size = t == LS_LOGITS_FLOAT32 ? 4 : 2, n = size_t(rows) * 4;
+    const size_t need = ls::sample_workspace_bytes(rows, vocab);
+    const Buffer buffers[] = {
+        {logits, matrix_bytes(rows, vocab, row_stride, size), size, false},
+        {uniforms, n, 4, false},
+        {temperature, n, 4, false},
+        {top_k, top_k != nullptr ? n : 0, 4, false},
+        {top_p, top_p != nullptr ? n : 0, 4, false},
+        {min_p, min_p != nullptr ? n : 0, 4, false},
+        {tokens, 2 * n, 8, true},
+        {logprobs, logprobs != nullptr ? n : 0, 4, true},
+        {ws, ws != nullptr && ws_bytes >= need ? need : 0, 16, true},
+    };
+    if (!buffers_ok(buffers))
+        return LS_ERR_INVALID_ARG;
+    const ls_status st = check_ws(ws, ws_bytes, need);
+    if (st != LS_OK)
+        return st;
+    const ls::SampleCall call = {logits, rows, vocab, row_stride, uniforms, temperature,
+                                 top_k,  top_p, min_p, tokens,    logprobs};
+    return from_hip(ls::launch_sample(call, int(t), ws, reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status pages_append(const int32_t* lens, const int32_t* new_lens, int64_t requests, int32_t* tables,
+                       int64_t columns, int64_t table_stride, const int32_t* free_pages, int64_t free_capacity,
+                       const int64_t* free_count, int64_t page_size, int64_t* count_out, uint8_t* granted,
+                       void* stream)
+{
+    if (!matrix_ok(requests, columns, table_stride, false) || !size_ok(free_capacity) || !page_size_ok(page_size))
+        return LS_ERR_INVALID_ARG;
+    const size_t n = size_t(requests) * 4;
+    const Buffer buffers[] = {
+        {lens, n, 4, false},
+        {new_lens, n, 4, false},
+        {tables, matrix_bytes(requests, columns, table_stride, 4), 4, true},
+        {free_pages, size_t(free_capacity) * 4, 4, false},
+        {free_count, 8, 8, false},
+        {count_out, 8, 8, true},
+        {granted, size_t(requests), 1, true},
+    };
+    if (!buffers_ok(buffers))
+        return LS_ERR_INVALID_ARG;
+    return from_hip(ls::launch_pages_append(lens, new_lens, requests, tables, columns, table_stride, free_pages,
+                                            free_capacity, free_count, page_size, count_out, granted,
+                                            reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status slot_map(const int32_t* lens, const int32_t* new_lens, int64_t requests, const int32_t* tables,
+                   int64_t columns, int64_t table_stride, int64_t page_size, int64_t n, int64_t* slots,
+                   int32_t* positions, int32_t* request_ids, int64_t* offsets, void* stream)
+{
+    if (!matrix_ok(requests, columns, table_stride, true) || !size_ok(n) || !page_size_ok(page_size))
+        return LS_ERR_INVALID_ARG;
+    const Buffer buffers[] = {
+        {lens, size_t(requests) * 4, 4, false},
+        {new_lens, size_t(requests) * 4, 4, false},
+        {tables, matrix_bytes(requests, columns, table_stride, 4), 4, false},
+        {slots, size_t(n) * 8, 8, true},
+        {positions, size_t(n) * 4, 4, true},
+        {request_ids, size_t(n) * 4, 4, true},
+        {offsets, size_t(requests + 1) * 8, 8, true},
+    };
+    if (!buffers_ok(buffers))
+        return LS_ERR_INVALID_ARG;
+    return from_hip(ls::launch_slot_map(lens, new_lens, requests, tables, columns, table_stride, page_size, n, slots,
+                                        positions, request_ids, offsets, reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status pages_release(const int32_t* lens, const uint8_t* finished, int64_t requests, const int32_t* tables,
+                        int64_t columns, int64_t table_stride, int32_t* free_pages, int64_t free_capacity,
+                        const int64_t* free_count, int64_t page_size, int64_t* count_out, void* stream)
+{
+    if (!matrix_ok(requests, columns, table_stride, true) || !size_ok(free_capacity) || !page_size_ok(page_size))
+        return LS_ERR_INVALID_ARG;
+    const Buffer buffers[] = {
+        {lens, size_t(requests) * 4, 4, false},
+        {finished, size_t(requests), 1, false},
+        {tables, matrix_bytes(requests, columns, table_stride, 4), 4, false},
+        {free_pages, size_t(free_capacity) * 4, 4, true},
+        {free_count, 8, 8, false},
+        {count_out, 8, 8, true},
+    };
+    if (!buffers_ok(buffers))
+        return LS_ERR_INVALID_ARG;
+    return from_hip(ls::launch_pages_release(lens, finished, requests, tables, columns, table_stride, free_pages,
+                                             free_capacity, free_count, page_size, count_out,
+                                             reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -67,4 +67,31 @@ hipError_t launch_segmented(const void* in, void* out, int64_t n, int dtype, int
                             const uint8_t* heads, const int64_t* offsets, int64_t nseg, void* total,
                             void* ws, hipStream_t stream);
 
+// ---- the books of a paged cache (ls_pages.hip); strides in elements
+hipError_t launch_pages_append(const int32_t* lens, const int32_t* new_lens, int64_t requests, int32_t* tables,
+                               int64_t columns, int64_t stride, const int32_t* free_pages, int64_t capacity,
+                               const int64_t* free_count, int64_t page_size, int64_t* count_out, uint8_t* granted,
+                               hipStream_t stream);
+hipError_t launch_slot_map(const int32_t* lens, const int32_t* new_lens, int64_t requests, const int32_t* tables,
+                           int64_t columns, int64_t stride, int64_t page_size, int64_t n, int64_t* slots,
+                           int32_t* positions, int32_t* request_ids, int64_t* offsets, hipStream_t stream);
+hipError_t launch_pages_release(const int32_t* lens, const uint8_t* finished, int64_t requests,
+                                const int32_t* tables, int64_t columns, int64_t stride, int32_t* free_pages,
+                                int64_t capacity, const int64_t* free_count, int64_t page_size, int64_t* count_out,
+                                hipStream_t stream);
+
+// ---- token sampling (ls_sample.hip)
+enum LogitType : int { LOGITS_F32 = 0, LOGITS_F16 = 1, LOGITS_BF16 = 2 };
+struct SampleCall {
+    const void* logits;
+    int64_t rows, vocab, stride;  // stride in elements
+    const float *uniforms, *temperature;
+    const int32_t* top_k;         // the cuts: NULL = not in force
+    const float *top_p, *min_p;
+    int64_t* tokens;
+    float* logprobs;              // or NULL
+};
+size_t sample_workspace_bytes(int64_t rows, int64_t vocab);
+hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t stream);
+
 }  // namespace ls
