@@ -617,50 +617,66 @@ def radix_sort(keys: torch.Tensor, values: torch.Tensor | None = None,
 
 # ------------------------------------------------------------ a decoding step
 
-def _need(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(f"libscan: {what}")
+# A step makes these calls many times a second, each for a few microseconds of GPU work, so
+# the checks are kept to what one comparison each can tell (10 us a call with
+# torch.cuda.current_stream and a check per attribute, 6 us so); what is wrong is found out
+# after one has failed.
+
+def _vector(t, name: str, dtype, n: int, index: int) -> int:
+    """Address of a contiguous vector of n elements of `dtype` on GPU `index`."""
+    if t.dtype is dtype and t.get_device() == index and t.shape == (n,) and t.is_contiguous():
+        return t.data_ptr()
+    _require_gpu(t)
+    if t.get_device() != index:
+        raise ValueError(f"libscan: {name} is on {t.device}, not on cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"libscan: {name} must be {dtype}, not {t.dtype}")
+    raise ValueError(f"libscan: {name} must be a contiguous vector of {n} elements")
 
 
-def _vector(t, name: str, dtypes: tuple, n: int, device) -> int:
-    """Address of a contiguous vector of n elements on `device`."""
-    if t.device != device:
-        _require_gpu(t)
-        raise ValueError(f"libscan: {name} is on {t.device}, not on {device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"libscan: {name} must be {' / '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"libscan: {name} must be a contiguous vector of {n} elements")
-    return t.data_ptr()
-
-
-def _matrix(t, name: str, rows, overlapping: bool) -> tuple:
+def _matrix(t, name: str, overlapping: bool) -> tuple:
     """(rows, columns, row stride) of a matrix whose rows are contiguous.  Rows may be
     one and the same (stride 0) only where `overlapping`."""
-    _require_gpu(t)
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"libscan: {name} must be a matrix" + ("" if rows is None else f" of {rows} rows"))
-    n, columns = t.shape
-    stride = t.stride(0)
-    if columns > 1 and n > 0 and t.stride(1) != 1:
+    if not t.is_cuda:
+        _require_gpu(t)
+    if t.dim() != 2:
+        raise ValueError(f"libscan: {name} must be a matrix")
+    rows, columns = t.shape
+    if t.is_contiguous():
+        return rows, columns, columns
+    stride, step = t.stride()
+    if columns > 1 and step != 1:
         raise ValueError(f"libscan: the rows of {name} must be contiguous")
-    if n > 1 and stride < columns and not (overlapping and stride == 0):
+    if rows > 1 and stride < columns and not (overlapping and stride == 0):
         raise ValueError(f"libscan: the rows of {name} overlap")
-    return n, columns, stride if n > 1 else columns
+    return rows, columns, stride if rows > 1 else columns
 
 
-def _on(device, call, *args) -> int:
-    """call(*args, stream) on `device`'s current stream."""
-    index = device.index
-    stream = torch.cuda.current_stream(device).cuda_stream
+def _table(tables, overlapping: bool) -> tuple:
+    """(requests, columns, row stride, GPU index) of a block table."""
+    if tables.dtype is not torch.int32:
+        raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
+    return *_matrix(tables, "tables", overlapping), tables.get_device()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:  # pragma: no cover - a torch build without it
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _on(index: int, name: str, call, *args) -> None:
+    """call(*args, stream) on the current stream of GPU `index`."""
     if torch.cuda.current_device() == index:
-        return call(*args, stream)
-    with torch.cuda.device(index):
-        return call(*args, stream)
+        st = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = call(*args, _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, name)
 
 
-_I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
-_BYTES = (torch.bool, torch.uint8)
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 def ls_sample_workspace_bytes(rows: int, vocab: int) -> int:
@@ -687,34 +703,41 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature: tor
     uniforms, temperature, top_p, min_p are float32 and top_k int32 vectors of one entry
     a row; a cut that is None is not made.  Returns (tokens int64, logprobs float32),
     written into `out` and `logprobs` where given."""
-    lib = load_library()
-    rows, vocab, stride = _matrix(logits, "logits", None, True)
+    lib = _lib or load_library()
+    rows, vocab, stride = _matrix(logits, "logits", True)
     code = LOGITS_CODES.get(logits.dtype)
     if code is None:
         raise TypeError(f"libscan: unsupported dtype {logits.dtype} (float32, float16, bfloat16)")
-    device = logits.device
+    index = logits.get_device()
     if out is None:
-        out = torch.empty(rows, dtype=torch.int64, device=device)
+        out = torch.empty(rows, dtype=torch.int64, device=logits.device)
     if logprobs is None:
-        logprobs = torch.empty(rows, dtype=torch.float32, device=device)
-    u = _vector(uniforms, "uniforms", _F32, rows, device)
-    t = _vector(temperature, "temperature", _F32, rows, device)
-    k = None if top_k is None else _vector(top_k, "top_k", _I32, rows, device)
-    p = None if top_p is None else _vector(top_p, "top_p", _F32, rows, device)
-    m = None if min_p is None else _vector(min_p, "min_p", _F32, rows, device)
-    o = _vector(out, "out", _I64, rows, device)
-    lp = _vector(logprobs, "logprobs", _F32, rows, device)
-    stream = torch.cuda.current_stream(device)
-    ws = workspace_for(device, stream, ls_sample_workspace_bytes(rows, vocab), "sample")
-    st = _on(device, lib.sample_tokens, logits.data_ptr(), rows, vocab, stride, code, u, t, k, p, m, o, lp,
-             ws.data_ptr(), ws.numel())
-    _check(st, "sample_tokens")
+        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    ws = _sample_workspace(index, rows, vocab)
+    _on(index, "sample_tokens", lib.sample_tokens, logits.data_ptr(), rows, vocab, stride, code,
+        _vector(uniforms, "uniforms", _F32, rows, index), _vector(temperature, "temperature", _F32, rows, index),
+        None if top_k is None else _vector(top_k, "top_k", _I32, rows, index),
+        None if top_p is None else _vector(top_p, "top_p", _F32, rows, index),
+        None if min_p is None else _vector(min_p, "min_p", _F32, rows, index),
+        _vector(out, "out", _I64, rows, index), _vector(logprobs, "logprobs", _F32, rows, index),
+        ws.data_ptr(), ws.numel())
     return out, logprobs
+
+
+def _sample_workspace(index: int, rows: int, vocab: int) -> torch.Tensor:
+    """The current stream's cached workspace for sample_tokens."""
+    need = ls_sample_workspace_bytes(rows, vocab)
+    buf = _ws_cache.get((index, _raw_stream(index), "sample"))
+    if buf is None or buf.numel() < need:
+        device = torch.device("cuda", index)
+        buf = workspace_for(device, torch.cuda.current_stream(device), need, "sample")
+    return buf
 
 
 def _page_size(page_size) -> int:
     page_size = int(page_size)
-    _need(1 <= page_size < 1 << 31, "page_size must be in [1, 2^31)")
+    if not 1 <= page_size < 1 << 31:
+        raise ValueError("libscan: page_size must be in [1, 2^31)")
     return page_size
 
 
@@ -729,22 +752,18 @@ def pages_append(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tenso
 
     Returns (count_out, granted): free pages left (one int64) and a bool for each
     request.  count_out may not be free_count itself."""
-    lib = load_library()
-    requests, columns, stride = _matrix(tables, "tables", None, False)
-    device = tables.device
+    lib = _lib or load_library()
+    requests, columns, stride, index = _table(tables, False)
     if count_out is None:
-        count_out = torch.empty(1, dtype=torch.int64, device=device)
+        count_out = torch.empty(1, dtype=torch.int64, device=tables.device)
     if granted is None:
-        granted = torch.empty(requests, dtype=torch.bool, device=device)
-    if tables.dtype != torch.int32:
-        raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
+        granted = torch.empty(requests, dtype=torch.bool, device=tables.device)
     capacity = free_pages.numel()
-    st = _on(device, lib.pages_append, _vector(lens, "lens", _I32, requests, device),
-             _vector(new_lens, "new_lens", _I32, requests, device), requests, tables.data_ptr(), columns, stride,
-             _vector(free_pages, "free_pages", _I32, capacity, device), capacity,
-             _vector(free_count, "free_count", _I64, 1, device), _page_size(page_size),
-             _vector(count_out, "count_out", _I64, 1, device), _vector(granted, "granted", _BYTES, requests, device))
-    _check(st, "pages_append")
+    _on(index, "pages_append", lib.pages_append, _vector(lens, "lens", _I32, requests, index),
+        _vector(new_lens, "new_lens", _I32, requests, index), requests, tables.data_ptr(), columns, stride,
+        _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
+        _vector(free_count, "free_count", _I64, 1, index), _page_size(page_size),
+        _vector(count_out, "count_out", _I64, 1, index), _vector(granted, "granted", torch.bool, requests, index))
     return count_out, granted
 
 
@@ -758,24 +777,22 @@ def slot_map(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tensor, p
 
     Returns (slots, positions, requests, offsets), written into the tensors of `out`
     where given."""
-    lib = load_library()
-    requests, columns, stride = _matrix(tables, "tables", None, True)
-    device = tables.device
+    lib = _lib or load_library()
+    requests, columns, stride, index = _table(tables, True)
     n = int(capacity)
-    _need(n >= 0, "capacity must not be negative")
-    if tables.dtype != torch.int32:
-        raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
+    if n < 0:
+        raise ValueError("libscan: capacity must not be negative")
     if out is None:
+        device = tables.device
         out = (torch.empty(n, dtype=torch.int64, device=device), torch.empty(n, dtype=torch.int32, device=device),
                torch.empty(n, dtype=torch.int32, device=device),
                torch.empty(requests + 1, dtype=torch.int64, device=device))
     slots, positions, ids, offsets = out
-    st = _on(device, lib.slot_map, _vector(lens, "lens", _I32, requests, device),
-             _vector(new_lens, "new_lens", _I32, requests, device), requests, tables.data_ptr(), columns, stride,
-             _page_size(page_size), n, _vector(slots, "slots", _I64, n, device),
-             _vector(positions, "positions", _I32, n, device), _vector(ids, "requests", _I32, n, device),
-             _vector(offsets, "offsets", _I64, requests + 1, device))
-    _check(st, "slot_map")
+    _on(index, "slot_map", lib.slot_map, _vector(lens, "lens", _I32, requests, index),
+        _vector(new_lens, "new_lens", _I32, requests, index), requests, tables.data_ptr(), columns, stride,
+        _page_size(page_size), n, _vector(slots, "slots", _I64, n, index),
+        _vector(positions, "positions", _I32, n, index), _vector(ids, "requests", _I32, n, index),
+        _vector(offsets, "offsets", _I64, requests + 1, index))
     return slots, positions, ids, offsets
 
 
@@ -784,18 +801,14 @@ def pages_release(lens: torch.Tensor, finished: torch.Tensor, tables: torch.Tens
     """Puts the pages of the finished requests (a bool each) back on the free list, behind
     its free_count entries, in order of request and column.  Returns count_out: the new
     number of free pages (one int64; not free_count itself)."""
-    lib = load_library()
-    requests, columns, stride = _matrix(tables, "tables", None, True)
-    device = tables.device
+    lib = _lib or load_library()
+    requests, columns, stride, index = _table(tables, True)
     if count_out is None:
-        count_out = torch.empty(1, dtype=torch.int64, device=device)
-    if tables.dtype != torch.int32:
-        raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
+        count_out = torch.empty(1, dtype=torch.int64, device=tables.device)
     capacity = free_pages.numel()
-    st = _on(device, lib.pages_release, _vector(lens, "lens", _I32, requests, device),
-             _vector(finished, "finished", _BYTES, requests, device), requests, tables.data_ptr(), columns, stride,
-             _vector(free_pages, "free_pages", _I32, capacity, device), capacity,
-             _vector(free_count, "free_count", _I64, 1, device), _page_size(page_size),
-             _vector(count_out, "count_out", _I64, 1, device))
-    _check(st, "pages_release")
+    _on(index, "pages_release", lib.pages_release, _vector(lens, "lens", _I32, requests, index),
+        _vector(finished, "finished", torch.bool, requests, index), requests, tables.data_ptr(), columns, stride,
+        _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
+        _vector(free_count, "free_count", _I64, 1, index), _page_size(page_size),
+        _vector(count_out, "count_out", _I64, 1, index))
     return count_out
