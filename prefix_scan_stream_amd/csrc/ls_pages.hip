@@ -45,7 +45,31 @@ static PageDiv make_div(int64_t d)
     return p;
 }
 
-__device__ __forceinline__ int32_t at_least_0(int32_t v) { return v < 0 ? 0 : v; }
+// Entries r .. r+7 of a vector of lengths, negative ones and those past the end as 0.
+__device__ __forceinline__ void load_lens(const int32_t* p, int64_t r, int64_t n, uint32_t (&v)[PG_ITEMS])
+{
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+    static_assert(PG_ITEMS == 8, "two 128-bit loads");
+    if (r + PG_ITEMS <= n) {
+        const i32x4 a = *reinterpret_cast<const i32x4*>(p + r), b = *reinterpret_cast<const i32x4*>(p + r + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = uint32_t(a[k] < 0 ? 0 : a[k]);
+            v[4 + k] = uint32_t(b[k] < 0 ? 0 : b[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < PG_ITEMS; ++k) {
+            const int32_t l = r + k < n ? p[r + k] : 0;
+            v[k] = uint32_t(l < 0 ? 0 : l);
+        }
+    }
+}
+
+// Each operator below gives, for the requests r .. r+7 of a thread, what they make
+// (`c`), what their outputs need to know of them (`info`, kept in LDS) and whether they
+// can be served at all; writes output q, the i-th of request r; and writes the
+// per-request results.
 
 struct AppendOp {
     const int32_t *lens, *new_lens;
@@ -63,17 +87,24 @@ struct AppendOp {
         const int64_t c = *free_count;
         return c < 0 ? 0 : (c > capacity ? capacity : c);
     }
-    // Pages request r asks for; `fits`: its table row has the columns.
-    __device__ __forceinline__ uint32_t count(int64_t r, bool& fits) const
+    // pages asked for, pages held, and whether the table row has the columns
+    __device__ __forceinline__ void count(int64_t r, int64_t n, uint32_t (&c)[PG_ITEMS], uint32_t (&info)[PG_ITEMS],
+                                          bool (&fits)[PG_ITEMS]) const
     {
-        const uint32_t len = uint32_t(at_least_0(lens[r])), sum = len + uint32_t(at_least_0(new_lens[r]));
-        const uint32_t have = page.pages(len), want = page.pages(sum & 0x7fffffffu);
-        fits = sum <= 0x7fffffffu && int64_t(want) <= columns;
-        return fits ? want - have : 0u;
+        uint32_t len[PG_ITEMS], add[PG_ITEMS];
+        load_lens(lens, r, n, len);
+        load_lens(new_lens, r, n, add);
+#pragma unroll
+        for (int k = 0; k < PG_ITEMS; ++k) {
+            const uint32_t sum = len[k] + add[k];
+            const uint32_t have = page.pages(len[k]), want = page.pages(sum & 0x7fffffffu);
+            fits[k] = sum <= 0x7fffffffu && int64_t(want) <= columns;
+            c[k] = fits[k] ? want - have : 0u;
+            info[k] = have;
+        }
     }
-    __device__ __forceinline__ void emit(int64_t q, int64_t r, uint32_t i, int64_t lim) const
+    __device__ __forceinline__ void emit(int64_t q, int64_t r, uint32_t i, uint32_t have, int64_t lim) const
     {
-        const uint32_t have = page.pages(uint32_t(at_least_0(lens[r])));
         tables[r * stride + have + i] = free_pages[lim - 1 - q];
     }
     __device__ __forceinline__ void request(int64_t r, uint32_t c, bool fits, int64_t upto, int64_t lim) const
@@ -93,14 +124,15 @@ struct SlotsOp {
     static constexpr bool has_limit = false;
 
     __device__ __forceinline__ int64_t limit() const { return n; }
-    __device__ __forceinline__ uint32_t count(int64_t r, bool& fits) const
+    __device__ __forceinline__ void count(int64_t r, int64_t n, uint32_t (&c)[PG_ITEMS], uint32_t (&info)[PG_ITEMS],
+                                          bool (&)[PG_ITEMS]) const
     {
-        fits = true;
-        return uint32_t(at_least_0(new_lens[r]));
+        load_lens(new_lens, r, n, c);
+        load_lens(lens, r, n, info);
     }
-    __device__ __forceinline__ void emit(int64_t q, int64_t r, uint32_t i, int64_t) const
+    __device__ __forceinline__ void emit(int64_t q, int64_t r, uint32_t i, uint32_t len, int64_t) const
     {
-        const uint32_t at = uint32_t(at_least_0(lens[r])) + i;
+        const uint32_t at = len + i;
         int64_t slot = -1;
         if (at <= 0x7fffffffu) {
             const uint32_t col = page.div(at);
@@ -137,35 +169,59 @@ struct ReleaseOp {
     PageDiv page;
     static constexpr bool has_limit = false;
 
-    // Outputs past the end of the free list are counted but not written.
-    __device__ __forceinline__ int64_t limit() const { return capacity; }
-    __device__ __forceinline__ uint32_t count(int64_t r, bool& fits) const
-    {
-        fits = true;
-        if (finished[r] == 0)
-            return 0u;
-        const uint32_t held = page.pages(uint32_t(at_least_0(lens[r])));
-        return int64_t(held) < columns ? held : uint32_t(columns);
-    }
-    __device__ __forceinline__ void emit(int64_t q, int64_t r, uint32_t i, int64_t) const
-    {
-        const int64_t to = at_least_count() + q;
-        if (to < capacity)
-            free_pages[to] = tables[r * stride + i];
-    }
-    __device__ __forceinline__ int64_t at_least_count() const
+    // Where the pages go; those past the end of the free list are counted but not written.
+    __device__ __forceinline__ int64_t limit() const
     {
         const int64_t c = *free_count;
         return c < 0 ? 0 : c;
     }
+    __device__ __forceinline__ void count(int64_t r, int64_t n, uint32_t (&c)[PG_ITEMS], uint32_t (&info)[PG_ITEMS],
+                                          bool (&)[PG_ITEMS]) const
+    {
+        uint32_t len[PG_ITEMS];
+        load_lens(lens, r, n, len);
+#pragma unroll
+        for (int k = 0; k < PG_ITEMS; ++k) {
+            const uint32_t held = page.pages(len[k]);
+            c[k] = r + k >= n || finished[r + k] == 0 ? 0u : int64_t(held) < columns ? held : uint32_t(columns);
+            info[k] = 0;
+        }
+    }
+    __device__ __forceinline__ void emit(int64_t q, int64_t r, uint32_t i, uint32_t, int64_t base) const
+    {
+        if (q < capacity - base)
+            free_pages[base + q] = tables[r * stride + i];
+    }
     __device__ __forceinline__ void request(int64_t, uint32_t, bool, int64_t, int64_t) const {}
-    __device__ __forceinline__ void finish(int64_t taken, int64_t) const { *count_out = at_least_count() + taken; }
+    __device__ __forceinline__ void finish(int64_t taken, int64_t base) const { *count_out = base + taken; }
 };
+
+// LDS place of request i's prefix: one entry of padding after eight spreads a wave's
+// writes (8 entries per lane) over all banks.
+__device__ __forceinline__ int place(int i) { return i + (i >> 3); }
+
+// The last of n requests that starts at or before output `at`, by one wave: each step
+// cuts the range into 64 parts, a lane each (two steps for 4096 requests).  n >= 1.
+__device__ __forceinline__ int wave_find(const uint64_t* excl, int n, uint64_t at)
+{
+    const int lane = lane_id();
+    int lo = 0;
+    int step = PG_CHUNK / 64;
+    static_assert(PG_CHUNK == 64 * 64, "two steps");
+    for (int k = 0; k < 2; ++k) {
+        const int i = lo + lane * step;
+        const uint64_t in = __ballot(i < n && excl[place(i < n ? i : 0)] <= at);
+        lo += (63 - __builtin_clzll(in | 1u)) * step;
+        step = 1;
+    }
+    return lo;
+}
 
 template <class Op>
 __global__ __launch_bounds__(PG_BLOCK) void expand_kernel(Op op, int64_t requests)
 {
-    __shared__ uint64_t s_excl[PG_CHUNK];  // outputs of the chunk before each of its requests
+    __shared__ uint64_t s_excl[PG_CHUNK + PG_CHUNK / 8];  // outputs of the chunk before each of its requests
+    __shared__ uint32_t s_info[PG_CHUNK];
     __shared__ uint64_t s_wave[PG_WAVES];
     __shared__ int64_t s_taken;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -176,16 +232,16 @@ __global__ __launch_bounds__(PG_BLOCK) void expand_kernel(Op op, int64_t request
     int64_t chunk = 0;
 
     for (int64_t r0 = 0; r0 < requests; r0 += PG_CHUNK, ++chunk) {
-        uint32_t c[PG_ITEMS];
-        bool fits[PG_ITEMS];
+        const int n = requests - r0 < PG_CHUNK ? int(requests - r0) : PG_CHUNK;
+        const int i0 = tid * PG_ITEMS;
+        uint32_t c[PG_ITEMS] = {}, info[PG_ITEMS] = {};
+        bool fits[PG_ITEMS] = {};
+        if (i0 < n)
+            op.count(r0 + i0, requests, c, info, fits);
         uint64_t sum = 0;
 #pragma unroll
-        for (int k = 0; k < PG_ITEMS; ++k) {
-            const int64_t r = r0 + tid * PG_ITEMS + k;
-            fits[k] = false;
-            c[k] = r < requests ? op.count(r, fits[k]) : 0u;
+        for (int k = 0; k < PG_ITEMS; ++k)
             sum += c[k];
-        }
         const uint64_t incl = wave_inclusive_sum64(sum);
         if (lane == 63)
             s_wave[wave] = incl;
@@ -200,19 +256,22 @@ __global__ __launch_bounds__(PG_BLOCK) void expand_kernel(Op op, int64_t request
             total += v;
         }
         const bool mine = block == chunk % grid;  // the block that writes this chunk's per-request results
+        if (i0 < n) {
 #pragma unroll
-        for (int k = 0; k < PG_ITEMS; ++k) {
-            const int64_t r = r0 + tid * PG_ITEMS + k;
-            s_excl[tid * PG_ITEMS + k] = excl;
-            const int64_t before = base + int64_t(excl);
-            excl += c[k];
-            const int64_t upto = base + int64_t(excl);
-            if (mine && r < requests)
-                op.request(r, c[k], fits[k], upto, lim);
-            if constexpr (Op::has_limit) {
-                // the first request whose pages the list does not hold: nothing is handed out from here on
-                if (before <= lim && upto > lim)
-                    s_taken = before;
+            for (int k = 0; k < PG_ITEMS; ++k) {
+                const int64_t r = r0 + i0 + k;
+                s_excl[place(i0 + k)] = excl;
+                s_info[i0 + k] = info[k];
+                const int64_t before = base + int64_t(excl);
+                excl += c[k];
+                const int64_t upto = base + int64_t(excl);
+                if (mine && r < requests)
+                    op.request(r, c[k], fits[k], upto, lim);
+                if constexpr (Op::has_limit) {
+                    // the first request whose pages the list does not hold: nothing is handed out from here on
+                    if (before <= lim && upto > lim)
+                        s_taken = before;
+                }
             }
         }
         __syncthreads();
@@ -222,32 +281,43 @@ __global__ __launch_bounds__(PG_BLOCK) void expand_kernel(Op op, int64_t request
                 taken = s_taken;
             if (taken >= 0 && end > taken)
                 end = taken;
-        } else {
-            if (end > lim)
-                end = lim;
+        } else if constexpr (__is_same(Op, SlotsOp)) {
+            if (end > op.n)
+                end = op.n;
         }
-        // turns of PG_TILE outputs, dealt to the blocks in turn, from another block in each chunk
-        for (int64_t q0 = base + (block - chunk % grid + grid) % grid * PG_TILE; q0 < end; q0 += grid * PG_TILE) {
+        // turns of PG_TILE outputs, dealt to the blocks in turn, from another block in each chunk; a wave's share
+        // of a turn is consecutive, and the requests it spans are found once
+        for (int64_t q0 = base + (block - chunk % grid + grid) % grid * PG_TILE + wave * (64 * PG_OUT); q0 < end;
+             q0 += grid * PG_TILE) {
+            const int64_t q1 = q0 + 64 * PG_OUT < end ? q0 + 64 * PG_OUT : end;
+            const int first = wave_find(s_excl, n, uint64_t(q0 - base));
+            const int last = wave_find(s_excl, n, uint64_t(q1 - 1 - base));
+            int lo[PG_OUT], hi[PG_OUT];
 #pragma unroll
             for (int k = 0; k < PG_OUT; ++k) {
-                const int64_t q = q0 + k * PG_BLOCK + tid;
-                if (q < end) {
-                    const uint64_t at = uint64_t(q - base);
-                    // the last request that starts at or before the output (empty ones share their start with the next)
-                    int lo = 0, hi = PG_CHUNK;
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) >> 1;
-                        if (s_excl[mid] <= at)
-                            lo = mid;
-                        else
-                            hi = mid;
-                    }
-                    op.emit(q, r0 + lo, uint32_t(at - s_excl[lo]), lim);
+                lo[k] = first;
+                hi[k] = last + 1;
+            }
+            // the last request that starts at or before the output (empty ones share their start with the next)
+            for (int span = last - first; span > 0; span >>= 1) {
+#pragma unroll
+                for (int k = 0; k < PG_OUT; ++k) {
+                    const uint64_t at = uint64_t(q0 + k * 64 + lane - base);
+                    const int mid = (lo[k] + hi[k]) >> 1;
+                    const bool right = s_excl[place(mid)] <= at;
+                    lo[k] = right ? mid : lo[k];
+                    hi[k] = right ? hi[k] : mid;
                 }
+            }
+#pragma unroll
+            for (int k = 0; k < PG_OUT; ++k) {
+                const int64_t q = q0 + k * 64 + lane;
+                if (q < q1)
+                    op.emit(q, r0 + lo[k], uint32_t(uint64_t(q - base) - s_excl[place(lo[k])]), s_info[lo[k]], lim);
             }
         }
         base += int64_t(total);
-        __syncthreads();  // s_excl, s_wave and s_taken are rewritten by the next chunk
+        __syncthreads();  // s_excl, s_info, s_wave and s_taken are rewritten by the next chunk
     }
     if constexpr (__is_same(Op, SlotsOp)) {
         for (int64_t q = base + block * PG_BLOCK + tid; q < op.n; q += grid * PG_BLOCK)
