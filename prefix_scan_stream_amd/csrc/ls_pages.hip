@@ -6,7 +6,7 @@
 // contains it.  One launch does the prefix sum and the outputs: every block scans the
 // requests' counts itself, PG_CHUNK requests at a time (32 KiB of lengths for 4096
 // requests, from L2), keeps the chunk's prefix sums in LDS, and writes its share of the
-// chunk's outputs, PG_TILE consecutive ones per turn.  Nothing is handed from block to
+// chunk's outputs, consecutive ones per turn.  Nothing is handed from block to
 // block, so there is no workspace, no wait and no second launch; the price is that each
 // block reads all counts, a few percent of the outputs' bytes at the sizes of a step.
 // Bound by the bytes of the outputs when there are many (prompts, an emptied cache), by
@@ -16,13 +16,16 @@
 
 namespace ls {
 
+// Measured for the outputs of 4096 prompts (2.9 M pages) / 2.9 M slots / 4.1 M released
+// pages: 512 blocks of 512 threads 11.1 / 12.2 / 13.5 us; 256 blocks 12.4 / 14.8 / 18.8 (too
+// few waves), 768 blocks 13.2 / 14.0 / 12.4 and 1024 13.7 / 13.2 / 15.9 (the LDS holds three
+// blocks a CU, so the last ones start late); 256 blocks of 1024 threads 10.0 / 13.1 / 13.1.
 constexpr int PG_BLOCK = 512;
 constexpr int PG_WAVES = PG_BLOCK / 64;
-constexpr int PG_ITEMS = 8;                     // requests per thread
-constexpr int PG_CHUNK = PG_BLOCK * PG_ITEMS;   // requests per scan
-constexpr int PG_OUT = 4;                       // outputs per thread and turn
-constexpr int PG_TILE = PG_BLOCK * PG_OUT;
-constexpr int PG_MAX_GRID = 1024;               // four blocks per CU
+constexpr int PG_CHUNK = 4096;                  // requests per scan
+constexpr int PG_ITEMS = PG_CHUNK / PG_BLOCK;   // requests per thread
+constexpr int PG_OUT = 4;                       // outputs per thread and turn, when there are many
+constexpr int PG_MAX_GRID = 512;
 
 // Division of 0 <= n < 2^31 by d >= 1: q = n * m >> (31 + s), s = ceil(log2 d),
 // m = ceil(2^(31+s) / d) < 2^32.  m d exceeds 2^(31+s) by less than 2^s, so the error
@@ -49,13 +52,14 @@ static PageDiv make_div(int64_t d)
 __device__ __forceinline__ void load_lens(const int32_t* p, int64_t r, int64_t n, uint32_t (&v)[PG_ITEMS])
 {
     typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
-    static_assert(PG_ITEMS == 8, "two 128-bit loads");
+    static_assert(PG_ITEMS % 4 == 0, "128-bit loads");
     if (r + PG_ITEMS <= n) {
-        const i32x4 a = *reinterpret_cast<const i32x4*>(p + r), b = *reinterpret_cast<const i32x4*>(p + r + 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = uint32_t(a[k] < 0 ? 0 : a[k]);
-            v[4 + k] = uint32_t(b[k] < 0 ? 0 : b[k]);
+        for (int j = 0; j < PG_ITEMS; j += 4) {
+            const i32x4 a = *reinterpret_cast<const i32x4*>(p + r + j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[j + k] = uint32_t(a[k] < 0 ? 0 : a[k]);
         }
     } else {
 #pragma unroll
@@ -217,6 +221,44 @@ __device__ __forceinline__ int wave_find(const uint64_t* excl, int n, uint64_t a
     return lo;
 }
 
+// Outputs [base, end) of the chunk's n requests from r0, U consecutive ones per lane and
+// turn; this block's first turn is `first_turn`.  A wave's share of a turn is
+// consecutive, and the requests it spans are found once.
+template <int U, class Op>
+__device__ __forceinline__ void write_outputs(const Op& op, const uint64_t* excl, const uint32_t* info, int n,
+                                              int64_t r0, int64_t base, int64_t end, int64_t first_turn,
+                                              int64_t turns, int64_t lim)
+{
+    const int lane = lane_id(), wave = threadIdx.x >> 6;
+    for (int64_t q0 = base + (first_turn * PG_WAVES + wave) * (64 * U); q0 < end; q0 += turns * (PG_BLOCK * U)) {
+        const int64_t q1 = q0 + 64 * U < end ? q0 + 64 * U : end;
+        const int first = wave_find(excl, n, uint64_t(q0 - base));
+        const int last = wave_find(excl, n, uint64_t(q1 - 1 - base));
+        int lo[U], hi[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            lo[k] = first;
+            hi[k] = last + 1;
+        }
+        // the last request that starts at or before the output (empty ones share their start with the next)
+        for (int span = last - first; span > 0; span >>= 1) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int mid = (lo[k] + hi[k]) >> 1;
+                const bool right = excl[place(mid)] <= uint64_t(q0 + k * 64 + lane - base);
+                lo[k] = right ? mid : lo[k];
+                hi[k] = right ? hi[k] : mid;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t q = q0 + k * 64 + lane;
+            if (q < q1)
+                op.emit(q, r0 + lo[k], uint32_t(uint64_t(q - base) - excl[place(lo[k])]), info[lo[k]], lim);
+        }
+    }
+}
+
 template <class Op>
 __global__ __launch_bounds__(PG_BLOCK) void expand_kernel(Op op, int64_t requests)
 {
@@ -285,37 +327,13 @@ __global__ __launch_bounds__(PG_BLOCK) void expand_kernel(Op op, int64_t request
             if (end > op.n)
                 end = op.n;
         }
-        // turns of PG_TILE outputs, dealt to the blocks in turn, from another block in each chunk; a wave's share
-        // of a turn is consecutive, and the requests it spans are found once
-        for (int64_t q0 = base + (block - chunk % grid + grid) % grid * PG_TILE + wave * (64 * PG_OUT); q0 < end;
-             q0 += grid * PG_TILE) {
-            const int64_t q1 = q0 + 64 * PG_OUT < end ? q0 + 64 * PG_OUT : end;
-            const int first = wave_find(s_excl, n, uint64_t(q0 - base));
-            const int last = wave_find(s_excl, n, uint64_t(q1 - 1 - base));
-            int lo[PG_OUT], hi[PG_OUT];
-#pragma unroll
-            for (int k = 0; k < PG_OUT; ++k) {
-                lo[k] = first;
-                hi[k] = last + 1;
-            }
-            // the last request that starts at or before the output (empty ones share their start with the next)
-            for (int span = last - first; span > 0; span >>= 1) {
-#pragma unroll
-                for (int k = 0; k < PG_OUT; ++k) {
-                    const uint64_t at = uint64_t(q0 + k * 64 + lane - base);
-                    const int mid = (lo[k] + hi[k]) >> 1;
-                    const bool right = s_excl[place(mid)] <= at;
-                    lo[k] = right ? mid : lo[k];
-                    hi[k] = right ? hi[k] : mid;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < PG_OUT; ++k) {
-                const int64_t q = q0 + k * 64 + lane;
-                if (q < q1)
-                    op.emit(q, r0 + lo[k], uint32_t(uint64_t(q - base) - s_excl[place(lo[k])]), s_info[lo[k]], lim);
-            }
-        }
+        // Turns of outputs are dealt to the blocks in turn, from another block in each chunk.  One output per
+        // thread when that covers them (a shorter chain: 3.6 us against 4.8 for 256 tokens), else PG_OUT.
+        const int64_t at = (block - chunk % grid + grid) % grid;
+        if (end - base <= grid * PG_BLOCK)
+            write_outputs<1>(op, s_excl, s_info, n, r0, base, end, at, grid, lim);
+        else
+            write_outputs<PG_OUT>(op, s_excl, s_info, n, r0, base, end, at, grid, lim);
         base += int64_t(total);
         __syncthreads();  // s_excl, s_info, s_wave and s_taken are rewritten by the next chunk
     }
@@ -333,7 +351,7 @@ __global__ __launch_bounds__(PG_BLOCK) void expand_kernel(Op op, int64_t request
 // Blocks for up to `outputs` outputs.
 static unsigned expand_grid(int64_t outputs)
 {
-    const int64_t tiles = (outputs + PG_TILE - 1) / PG_TILE;
+    const int64_t tiles = (outputs + PG_BLOCK - 1) / PG_BLOCK;
     return unsigned(tiles < 1 ? 1 : tiles > PG_MAX_GRID ? PG_MAX_GRID : tiles);
 }
 
