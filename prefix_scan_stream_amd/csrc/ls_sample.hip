@@ -16,36 +16,46 @@
 // 64 bits: a double multiply-add issues at the rate of a single one on this GPU, and 2^f
 // is a polynomial of degree 10.
 //
-// The cuts are found by value, without sorting the row: a histogram of weights and
-// counts over 2048 bins of log2 w (32 to the octave) tells which bin the cut lies in, and
-// only that bin's elements are collected in LDS and sorted.  Weights are added to bins as
-// integers of 2^-frac of the bin's octave, so that the sums do not depend on the order
-// of the atomics.  A bin of more elements than the list holds is cut into 2048 ranges
-// of its keys, and so on, until the list holds them or they are all equal.
+// One launch.  A row is cut into segments, and its segments are shared out to blocks, so
+// that few rows still use the whole GPU.  Every block leaves what its segments hold in
+// the workspace; the block of a row that arrives last at the row's counter goes on alone.
+//   No cuts: the segments hold their largest value and the sum of their weights (relative
+//   to it).  The last block has the running sums of the segments, so it knows the one
+//   the token lies in, and reads only that again.
+//   Cuts: the segments hold their largest value.  The k-th largest of these values is at
+//   most the k-th largest logit, so for a small k the candidates are the elements at or
+//   above it, which lie in about k segments: these are read again and a few more than k
+//   elements sorted in LDS.  min-p alone has its threshold from M the same way.
+//   Otherwise the cut is found by value without sorting the row (cut_row below).
+#include <type_traits>
+
 #include "ls_device.hpp"
 #include "ls_internal.hpp"
 
 namespace ls {
 
-constexpr int SM_BLOCK = 1024;
+constexpr int SM_BLOCK = 1024;              // threads of a block that makes cuts
 constexpr int SM_WAVES = SM_BLOCK / 64;
+constexpr int SM_ALL_BLOCK = 256;           // without cuts
 constexpr int SM_VEC = 8;                   // consecutive logits per lane and step
 constexpr int SM_STEP = 64 * SM_VEC;        // consecutive logits per wave and step
-constexpr int SM_SEGS = 1024;               // most segments of a row
-constexpr int SM_BINS = 2048;
-constexpr int SM_PER_OCTAVE = 32;
-constexpr int SM_OCTAVES = SM_BINS / SM_PER_OCTAVE;
-constexpr int SM_LIST = 4096;               // elements of one bin that are sorted in LDS
-static_assert(SM_SEGS == SM_BLOCK && SM_BINS == 2 * SM_BLOCK, "one segment and two bins per thread");
+constexpr int SM_PER_LANE = 8;
+constexpr int SM_SEGS = 64 * SM_PER_LANE;   // most segments of a row
+constexpr int SM_PER_OCTAVE = 8;            // bins per halving of the weight
+constexpr int SM_BINS = 256;
+constexpr int SM_RANGES = 256;              // ranges of a refinement
+constexpr int SM_LIST = 4096;               // elements of one bin kept in LDS
+constexpr int SM_SMALL = 512;               // elements that are ordered by counting
+constexpr int SM_ROWS = 16384;              // most rows of a launch (at most 128 blocks each)
+static_assert(SM_BINS == SM_RANGES, "one search for both");
 
-// 2^y for y <= 0 (NaN counts as -inf): 2^n p(f), n the nearest integer, |f| <= 1/2.
-// p interpolates 2^f at Chebyshev nodes (p(0) = 1); its largest relative error is
-// 2^-50.6.  Results below 2^-1074 are 0.
-__device__ __forceinline__ double exp2_neg(double y)
+constexpr double LOG2E = 0x1.71547652b82fep+0, LN2 = 0x1.62e42fefa39efp-1;
+constexpr double TO_INT = 0x1.8p52;  // adding it rounds to the nearest integer, into the low word
+
+// 2^f for |f| <= 1/2: interpolates at Chebyshev nodes with p(0) = 1; its largest
+// relative error is 2^-50.6.
+__device__ __forceinline__ double exp2_poly(double f)
 {
-    y = __builtin_fmax(y, -1100.0);
-    const double n = __builtin_rint(y);
-    const double f = y - n;
     double p = 0x1.e5e9f548e5725p-28;
     p = __builtin_fma(p, f, 0x1.b6571de2f2351p-24);
     p = __builtin_fma(p, f, 0x1.62bfe46117445p-20);
@@ -56,8 +66,38 @@ __device__ __forceinline__ double exp2_neg(double y)
     p = __builtin_fma(p, f, 0x1.c6b08d7044119p-5);
     p = __builtin_fma(p, f, 0x1.ebfbdff82c590p-3);
     p = __builtin_fma(p, f, 0x1.62e42fefa39f7p-1);
-    p = __builtin_fma(p, f, 1.0);
-    return __builtin_ldexp(p, int(n));
+    return __builtin_fma(p, f, 1.0);
+}
+
+// 2^(d c + e) for -1000 <= d c <= 1 and a small e, with the exponent added in the high word.
+__device__ __forceinline__ double exp2_fast(double d, double c, int e = 0)
+{
+    const double t = __builtin_fma(d, c, TO_INT);
+    const uint64_t b = __builtin_bit_cast(uint64_t, exp2_poly(__builtin_fma(d, c, TO_INT - t)));
+    const uint32_t n = uint32_t(__builtin_bit_cast(uint64_t, t)) + uint32_t(e);
+    return __builtin_bit_cast(double, (uint64_t(uint32_t(b >> 32) + (n << 20)) << 32) | uint32_t(b));
+}
+
+// 2^y for y <= 0 (NaN counts as -inf), 0 below 2^-1074.
+__device__ __forceinline__ double exp2_exact(double y)
+{
+    y = __builtin_fmax(y, -1100.0);
+    const double n = __builtin_rint(y);
+    return __builtin_ldexp(exp2_poly(y - n), int(n));
+}
+
+// A value that is the same in all lanes, as a scalar.
+template <class T>
+__device__ __forceinline__ T uniform(T v)
+{
+    if constexpr (sizeof(T) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(b));
+        const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(b >> 32));
+        return __builtin_bit_cast(T, (uint64_t(hi) << 32) | lo);
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+    }
 }
 
 // Order-preserving keys of the logits: larger value, larger key; -0 and 0 are one.
@@ -70,527 +110,1172 @@ __device__ __forceinline__ float value_of(uint32_t key)
 {
     return from_bits<float>((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
+constexpr uint32_t KEY_NEG_INF = 0x007fffffu;
 
-template <int TYPE>
-__device__ __forceinline__ float widen(uint32_t half)
-{
-    if constexpr (TYPE == LOGITS_BF16)
-        return from_bits<float>(half << 16);
-    else
-        return float(__builtin_bit_cast(_Float16, uint16_t(half)));
-}
+// ---------------------------------------------------------------- a row's logits
+typedef uint32_t u32x4_by4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_by2 __attribute__((ext_vector_type(4), aligned(2)));
 
-// Logits idx .. idx+7 of a row, NaN and what lies past the end as -inf.  Rows start at any
-// multiple of the element's size.
+// Eight consecutive logits as loaded; what lies past the row's end is -inf.
 template <int TYPE>
-__device__ __forceinline__ void load_logits(const void* row, int64_t idx, int64_t vocab, float (&x)[SM_VEC])
-{
-    constexpr float NEG = -__builtin_inff();
-    if constexpr (TYPE == LOGITS_F32) {
-        typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
-        const float* p = static_cast<const float*>(row) + idx;
-        if (idx + SM_VEC <= vocab) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+struct Raw {
+    static constexpr int WORDS = TYPE == LOGITS_F32 ? 8 : 4;
+    static constexpr uint32_t NEG = TYPE == LOGITS_F32 ? 0xff800000u : TYPE == LOGITS_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    uint32_t w[WORDS];
+
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[k] = a[k];
-                x[4 + k] = b[k];
+        for (int k = 0; k < WORDS; ++k)
+            w[k] = NEG;
+    }
+    // Logits idx .. idx+7; rows start at any multiple of the element's size.
+    __device__ __forceinline__ void load(const void* row, int64_t idx, int64_t vocab)
+    {
+        using E = typename std::conditional<TYPE == LOGITS_F32, uint32_t, uint16_t>::type;
+        using V = typename std::conditional<TYPE == LOGITS_F32, u32x4_by4, u32x4_by2>::type;
+        const E* p = static_cast<const E*>(row) + idx;
+        if (idx + SM_VEC <= vocab) {
+#pragma unroll
+            for (int k = 0; k < WORDS; k += 4) {
+                const V a = *reinterpret_cast<const V*>(reinterpret_cast<const uint32_t*>(p) + k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[k + j] = a[j];
             }
         } else {
+            clear();
 #pragma unroll
-            for (int k = 0; k < SM_VEC; ++k)
-                x[k] = idx + k < vocab ? p[k] : NEG;
-        }
-    } else {
-        typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(2)));
-        const uint16_t* p = static_cast<const uint16_t*>(row) + idx;
-        if (idx + SM_VEC <= vocab) {
-            const u32x4a a = *reinterpret_cast<const u32x4a*>(p);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[2 * k] = widen<TYPE>(a[k] & 0xffffu);
-                x[2 * k + 1] = widen<TYPE>(a[k] >> 16);
+            for (int k = 0; k < SM_VEC; ++k) {
+                if (idx + k < vocab) {
+                    if constexpr (TYPE == LOGITS_F32)
+                        w[k] = p[k];
+                    else
+                        w[k / 2] = k % 2 ? (w[k / 2] & 0xffffu) | (uint32_t(p[k]) << 16)
+                                         : (w[k / 2] & 0xffff0000u) | p[k];
+                }
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < SM_VEC; ++k)
-                x[k] = idx + k < vocab ? widen<TYPE>(p[k]) : NEG;
         }
     }
-#pragma unroll
-    for (int k = 0; k < SM_VEC; ++k)
-        x[k] = x[k] == x[k] ? x[k] : NEG;
+    __device__ __forceinline__ float at(int k) const
+    {
+        if constexpr (TYPE == LOGITS_F32)
+            return from_bits<float>(w[k]);
+        else if constexpr (TYPE == LOGITS_BF16)
+            return from_bits<float>(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+        else
+            return float(__builtin_bit_cast(_Float16, uint16_t(k % 2 ? w[k / 2] >> 16 : w[k / 2])));
+    }
+};
+
+// NaN as -inf; where the row's largest value is +inf (`inf`), its elements are +inf or
+// not: 0 or -inf.
+__device__ __forceinline__ float clean(float x, bool inf)
+{
+    constexpr float INF = __builtin_inff();
+    x = x == x ? x : -INF;
+    if (inf)
+        x = x == INF ? 0.0f : -INF;
+    return x;
 }
 
 // One past the last kept element in the order: kept are keys above `key`, and equal
 // ones up to `index`.
 struct Cut {
-    uint32_t key;
-    uint32_t index;
+    uint32_t key, index;
     __device__ __forceinline__ bool keeps(uint32_t k, uint32_t i) const { return k > key || (k == key && i <= index); }
 };
 
-struct SampleLds {
-    uint64_t mass[SM_BINS];
-    uint32_t count[SM_BINS];
-    uint64_t list[SM_LIST];     // ~key << 32 | index: ascending is the order
-    double seg[SM_SEGS];
-    double wave_f64[SM_WAVES];
-    uint32_t wave_u32[SM_WAVES];
-    uint32_t n_list, bin, tie_index, best;
-    double above, total;
-    uint32_t above_count, key_lo, key_hi;
-};
+// An infinite temperature makes all weights 1: so does this one, without 0 times infinity.
+__device__ __forceinline__ double finite_temperature(float t) { return __builtin_fmin(double(t), 1e300); }
 
-// What a block knows of its row.
 template <int TYPE>
 struct Row {
     const void* p;
     int64_t vocab;
-    int seg_steps;   // steps per segment
-    int segs;
-    float top;
-    double c;        // log2 e / t
+    int steps;       // of SM_STEP logits
+    int index_bits;  // vocab <= 2^index_bits
+    bool inf;        // see clean()
+    float top;       // largest logit (after clean)
+    double top64, c; // log2 w = (x - top) c, c = log2 e / t
+    double far;      // -1000 / c: weights further down count as 2^-1000, next to nothing
     int frac;        // bits below the octave's unit in the bins' integers
 
-    // log2 of the weight, at most 0; the same in every pass, and monotone in x
-    __device__ __forceinline__ double log2w(float x) const
+    __device__ __forceinline__ void set_top(float t)
     {
-        return x == top ? 0.0 : (double(x) - double(top)) * c;
+        inf = t == __builtin_inff();
+        top = inf ? 0.0f : t;
+        top64 = uniform(double(top));
     }
-    __device__ __forceinline__ double weight(float x) const { return exp2_neg(log2w(x)); }
-    __device__ __forceinline__ int bin(double y) const
+    __device__ __forceinline__ void set_temperature(float t)
     {
-        const float s = float(__builtin_fmin(-y, double(SM_OCTAVES)));
-        const int b = int(s * float(SM_PER_OCTAVE));
-        return b < SM_BINS ? b : SM_BINS - 1;
+        const double d = finite_temperature(t);
+        c = uniform(LOG2E / d);
+        far = uniform(-1000.0 * d / LOG2E);
     }
-    __device__ __forceinline__ uint64_t fixed(double w, int b) const
+    // log2 of the weight: 0 for the largest, at most 0, monotone in x.  The subtraction comes first: folded into
+    // one multiply-add it would leave the rounding of top c, 2e-12 for a logit of 400 at a temperature of 0.01,
+    // in every weight.
+    __device__ __forceinline__ double log2w(float x) const { return (double(x) - top64) * c; }
+    __device__ __forceinline__ double weight(float x) const { return exp2_exact(log2w(x)); }
+    // x - top in the range of exp2_fast; NaN counts as masked
+    __device__ __forceinline__ double below(float x) const { return __builtin_fmax(double(x) - top64, far); }
+    // bin: the nearest eighth of an octave below the largest weight
+    __device__ __forceinline__ uint32_t bin(double d) const
     {
-        return uint64_t(__builtin_ldexp(w, b / SM_PER_OCTAVE + frac) + 0.5);
+        const uint32_t b = uint32_t(__builtin_bit_cast(uint64_t, __builtin_fma(d, c * -double(SM_PER_OCTAVE), TO_INT)));
+        return b < SM_BINS - 1 ? b : SM_BINS - 1;
     }
-    __device__ __forceinline__ double unfixed(uint64_t m, int b) const
+    // a weight in bin b as an integer of 2^-frac of the bin's octave; below 2^(frac + 1/16)
+    __device__ __forceinline__ uint64_t fixed(double d, uint32_t b) const
     {
-        return __builtin_ldexp(double(m), -(b / SM_PER_OCTAVE + frac));
+        const double w = exp2_fast(d, c, int(b / SM_PER_OCTAVE) + frac) + 0x1p52;
+        return __builtin_bit_cast(uint64_t, w) & ((uint64_t(1) << 52) - 1);
     }
-
-    // f(x[8], index of x[0]) over the whole row: a wave takes every SM_WAVES-th segment
-    template <class F>
-    __device__ __forceinline__ void for_each(F f) const
+    __device__ __forceinline__ double unfixed(uint64_t m, uint32_t b) const
     {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        for (int s = wave; s < segs; s += SM_WAVES) {
-            for (int j = 0; j < seg_steps; ++j) {
-                const int64_t idx = (int64_t(s) * seg_steps + j) * SM_STEP + lane * SM_VEC;
-                if (idx >= vocab)
-                    break;
-                float x[SM_VEC];
-                load_logits<TYPE>(p, idx, vocab, x);
-                f(x, idx);
+        return __builtin_ldexp(double(m), -(int(b / SM_PER_OCTAVE) + frac));
+    }
+    // f(x[8], index of x[0]) over steps first, first + stride, ... below end, by one wave; the next U loads are
+    // in flight while f works on these.
+    template <int U, class F>
+    __device__ __forceinline__ void for_steps(int first, int end, int stride, F f) const
+    {
+        const int lane = lane_id();
+        Raw<TYPE> raw[U], next[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (first + u * stride < end)
+                raw[u].load(p, int64_t(first + u * stride) * SM_STEP + lane * SM_VEC, vocab);
+        for (int s = first; s < end; s += U * stride) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = s + (U + u) * stride;
+                if (at < end)
+                    next[u].load(p, int64_t(at) * SM_STEP + lane * SM_VEC, vocab);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = s + u * stride;
+                if (at < end) {
+                    float x[SM_VEC];
+#pragma unroll
+                    for (int k = 0; k < SM_VEC; ++k)
+                        x[k] = clean(raw[u].at(k), inf);
+                    f(x, uint32_t(at) * SM_STEP + uint32_t(lane * SM_VEC));
+                }
+                __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                raw[u] = next[u];
         }
     }
 };
 
-__device__ __forceinline__ float wave_max(float v)
-{
-    for (int d = 32; d > 0; d >>= 1)
-        v = __builtin_fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
+// ---------------------------------------------------------------- running sums
+// The place of u in a sum: u <= 0 and NaN count as 0.
+__device__ __forceinline__ double goal_of(double u, double total) { return u > 0.0 ? u * total : 0.0; }
 
-// Running sums over the block's threads, in thread order; `total` to all.
-__device__ __forceinline__ double block_inclusive_sum(double v, SampleLds& lds, double& total)
+// Sums of N values per lane: `incl` with the lanes before, `total` of all.
+template <int N>
+__device__ __forceinline__ void wave_sums(const double (&v)[N], double& incl, double& total)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double incl = wave_inclusive_sum64(v);
-    __syncthreads();
-    if (lane == 63)
-        lds.wave_f64[wave] = incl;
-    __syncthreads();
-    double before = 0.0;
-    total = 0.0;
-    for (int w = 0; w < SM_WAVES; ++w) {
-        before = w == wave ? total : before;
-        total += lds.wave_f64[w];
-    }
-    return before + incl;
-}
-__device__ __forceinline__ uint32_t block_inclusive_sum(uint32_t v, SampleLds& lds, uint32_t& total)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t incl = wave_inclusive_scan<SumU32>(v);
-    __syncthreads();
-    if (lane == 63)
-        lds.wave_u32[wave] = incl;
-    __syncthreads();
-    uint32_t before = 0;
-    total = 0;
-    for (int w = 0; w < SM_WAVES; ++w) {
-        before = w == wave ? total : before;
-        total += lds.wave_u32[w];
-    }
-    return before + incl;
-}
-
-// The first index, in index order, at which the running sum of f(x, index) exceeds
-// goal(total); the last one of nonzero weight if none does.  total and that index to all.
-template <int TYPE, class F, class G>
-__device__ int64_t find_in_order(const Row<TYPE>& row, SampleLds& lds, F f, G goal_of, double& total)
-{
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    __syncthreads();
-    for (int s = wave; s < row.segs; s += SM_WAVES) {
-        double sum = 0.0;
-        for (int j = 0; j < row.seg_steps; ++j) {
-            const int64_t idx = (int64_t(s) * row.seg_steps + j) * SM_STEP + lane * SM_VEC;
-            if (idx < row.vocab) {
-                float x[SM_VEC];
-                load_logits<TYPE>(row.p, idx, row.vocab, x);
+    double sum = 0.0;
 #pragma unroll
-                for (int k = 0; k < SM_VEC; ++k)
-                    sum += f(x[k], uint32_t(idx + k));
+    for (int k = 0; k < N; ++k)
+        sum += v[k];
+    incl = wave_inclusive_sum64(sum);
+    total = read_lane64(incl, 63);
+}
+
+// One wave, N values per lane in order (lane 0's first): the first at which `before` plus
+// their running sum exceeds `goal` (`over`), the last positive one if none does, -1 if none
+// is positive.  `incl`: the sum with the lanes before (wave_sums).  `before` becomes the sum
+// in front of it.
+template <int N>
+__device__ __forceinline__ int wave_first_over(const double (&v)[N], double goal, double incl, double& before,
+                                               bool& over)
+{
+    double r = before + dpp_move64<DPP_WAVE_SHR1, 0xf>(incl), at_hit = 0.0, at_last = 0.0;
+    int hit = -1, last = -1;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const double up = r + v[k];
+        if (v[k] > 0.0) {
+            last = k;
+            at_last = r;
+            if (hit < 0 && up > goal) {
+                hit = k;
+                at_hit = r;
+            }
+        }
+        r = up;
+    }
+    const uint64_t hits = __ballot(hit >= 0), any = __ballot(last >= 0);
+    over = hits != 0;
+    if (any == 0)
+        return -1;
+    const int l = over ? __builtin_ctzll(hits) : 63 - __builtin_clzll(any);
+    before = read_lane64(over ? at_hit : at_last, l);
+    return l * N + read_lane(over ? hit : last, l);
+}
+
+// One wave: the first index in steps [first, end) at which `run` and the running sum of
+// f(x, index) exceed `goal`, or the last of positive weight; ~0 if there is none.
+template <int TYPE, class F>
+__device__ __forceinline__ uint32_t wave_find_token(const Row<TYPE>& row, int first, int end, double run, double goal,
+                                                    F f)
+{
+    uint32_t found = ~0u;
+    bool over = false;
+    row.template for_steps<1>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
+        if (over)
+            return;
+        double w[SM_VEC], incl, total, before = run;
+#pragma unroll
+        for (int k = 0; k < SM_VEC; ++k)
+            w[k] = f(x[k], idx + k);
+        wave_sums(w, incl, total);
+        const int at = wave_first_over(w, goal, incl, before, over);
+        if (at >= 0)
+            found = uniform(idx) + uint32_t(at);
+        run += total;
+    });
+    return found;
+}
+
+struct SharedSums {
+    double sums[SM_BLOCK];
+    uint32_t first, last, found, arrived;
+};
+
+// The block: the first index in the whole row, in index order, at which the running sum of
+// f(x, index) exceeds u times the sum of all.  To all threads, with that sum.
+template <int TYPE, class F>
+__device__ __forceinline__ uint32_t find_in_order(const Row<TYPE>& row, SharedSums& sh, double u, F f, double& total)
+{
+    constexpr int N = SM_BLOCK / 64;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (row.steps + SM_BLOCK - 1) / SM_BLOCK;  // steps per sum
+    const int sums = (row.steps + per - 1) / per;
+    __syncthreads();
+    if (tid >= sums)
+        sh.sums[tid] = 0.0;
+    for (int s = wave; s < sums; s += SM_WAVES) {
+        double sum = 0.0;
+        row.template for_steps<1>(s * per, s * per + per < row.steps ? s * per + per : row.steps, 1,
+                                  [&](const float(&x)[SM_VEC], uint32_t idx) {
+#pragma unroll
+                                      for (int k = 0; k < SM_VEC; ++k)
+                                          sum += f(x[k], idx + k);
+                                  });
+        sum = wave_inclusive_sum64(sum);
+        if (lane == 63)
+            sh.sums[s] = sum;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        double v[N], incl, before = 0.0;
+        bool over;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] = sh.sums[lane * N + k];
+        wave_sums(v, incl, total);
+        const int s = wave_first_over(v, goal_of(u, total), incl, before, over);
+        const uint32_t token = wave_find_token(row, s * per, s * per + per < row.steps ? s * per + per : row.steps,
+                                               before, goal_of(u, total), f);
+        if (lane == 0) {
+            sh.found = token;
+            sh.sums[0] = total;
+        }
+    }
+    __syncthreads();
+    total = uniform(sh.sums[0]);
+    return uniform(sh.found);
+}
+
+// ---------------------------------------------------------------- handing a row on
+// What a row's waves leave for the last of them: written and read at device scope, with
+// the stores complete before the wave (or its block) counts itself in.
+template <class T>
+__device__ __forceinline__ void put(T* p, T v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T get(const T* p)
+{
+    return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Counts the caller in; whether it is the last of `parts`, which leaves the counter at 0.
+__device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t parts)
+{
+    const bool last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u == parts;
+    if (last)
+        put(counter, 0u);
+    return last;
+}
+
+// The launch: part p of row r is block p * rows + r, so that the last blocks of the rows,
+// which go on alone, lie on all XCDs (rows' blocks next to each other had put them on two
+// of the eight: 416 us against 101 for 256 rows cut by mass).  Each wave of a block takes
+// `per_wave` segments of seg_steps steps.
+struct SampleGrid {
+    uint32_t* counters;  // one per row, 0 between calls
+    float* tops;         // rows x segs: each segment's largest value
+    double* sums;        // rows x segs: and its weights relative to that
+    int steps, seg_steps, segs, per_wave, parts;
+};
+
+template <int TYPE>
+__device__ __forceinline__ Row<TYPE> make_row(const SampleCall& call, const SampleGrid& g, int64_t r)
+{
+    Row<TYPE> row;
+    row.p = static_cast<const char*>(call.logits) + r * call.stride * (TYPE == LOGITS_F32 ? 4 : 2);
+    row.vocab = call.vocab;
+    row.steps = g.steps;
+    row.index_bits = call.vocab > 1 ? 32 - __builtin_clz(uint32_t(call.vocab - 1)) : 0;
+    row.frac = 61 - row.index_bits < 44 ? 61 - row.index_bits : 44;
+    row.inf = false;
+    return row;
+}
+
+// One wave writes the row's result.
+__device__ __forceinline__ void write_result(const SampleCall& call, int64_t r, int64_t token, double logprob)
+{
+    if (lane_id() == 0) {
+        call.tokens[r] = token;
+        if (call.logprobs != nullptr)
+            call.logprobs[r] = float(logprob);
+    }
+}
+
+template <int TYPE>
+__device__ __forceinline__ void write_token(const SampleCall& call, int64_t r, const Row<TYPE>& row, uint32_t token,
+                                            double total)
+{
+    if (lane_id() == 0) {
+        float x;
+        if constexpr (TYPE == LOGITS_F32)
+            x = static_cast<const float*>(row.p)[token];
+        else if constexpr (TYPE == LOGITS_BF16)
+            x = from_bits<float>(uint32_t(static_cast<const uint16_t*>(row.p)[token]) << 16);
+        else
+            x = float(static_cast<const _Float16*>(row.p)[token]);
+        call.tokens[r] = token;
+        if (call.logprobs != nullptr)
+            call.logprobs[r] = float(row.log2w(clean(x, row.inf)) * LN2 - ::log(total));
+    }
+}
+
+// The largest values of a row's segments, in one wave's registers in order.
+struct Tops {
+    float v[SM_PER_LANE];
+    int per_lane;
+    __device__ __forceinline__ int seg(int k) const { return lane_id() * per_lane + k; }
+    __device__ __forceinline__ float load(const SampleGrid& g, int64_t r)
+    {
+        per_lane = (g.segs + 63) / 64;
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int k = 0; k < SM_PER_LANE; ++k) {
+            v[k] = -__builtin_inff();
+            if (k < per_lane && seg(k) < g.segs)
+                v[k] = get(&g.tops[r * g.segs + seg(k)]);
+        }
+#pragma unroll
+        for (int k = 0; k < SM_PER_LANE; ++k)
+            m = v[k] > m ? v[k] : m;
+        return read_lane(wave_inclusive_scan<MaxF32>(m), 63);
+    }
+};
+
+// One wave: rows with nothing left, and the first index of the largest value where the
+// temperature asks for it.  True when the row is done.
+template <int TYPE>
+__device__ __forceinline__ bool settle(const SampleCall& call, const SampleGrid& g, int64_t r, Row<TYPE>& row,
+                                       const Tops& tops, float top, bool writes)
+{
+    row.set_top(top);
+    if (top == -__builtin_inff()) {
+        if (writes)
+            write_result(call, r, -1, -double(__builtin_inff()));
+        return true;
+    }
+    const float t = call.temperature[r];
+    if (t > 0.0f) {
+        row.set_temperature(t);
+        return false;
+    }
+    if (!writes)
+        return true;
+    uint32_t seg = ~0u;
+#pragma unroll
+    for (int k = SM_PER_LANE - 1; k >= 0; --k)
+        if (tops.v[k] == top)
+            seg = uint32_t(tops.seg(k));
+    seg = read_lane(wave_inclusive_scan<MinU32>(seg), 63);
+    const int s0 = int(seg) * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
+    uint32_t first = ~0u;
+    row.template for_steps<1>(s0, s1, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
+#pragma unroll
+        for (int k = SM_VEC - 1; k >= 0; --k)
+            if (x[k] == row.top && idx + k < first)
+                first = idx + k;
+    });
+    write_result(call, r, int64_t(read_lane(wave_inclusive_scan<MinU32>(first), 63)), 0.0);
+    return true;
+}
+
+// ---------------------------------------------------------------- no cuts
+// Waves work for themselves; the one that finishes a row last finds its token.  Bound by the
+// logits' bytes in float32 and by the multiply-adds (about 20 a logit) in 16 bits.
+template <int TYPE>
+__global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall call, SampleGrid g)
+{
+    constexpr float NEG = -__builtin_inff();
+    constexpr int U = 4;
+    constexpr int WAVES = SM_ALL_BLOCK / 64;
+    const int lane = lane_id(), wave = uniform(int(threadIdx.x >> 6));
+    const int64_t r = blockIdx.x % uint32_t(call.rows);
+    const int part = int(blockIdx.x / uint32_t(call.rows));
+    Row<TYPE> row = make_row<TYPE>(call, g, r);
+    const float t = call.temperature[r];
+    const bool sums = t > 0.0f;
+    const double c = uniform(LOG2E / finite_temperature(t)), far = uniform(-1000.0 * finite_temperature(t) / LOG2E);
+    for (int i = 0; i < g.per_wave; ++i) {
+        const int seg = (part * WAVES + wave) * g.per_wave + i;
+        if (seg >= g.segs)
+            break;
+        const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
+        float top = NEG;
+        double sum = 0.0;
+        for (int s = s0; s < s1; s += U) {
+            Raw<TYPE> raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (s + u < s1)
+                    raw[u].load(row.p, int64_t(s + u) * SM_STEP + lane * SM_VEC, row.vocab);
+                else
+                    raw[u].clear();
+            }
+            float m = top;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < SM_VEC; ++k) {
+                    const float x = raw[u].at(k);
+                    m = x > m ? x : m;
+                }
+            m = read_lane(wave_inclusive_scan<MaxF32>(m), 63);
+            if (m == NEG || !sums) {  // nothing yet, or only the largest is asked for
+                top = m;
+                continue;
+            }
+            // the running sum changes over to the new largest value
+            const bool inf = m == __builtin_inff();
+            if (m != top)
+                sum = inf || top == NEG ? 0.0 : sum * exp2_exact((double(top) - double(m)) * c);
+            top = m;
+            if (inf) {  // +inf counts 1 each, the rest nothing
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < SM_VEC; ++k)
+                        sum += raw[u].at(k) == m ? 1.0 : 0.0;
+                continue;
+            }
+            const double m64 = double(m);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (s + u < s1) {
+#pragma unroll
+                    for (int k = 0; k < SM_VEC; ++k)
+                        sum += exp2_fast(__builtin_fmax(double(raw[u].at(k)) - m64, far), c);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
             }
         }
         sum = wave_inclusive_sum64(sum);
-        if (lane == 63)
-            lds.seg[s] = sum;
-    }
-    if (tid == 0) {
-        lds.bin = ~0u;
-        lds.best = 0;
-    }
-    __syncthreads();
-    const double mine = tid < row.segs ? lds.seg[tid] : 0.0;
-    const double incl = block_inclusive_sum(mine, lds, total);
-    const double goal = goal_of(total);
-    if (incl > goal)
-        atomicMin(&lds.bin, uint32_t(tid));
-    if (mine > 0.0)
-        atomicMax(&lds.best, uint32_t(tid));
-    lds.seg[tid] = incl;
-    __syncthreads();
-    const int s = int(lds.bin != ~0u ? lds.bin : lds.best);
-    if (wave == 0) {
-        double run = s > 0 ? lds.seg[s - 1] : 0.0;
-        int64_t found = -1, last = 0;
-        for (int j = 0; j < row.seg_steps && found < 0; ++j) {
-            const int64_t idx = (int64_t(s) * row.seg_steps + j) * SM_STEP + lane * SM_VEC;
-            float x[SM_VEC];
-#pragma unroll
-            for (int k = 0; k < SM_VEC; ++k)
-                x[k] = -__builtin_inff();
-            if (idx < row.vocab)
-                load_logits<TYPE>(row.p, idx, row.vocab, x);
-            double w[SM_VEC], sum = 0.0;
-#pragma unroll
-            for (int k = 0; k < SM_VEC; ++k) {
-                w[k] = idx + k < row.vocab ? f(x[k], uint32_t(idx + k)) : 0.0;
-                sum += w[k];
-            }
-            const double lane_incl = wave_inclusive_sum64(sum);
-            double r = run + (lane_incl - sum);
-            int hit = SM_VEC, end = -1;
-#pragma unroll
-            for (int k = 0; k < SM_VEC; ++k) {
-                r += w[k];
-                if (w[k] > 0.0) {
-                    end = k;
-                    if (r > goal && hit == SM_VEC)
-                        hit = k;
-                }
-            }
-            const uint64_t hits = __ballot(hit < SM_VEC), ends = __ballot(end >= 0);
-            const int64_t step0 = (int64_t(s) * row.seg_steps + j) * SM_STEP;
-            if (hits != 0) {
-                const int l = __builtin_ctzll(hits);
-                found = step0 + l * SM_VEC + read_lane(hit, l);
-            }
-            if (ends != 0) {
-                const int l = 63 - __builtin_clzll(ends);
-                last = step0 + l * SM_VEC + read_lane(end, l);
-            }
-            run += read_lane64(lane_incl, 63);
+        if (lane == 63) {
+            put(&g.tops[r * g.segs + seg], top);
+            put(&g.sums[r * g.segs + seg], sum);
         }
-        if (lane == 0)
-            lds.tie_index = uint32_t(found >= 0 ? found : last);
     }
-    __syncthreads();
-    return int64_t(lds.tie_index);
+    stores_done();
+    bool last = false;
+    if (lane == 0)
+        last = count_in(&g.counters[r], uint32_t(g.parts * WAVES));
+    if (__ballot(last) == 0)
+        return;
+
+    Tops tops;
+    const float top = tops.load(g, r);
+    if (settle(call, g, r, row, tops, top, true))
+        return;
+    double v[SM_PER_LANE], incl, total, before = 0.0;
+#pragma unroll
+    for (int k = 0; k < SM_PER_LANE; ++k) {
+        v[k] = 0.0;
+        if (k < tops.per_lane && tops.v[k] != NEG)
+            v[k] = get(&g.sums[r * g.segs + tops.seg(k)]) * row.weight(clean(tops.v[k], row.inf));
+    }
+    wave_sums(v, incl, total);
+    const double goal = goal_of(double(call.uniforms[r]), total);
+    bool over;
+    const int at = wave_first_over(v, goal, incl, before, over);
+    const int seg = at / SM_PER_LANE * tops.per_lane + at % SM_PER_LANE;
+    const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
+    const uint32_t token =
+        wave_find_token(row, s0, s1, before, goal, [&](float x, uint32_t) { return row.weight(x); });
+    write_token(call, r, row, token, total);
 }
 
-// Ascending sort of the list's first n entries.
-__device__ void sort_list(SampleLds& lds, uint32_t n)
+// ---------------------------------------------------------------- cuts
+struct SharedCuts {
+    SharedSums s;
+    uint64_t mass[SM_WAVES][SM_BINS];  // weight by bin of each sixteenth of the row, in units of the bin's octave
+    uint64_t bin_mass[SM_BINS];        // of all
+    uint32_t bin_count[SM_BINS];
+    uint64_t range_mass[SM_RANGES];
+    uint32_t range_count[SM_RANGES];
+    uint64_t list[SM_LIST];    // places in the order: (largest key - key) << index_bits | index
+    uint64_t small[SM_SMALL], sorted[SM_SMALL];
+    double weight[SM_SMALL];
+    double part_sum[SM_WAVES];
+    uint64_t part_mass[SM_WAVES];
+    uint32_t n_list, n_small;
+    uint16_t segs[SM_WAVES][SM_SEGS / SM_WAVES];  // each wave's segments with candidates
+};
+
+// Counts `mine` lanes' flagged elements into a shared counter, one addition for the wave:
+// the place of this lane's first.
+__device__ __forceinline__ uint32_t wave_append(uint32_t* counter, uint32_t mine)
 {
-    uint32_t size = 2;
-    while (size < n)
-        size <<= 1;
-    for (uint32_t i = n + threadIdx.x; i < size; i += SM_BLOCK)
-        lds.list[i] = ~uint64_t(0);
-    for (uint32_t run = 2; run <= size; run <<= 1) {
-        for (uint32_t d = run >> 1; d > 0; d >>= 1) {
-            __syncthreads();
-            for (uint32_t i = threadIdx.x; i < size / 2; i += SM_BLOCK) {
-                const uint32_t a = 2 * i - (i & (d - 1)), b = a + d;
-                const uint64_t va = lds.list[a], vb = lds.list[b];
-                if ((va > vb) == ((a & run) == 0)) {
-                    lds.list[a] = vb;
-                    lds.list[b] = va;
-                }
-            }
-        }
-    }
+    const uint32_t incl = wave_inclusive_scan<SumU32>(mine), all = read_lane(incl, 63);
+    uint32_t base = 0;
+    if (lane_id() == 0)
+        base = atomicAdd(counter, all);
+    return uniform(base) + incl - mine;
+}
+
+// Orders the n <= SM_SMALL distinct places of `small` into `sorted`: each place's rank is the
+// number of smaller ones, counted by a group of lanes.
+__device__ __forceinline__ void order_small(SharedCuts& sh, uint32_t n)
+{
+    uint32_t group = 64;
+    while (group > 1 && SM_BLOCK / group < n)
+        group >>= 1;
+    const uint32_t e = threadIdx.x / group, part = threadIdx.x & (group - 1);
+    uint32_t rank = 0;
+    const uint64_t v = e < n ? sh.small[e] : 0;
+    if (e < n)
+        for (uint32_t j = part; j < n; j += group)
+            rank += sh.small[j] < v ? 1u : 0u;
+    for (uint32_t d = 1; d < group; d <<= 1)
+        rank += __shfl_xor(rank, int(d));
+    if (e < n && part == 0)
+        sh.sorted[rank] = v;
     __syncthreads();
 }
 
-// Puts the bins' counts and weights together: picks the bin in which the running count
-// reaches `want` (by_count) or the running weight reaches `goal`, into lds.bin, and what
-// lies before it into lds.above / lds.above_count.  `total` and `elements` are the sums.
+// One wave (all of them alike): the first of 256 bins or ranges at which the running count
+// reaches `want` (by_count) or the running weight `goal`, the last one that holds anything
+// if none does.  above_count and above become what lies before it, `n` what it holds.
 template <class W>
-__device__ void pick_bin(SampleLds& lds, W weight_of, bool by_count, uint32_t want, double goal, double base,
-                         double& total, uint32_t& elements)
+__device__ __forceinline__ uint32_t pick(const uint32_t* counts, const uint64_t* masses, W weight_of, bool by_count,
+                                         uint32_t want, double goal, uint32_t& above_count, double& above,
+                                         double& total, uint32_t& n)
 {
-    const int tid = threadIdx.x;
-    __syncthreads();
-    if (tid == 0)
-        lds.bin = ~0u, lds.best = 0;
-    const uint32_t n0 = lds.count[2 * tid], n1 = lds.count[2 * tid + 1];
-    const double m0 = weight_of(lds.mass[2 * tid], 2 * tid), m1 = weight_of(lds.mass[2 * tid + 1], 2 * tid + 1);
-    const uint32_t n_incl = block_inclusive_sum(n0 + n1, lds, elements);
-    const double m_incl = block_inclusive_sum(m0 + m1, lds, total) + base;
-    const uint32_t n_a = n_incl - n1, n_before = n_a - n0;
-    const double m_a = m_incl - m1, m_before = m_a - m0;
-    if (n1 != 0)
-        atomicMax(&lds.best, uint32_t(2 * tid + 1));
-    else if (n0 != 0)
-        atomicMax(&lds.best, uint32_t(2 * tid));
-    if (n0 != 0 && (by_count ? n_a >= want : m_a >= goal))
-        atomicMin(&lds.bin, uint32_t(2 * tid));
-    else if (n1 != 0 && (by_count ? n_incl >= want : m_incl >= goal))
-        atomicMin(&lds.bin, uint32_t(2 * tid + 1));
-    __syncthreads();
-    if (tid == 0 && lds.bin == ~0u)
-        lds.bin = lds.best;  // rounding at the very end of the sums
-    __syncthreads();
-    const int b = int(lds.bin);
-    if (b / 2 == tid) {
-        lds.above = b & 1 ? m_a : m_before;
-        lds.above_count = b & 1 ? n_a : n_before;
+    constexpr int N = SM_BINS / 64;
+    const int first = lane_id() * N;
+    uint32_t c[N], cs = 0;
+    double m[N], ms = 0.0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        c[k] = counts[first + k];
+        m[k] = weight_of(masses[first + k], uint32_t(first + k));
+        cs += c[k];
+        ms += m[k];
     }
-    __syncthreads();
+    const uint32_t c_incl = wave_inclusive_scan<SumU32>(cs);
+    const double m_incl = wave_inclusive_sum64(ms);
+    total = read_lane64(m_incl, 63);
+    uint32_t cr = above_count + c_incl - cs, hit_c = 0, last_c = 0, hit_n = 0, last_n = 0;
+    double mr = above + (m_incl - ms), hit_m = 0.0, last_m = 0.0;
+    int hit = -1, last = -1;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t cu = cr + c[k];
+        const double mu = mr + m[k];
+        if (c[k] != 0) {
+            last = k, last_c = cr, last_m = mr, last_n = c[k];
+            if (hit < 0 && (by_count ? cu >= want : mu >= goal))
+                hit = k, hit_c = cr, hit_m = mr, hit_n = c[k];
+        }
+        cr = cu;
+        mr = mu;
+    }
+    const uint64_t hits = __ballot(hit >= 0), any = __ballot(last >= 0);
+    const bool over = hits != 0;
+    const int l = over ? __builtin_ctzll(hits) : any != 0 ? 63 - __builtin_clzll(any) : 0;
+    above_count = read_lane(over ? hit_c : last_c, l);
+    above = read_lane64(over ? hit_m : last_m, l);
+    n = read_lane(over ? hit_n : last_n, l);
+    const int k = read_lane(over ? hit : last, l);
+    return uint32_t(l * N + (k < 0 ? 0 : k));
 }
 
-// The cut inside one bin of the row's histogram (`bin`, holding `n` elements): the
-// element that makes the count reach `want` (by_count) or the weight reach `goal`, where
-// `above_count` and `above` lie in front of the bin.  Returns the weight up to and
-// including the cut.
+// The smallest key whose bin is at most b (all keys down to the lowest finite one for the
+// last bin), by one wave: 64 tries a step, the first ones around where the bin ends by
+// its formula.
 template <int TYPE>
-__device__ Cut cut_in_bin(const Row<TYPE>& row, SampleLds& lds, int bin, uint32_t n, bool by_count, uint32_t want,
-                          double goal, uint32_t above_count, double above, double& weight)
+__device__ __forceinline__ uint32_t lowest_key(const Row<TYPE>& row, uint32_t b)
 {
-    const int tid = threadIdx.x;
-    const double inf = __builtin_inf();
-    uint32_t lo = 0, hi = ~0u;  // the keys looked at
-    if (n > SM_LIST) {
-        __syncthreads();
-        if (tid == 0)
-            lds.key_lo = ~0u, lds.key_hi = 0;
-        __syncthreads();
-        uint32_t klo = ~0u, khi = 0;
-        row.for_each([&](const float(&x)[SM_VEC], int64_t) {
-#pragma unroll
-            for (int k = 0; k < SM_VEC; ++k) {
-                if (x[k] != -inf && row.bin(row.log2w(x[k])) == bin) {
-                    const uint32_t key = key_of(x[k]);
-                    klo = key < klo ? key : klo;
-                    khi = key > khi ? key : khi;
-                }
-            }
-        });
-        atomicMin(&lds.key_lo, klo);
-        atomicMax(&lds.key_hi, khi);
-        __syncthreads();
-        lo = lds.key_lo;
-        hi = lds.key_hi;
+    uint32_t lo = KEY_NEG_INF, hi = key_of(row.top);  // lo is out, hi is in
+    if (b >= SM_BINS - 1)
+        return KEY_NEG_INF + 1;
+    const float edge = float(row.top64 - (double(b) + 0.5) / SM_PER_OCTAVE / row.c);
+    if (edge > -__builtin_inff() && edge < row.top) {
+        const uint32_t key = uniform(key_of(edge)) - 32u + uint32_t(lane_id());
+        const uint64_t in = __ballot(key >= hi || (key > lo && row.bin(row.below(value_of(key))) <= b));
+        const int l = in != 0 ? __builtin_ctzll(in) : 64;
+        const uint32_t first = uniform(key_of(edge)) - 32u;
+        if (l > 0 && first > lo)
+            lo = first + uint32_t(l) - 1u;  // out
+        if (l < 64 && first + uint32_t(l) < hi)
+            hi = first + uint32_t(l);
     }
-    while (n > SM_LIST && lo != hi) {
-        const uint32_t span = hi - lo;
-        const int bits = 32 - __builtin_clz(span);
-        const int shift = bits > 11 ? bits - 11 : 0;  // 2048 ranges
-        __syncthreads();
-        for (int i = tid; i < SM_BINS; i += SM_BLOCK) {
-            lds.mass[i] = 0;
-            lds.count[i] = 0;
-        }
-        __syncthreads();
-        row.for_each([&](const float(&x)[SM_VEC], int64_t) {
-#pragma unroll
-            for (int k = 0; k < SM_VEC; ++k) {
-                const uint32_t key = key_of(x[k]);
-                if (key >= lo && key <= hi) {
-                    const uint32_t b = (hi - key) >> shift;
-                    atomicAdd(&lds.count[b], 1u);
-                    atomicAdd(reinterpret_cast<unsigned long long*>(&lds.mass[b]),
-                              static_cast<unsigned long long>(row.fixed(row.weight(x[k]), bin)));
-                }
-            }
-        });
-        double total;
-        uint32_t elements;
-        pick_bin(
-            lds, [&](uint64_t m, int) { return row.unfixed(m, bin); }, by_count, want - above_count, goal, above, total,
-            elements);
-        const uint32_t b = lds.bin;
-        above = lds.above;
-        above_count += lds.above_count;
-        n = lds.count[b];
-        hi -= b << shift;
-        const uint32_t width = (1u << shift) - 1u;
-        lo = hi - lo > width ? hi - width : lo;
-        __syncthreads();
+    while (hi - lo > 1) {
+        const uint32_t step = (hi - lo + 63) / 64, off = uint32_t(lane_id() + 1) * step;
+        const uint32_t key = off < hi - lo ? lo + off : hi;
+        const uint64_t in = __ballot(key == hi || row.bin(row.below(value_of(key))) <= b);
+        const int l = __builtin_ctzll(in);
+        const uint32_t first = read_lane(key, l), before = l > 0 ? read_lane(key, l - 1) : lo;
+        lo = before;
+        hi = first;
     }
-    if (n > SM_LIST) {
-        // equal values: the cut falls at a count of them, in index order
-        const double w = row.weight(value_of(lo));
-        uint32_t take = n;
-        if (by_count) {
-            take = want - above_count;
-        } else if (w > 0.0) {
-            const double m = __builtin_ceil((goal - above) / w);
-            take = m < 1.0 ? 1u : (m < double(n) ? uint32_t(m) : n);
-        }
-        double ties;
-        const uint32_t key = lo;
-        const int64_t at = find_in_order(
-            row, lds, [&](float x, uint32_t) { return key_of(x) == key ? 1.0 : 0.0; },
-            [&](double) { return double(take) - 0.5; }, ties);
-        weight = above + w * double(take);
-        return Cut{key, uint32_t(at)};
-    }
-    __syncthreads();
-    if (tid == 0)
-        lds.n_list = 0, lds.best = ~0u;
-    __syncthreads();
-    row.for_each([&](const float(&x)[SM_VEC], int64_t idx) {
-#pragma unroll
-        for (int k = 0; k < SM_VEC; ++k) {
-            const uint32_t key = key_of(x[k]);
-            if (x[k] != -inf && key >= lo && key <= hi && row.bin(row.log2w(x[k])) == bin) {
-                const uint32_t at = atomicAdd(&lds.n_list, 1u);
-                if (at < SM_LIST)
-                    lds.list[at] = (uint64_t(~key) << 32) | uint32_t(idx + k);
-            }
-        }
-    });
-    __syncthreads();
-    n = lds.n_list < SM_LIST ? lds.n_list : SM_LIST;
-    sort_list(lds, n);
-    constexpr int PER = SM_LIST / SM_BLOCK;
-    double w[PER], sum = 0.0, total;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const uint32_t i = tid * PER + k;
-        w[k] = i < n ? row.weight(value_of(~uint32_t(lds.list[i] >> 32))) : 0.0;
-        sum += w[k];
-    }
-    const double incl = block_inclusive_sum(sum, lds, total);
-    double r = above + (incl - sum);
-    uint32_t at = ~0u;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const uint32_t i = tid * PER + k;
-        r += w[k];
-        if (at == ~0u && i < n && (by_count ? above_count + i + 1 >= want : r >= goal))
-            at = i;
-    }
-    if (at != ~0u)
-        atomicMin(&lds.best, at);
-    __syncthreads();
-    at = lds.best != ~0u ? lds.best : n - 1;
-    r = above + (incl - sum);
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        r += w[k];
-        if (uint32_t(tid * PER + k) == at)
-            lds.total = r;
-    }
-    __syncthreads();
-    weight = lds.total;
-    const uint64_t e = lds.list[at];
-    return Cut{~uint32_t(e >> 32), uint32_t(e)};
+    return hi;
 }
 
-// One block per row.
+struct Bin {
+    uint32_t bin, key_lo, key_hi;
+};
+
 template <int TYPE>
-__global__ __launch_bounds__(SM_BLOCK) void sample_row_kernel(SampleCall call)
+__device__ __forceinline__ Bin make_bin(const Row<TYPE>& row, uint32_t b)
 {
-    __shared__ SampleLds lds;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const double inf = __builtin_inf();
-    const int64_t r = blockIdx.x;
-    constexpr int SIZE = TYPE == LOGITS_F32 ? 4 : 2;
+    Bin bin;
+    bin.bin = b;
+    bin.key_lo = lowest_key(row, b);
+    bin.key_hi = b > 0 ? lowest_key(row, b - 1) - 1 : key_of(row.top);
+    return bin;
+}
 
-    Row<TYPE> row;
-    row.p = static_cast<const char*>(call.logits) + r * call.stride * SIZE;
-    row.vocab = call.vocab;
-    const int64_t steps = (call.vocab + SM_STEP - 1) / SM_STEP;
-    row.seg_steps = int((steps + SM_SEGS - 1) / SM_SEGS);
-    row.segs = row.seg_steps > 0 ? int((steps + row.seg_steps - 1) / row.seg_steps) : 0;
-    int bits = 0;
-    while (bits < 31 && (int64_t(1) << bits) < call.vocab)
-        ++bits;
-    row.frac = 62 - bits < 45 ? 62 - bits : 45;
+// A place in the order, relative to a bin's largest key.
+template <int TYPE>
+__device__ __forceinline__ uint64_t place_of(const Row<TYPE>& row, uint32_t key_hi, uint32_t key, uint32_t index)
+{
+    return (uint64_t(key_hi - key) << row.index_bits) | index;
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t key_at(const Row<TYPE>& row, uint32_t key_hi, uint64_t place)
+{
+    return key_hi - uint32_t(place >> row.index_bits);
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t index_at(const Row<TYPE>& row, uint64_t place)
+{
+    return uint32_t(place) & ((1u << row.index_bits) - 1u);
+}
 
-    float top = -__builtin_inff();
-    row.for_each([&](const float(&x)[SM_VEC], int64_t) {
+// Collects the places in [lo, hi] of a bin's elements into the list; their number (the list
+// holds SM_LIST).
+template <int TYPE>
+__device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, uint64_t lo,
+                                            uint64_t hi)
+{
+    const float x_lo = value_of(bin.key_lo), x_hi = value_of(bin.key_hi);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        sh.n_list = 0;
+    __syncthreads();
+    row.template for_steps<2>(int(threadIdx.x >> 6), row.steps, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+        uint32_t in = 0;
 #pragma unroll
         for (int k = 0; k < SM_VEC; ++k)
-            top = x[k] > top ? x[k] : top;
-    });
-    top = wave_max(top);
-    if (lane == 0)
-        lds.wave_u32[wave] = to_bits(top);
-    __syncthreads();
-    for (int w = 0; w < SM_WAVES; ++w)
-        top = __builtin_fmaxf(top, from_bits<float>(lds.wave_u32[w]));
-    row.top = top;
-    if (top == -__builtin_inff()) {
-        if (tid == 0) {
-            call.tokens[r] = -1;
-            if (call.logprobs != nullptr)
-                call.logprobs[r] = -__builtin_inff();
-        }
-        return;
-    }
-    const float t = call.temperature[r];
-    if (!(t > 0.0f)) {
-        if (tid == 0)
-            lds.best = ~0u;
-        __syncthreads();
-        uint32_t first = ~0u;
-        row.for_each([&](const float(&x)[SM_VEC], int64_t idx) {
+            in |= x[k] >= x_lo && x[k] <= x_hi ? 1u << k : 0u;
+        if (__ballot(in != 0) == 0)
+            return;
+        uint64_t v[SM_VEC];
 #pragma unroll
-            for (int k = SM_VEC - 1; k >= 0; --k)
-                if (x[k] == top && uint32_t(idx + k) < first)
-                    first = uint32_t(idx + k);
-        });
-        if (first != ~0u)
-            atomicMin(&lds.best, first);
-        __syncthreads();
-        if (tid == 0) {
-            call.tokens[r] = int64_t(lds.best);
-            if (call.logprobs != nullptr)
-                call.logprobs[r] = 0.0f;
+        for (int k = 0; k < SM_VEC; ++k) {
+            v[k] = place_of(row, bin.key_hi, key_of(x[k]), idx + k);
+            if (v[k] < lo || v[k] > hi)
+                in &= ~(1u << k);
         }
+        uint32_t at = wave_append(&sh.n_list, uint32_t(__builtin_popcount(in)));
+#pragma unroll
+        for (int k = 0; k < SM_VEC; ++k) {
+            if (in >> k & 1u) {
+                if (at < SM_LIST)
+                    sh.list[at] = v[k];
+                ++at;
+            }
+        }
+    });
+    __syncthreads();
+    return uniform(sh.n_list);
+}
+
+// The element of a bin that makes the count reach `want` (by_count) or the weight reach
+// `goal`, where above_count and above lie in front of the bin.  Its elements are
+// collected; while they are too many, the range of places is cut into SM_RANGES and the
+// one the cut lies in is kept (at one place to a range there is one element left, so this
+// ends).  Returns the place; `weight`: the weight up to and including it; `listed`:
+// whether the list holds the whole bin.
+template <int TYPE>
+__device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, bool by_count,
+                                               uint32_t want, double goal, uint32_t above_count, double above,
+                                               double& weight, bool& listed)
+{
+    const uint32_t tid = threadIdx.x;
+    uint64_t lo = 0, hi = place_of(row, bin.key_hi, bin.key_lo, (1u << row.index_bits) - 1u);
+    uint32_t n = collect(row, sh, bin, lo, hi);
+    listed = n <= SM_LIST;
+    bool in_list = listed;
+    while (n > SM_SMALL) {
+        const uint64_t span = hi - lo;
+        const int bits = 64 - __builtin_clzll(span | 1u);
+        const int shift = bits > 8 ? bits - 8 : 0;
+        static_assert(SM_RANGES == 1 << 8, "eight bits of the span");
+        if (tid < SM_RANGES) {
+            sh.range_mass[tid] = 0;
+            sh.range_count[tid] = 0;
+        }
+        __syncthreads();
+        const auto add = [&](uint64_t v, float x) {
+            const uint32_t b = uint32_t((v - lo) >> shift);
+            atomicAdd(&sh.range_count[b], 1u);
+            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.range_mass[b]),
+                      static_cast<unsigned long long>(row.fixed(row.below(x), bin.bin)));
+        };
+        if (in_list) {
+            for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
+                const uint64_t v = sh.list[i];
+                if (v >= lo && v <= hi)
+                    add(v, value_of(key_at(row, bin.key_hi, v)));
+            }
+        } else {
+            const float x_lo = value_of(bin.key_lo), x_hi = value_of(bin.key_hi);
+            row.template for_steps<2>(int(tid >> 6), row.steps, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+#pragma unroll
+                for (int k = 0; k < SM_VEC; ++k) {
+                    if (x[k] >= x_lo && x[k] <= x_hi) {
+                        const uint64_t v = place_of(row, bin.key_hi, key_of(x[k]), idx + k);
+                        if (v >= lo && v <= hi)
+                            add(v, x[k]);
+                    }
+                }
+            });
+        }
+        __syncthreads();
+        double total;
+        const uint32_t b = pick(
+            sh.range_count, sh.range_mass, [&](uint64_t m, uint32_t) { return row.unfixed(m, bin.bin); }, by_count,
+            want, goal, above_count, above, total, n);
+        lo += uint64_t(b) << shift;
+        const uint64_t last = lo + ((uint64_t(1) << shift) - 1);
+        hi = hi < last ? hi : last;
+        __syncthreads();
+        if (!in_list && n <= SM_LIST) {
+            collect(row, sh, bin, lo, hi);
+            in_list = true;
+        }
+    }
+    if (tid == 0)
+        sh.n_small = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
+        const uint64_t v = sh.list[i];
+        if (v >= lo && v <= hi)
+            sh.small[atomicAdd(&sh.n_small, 1u)] = v;
+    }
+    __syncthreads();
+    order_small(sh, n);
+    // 64 of the order at a time, by every wave for itself
+    uint64_t place = 0;
+    for (uint32_t i = 0; i < n; i += 64) {
+        const uint32_t at = i + uint32_t(lane_id());
+        place = at < n ? sh.sorted[at] : 0;
+        const double w = at < n ? row.weight(value_of(key_at(row, bin.key_hi, place))) : 0.0;
+        const double incl = above + wave_inclusive_sum64(w);
+        const uint64_t hits =
+            __ballot(at < n && (at == n - 1 || (by_count ? above_count + at + 1 >= want : incl >= goal)));
+        if (hits != 0) {
+            const int l = __builtin_ctzll(hits);
+            place = read_lane64(place, l);
+            weight = read_lane64(incl, l);
+            break;
+        }
+        above = read_lane64(incl, 63);
+    }
+    return place;
+}
+
+// The cuts of a row that are not settled by a few candidates: a histogram of weights (and
+// counts, for top-k) by log2 w, eight bins to the octave, tells which bin the cut lies in,
+// and only that bin's elements are collected and ordered.  Weights are added to bins as
+// integers of the bin's octave, so that sums do not depend on the order of the atomics.
+// Each wave takes a sixteenth of the row and keeps its own bins: with the cut known, the
+// kept weight of each sixteenth is known too, and only the one with the token is read
+// for the running sums.
+template <int TYPE>
+__device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const Row<TYPE>& row, SharedCuts& sh,
+                                        uint32_t k, double p, double least, double u)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int share = (row.steps + SM_WAVES - 1) / SM_WAVES;
+    const bool by_k = int64_t(k) < row.vocab, by_p = p < 1.0;
+    Cut cut{0u, ~0u};  // keeps all
+    bool in_parts = false;
+    Bin bin{0, 0, 0};
+    uint64_t place = 0;
+    if (by_k || by_p) {
+        for (int i = lane; i < SM_BINS; i += 64)
+            sh.mass[wave][i] = 0;
+        if (tid < SM_BINS)
+            sh.bin_count[tid] = 0;
+        if (tid < SM_WAVES)
+            sh.part_mass[tid] = 0;
+        __syncthreads();
+        const int first = wave * share, end = first + share < row.steps ? first + share : row.steps;
+        uint64_t* mass = sh.mass[wave];
+        row.template for_steps<2>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+#pragma unroll
+            for (int j = 0; j < SM_VEC; ++j) {
+                const double d = row.below(x[j]);
+                const uint32_t b = row.bin(d);
+                atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
+                          static_cast<unsigned long long>(row.fixed(d, b)));
+                if (by_k && x[j] != -__builtin_inff())
+                    atomicAdd(&sh.bin_count[b], 1u);
+            }
+        });
+        __syncthreads();
+        if (tid < SM_BINS) {
+            uint64_t m = 0;
+#pragma unroll
+            for (int w = 0; w < SM_WAVES; ++w)
+                m += sh.mass[w][tid];
+            sh.bin_mass[tid] = m;
+            if (!by_k)
+                sh.bin_count[tid] = m != 0 ? 1u : 0u;
+        }
+        __syncthreads();
+        const auto in_bin = [&](uint64_t m, uint32_t b) { return row.unfixed(m, b); };
+        uint32_t above_count = 0, n;
+        double above = 0.0, total;
+        uint32_t b = pick(sh.bin_count, sh.bin_mass, in_bin, by_k, k, p * 0.0, above_count, above, total, n);
+        double kept = total;
+        if (by_k && above_count + n >= k) {
+            bin = make_bin(row, b);
+            place = cut_in_bin(row, sh, bin, true, k, 0.0, above_count, above, kept, in_parts);
+            cut = Cut{key_at(row, bin.key_hi, place), index_at(row, place)};
+        }
+        if (by_p) {
+            const double goal = p * kept;
+            const Bin k_bin = bin;
+            const uint64_t k_place = place;
+            const Cut k_cut = cut;
+            above_count = 0;
+            above = 0.0;
+            b = pick(sh.bin_count, sh.bin_mass, in_bin, false, 0, goal, above_count, above, total, n);
+            bin = make_bin(row, b);
+            double weight;
+            place = cut_in_bin(row, sh, bin, false, 0, goal, 0, above, weight, in_parts);
+            cut = Cut{key_at(row, bin.key_hi, place), index_at(row, place)};
+            if (k_cut.key != 0 && cut.keeps(k_cut.key, k_cut.index)) {
+                // no later than top-k's own cut, which rounding may have put first
+                in_parts = in_parts && k_bin.bin == bin.bin;
+                place = k_place;
+                cut = k_cut;
+            }
+        }
+    }
+    // where the cut's own element has the weight that min-p asks for, min-p drops nothing more
+    if (cut.key != 0 && row.weight(value_of(cut.key)) >= least)
+        least = 0.0;
+    const auto kept_weight = [&](float x, uint32_t i) {
+        const double w = cut.keeps(key_of(x), i) ? row.weight(x) : 0.0;
+        return w >= least ? w : 0.0;
+    };
+    double total;
+    if (in_parts && least == 0.0 && u > 0.0) {
+        for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
+            const uint64_t v = sh.list[i];
+            if (v <= place)
+                atomicAdd(reinterpret_cast<unsigned long long*>(
+                              &sh.part_mass[index_at(row, v) / uint32_t(share * SM_STEP)]),
+                          static_cast<unsigned long long>(
+                              row.fixed(row.below(value_of(key_at(row, bin.key_hi, v))), bin.bin)));
+        }
+        double sum = 0.0;
+        for (uint32_t b = lane; b < bin.bin; b += 64)
+            sum += row.unfixed(sh.mass[wave][b], b);
+        sum = wave_inclusive_sum64(sum);
+        if (lane == 63)
+            sh.part_sum[wave] = sum;
+        __syncthreads();
+        // every wave for itself: the sixteenth with the token
+        double v[1] = {lane < SM_WAVES ? sh.part_sum[lane] + row.unfixed(sh.part_mass[lane], bin.bin) : 0.0};
+        double incl, before = 0.0;
+        bool over;
+        wave_sums(v, incl, total);
+        const double goal = goal_of(u, total);
+        const int part = wave_first_over(v, goal, incl, before, over);
+        const int begin = part * share, end = begin + share < row.steps ? begin + share : row.steps;
+        // a wave takes one step in sixteen of it, adds up and hands the sums round
+        const int per = (share + SM_WAVES - 1) / SM_WAVES;
+        const int mine = begin + wave * per, mine_end = mine + per < end ? mine + per : end;
+        sum = 0.0;
+        row.template for_steps<1>(mine, mine_end, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
+#pragma unroll
+            for (int j = 0; j < SM_VEC; ++j)
+                sum += kept_weight(x[j], idx + j);
+        });
+        sum = wave_inclusive_sum64(sum);
+        __syncthreads();
+        if (lane == 63)
+            sh.part_sum[wave] = sum;
+        __syncthreads();
+        double rest;
+        v[0] = lane < SM_WAVES ? sh.part_sum[lane] : 0.0;
+        wave_sums(v, incl, rest);
+        if (wave_first_over(v, goal, incl, before, over) == wave)
+            write_token(call, r, row, wave_find_token(row, mine, mine_end, before, goal, kept_weight), total);
         return;
     }
-    row.c = 0x1.71547652b82fep+0 / double(t);
+    const uint32_t token = find_in_order(row, sh.s, u, kept_weight, total);
+    if (wave == 0)
+        write_token(call, r, row, token, total);
+}
 
-    // the cuts in force
+// Rows whose cut lies within a few candidates: at least the k largest elements (few), or all
+// that min-p may keep.  False when they are more than SM_SMALL.
+template <int TYPE>
+__device__ __forceinline__ bool cut_candidates(const SampleCall& call, const SampleGrid& g, int64_t r,
+                                               const Row<TYPE>& row, SharedCuts& sh, const Tops& tops, bool few,
+                                               uint32_t k, double p, double least, double u)
+{
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    if (tid == 0)
+        sh.n_small = 0, sh.s.found = ~0u, sh.s.last = 0;
+    __syncthreads();
+    // every wave for itself up to the reading of the segments
+    float low;
+    if (few) {
+        // the k-th largest of the segments' largest values, to 16 bits of its key
+        uint32_t key[SM_PER_LANE], at = 0;
+#pragma unroll
+        for (int j = 0; j < SM_PER_LANE; ++j)
+            key[j] = key_of(clean(tops.v[j], row.inf)) >> 16;
+        const auto narrow = [&](auto lanes) {
+            for (uint32_t bit = 1u << 15; bit != 0; bit >>= 1) {
+                uint32_t n = 0;
+#pragma unroll
+                for (int j = 0; j < decltype(lanes)::value; ++j)
+                    n += uint32_t(__builtin_popcountll(__ballot(key[j] >= (at | bit))));
+                at = n >= k ? at | bit : at;
+            }
+        };
+        if (tops.per_lane <= 4)
+            narrow(std::integral_constant<int, 4>{});
+        else
+            narrow(std::integral_constant<int, SM_PER_LANE>{});
+        const uint32_t lowest = at << 16;
+        low = value_of(lowest > KEY_NEG_INF ? lowest : KEY_NEG_INF + 1);
+    } else {
+        // a little below the smallest logit that min-p may keep
+        const double x = double(row.top) + ::log(least) * LOG2E / row.c;
+        low = float(x - 1e-6 * (__builtin_fabs(x) + __builtin_fabs(double(row.top))) - 1e-30);
+        low = low > -__builtin_inff() ? low : value_of(KEY_NEG_INF + 1);
+    }
+    uint32_t flags = 0;
+#pragma unroll
+    for (int j = 0; j < SM_PER_LANE; ++j)
+        flags |= clean(tops.v[j], row.inf) >= low ? 1u << j : 0u;
+    const uint32_t mine = uint32_t(__builtin_popcount(flags));
+    const uint32_t incl = wave_inclusive_scan<SumU32>(mine), n_segs = read_lane(incl, 63);
+    if (n_segs > SM_SMALL)
+        return false;
+    uint32_t q = incl - mine;
+#pragma unroll
+    for (int j = 0; j < SM_PER_LANE; ++j) {
+        if (flags >> j & 1u) {
+            if ((q & (SM_WAVES - 1)) == wave)
+                sh.segs[wave][q / SM_WAVES] = uint16_t(tops.seg(j));
+            ++q;
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t key_hi = key_of(row.top);
+    constexpr int U = TYPE == LOGITS_F32 ? 2 : 4;
+    const int todo = int((n_segs + SM_WAVES - 1 - wave) / SM_WAVES) * g.seg_steps;  // this wave's steps
+    for (int i = 0; i < todo; i += U) {
+        Raw<TYPE> raw[U];
+        int step[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            step[j] = g.steps;
+            if (i + j < todo) {
+                const int s = (i + j) / g.seg_steps;
+                step[j] = uniform(int(sh.segs[wave][s])) * g.seg_steps + (i + j - s * g.seg_steps);
+            }
+            if (step[j] < g.steps)
+                raw[j].load(row.p, int64_t(step[j]) * SM_STEP + lane * SM_VEC, row.vocab);
+            else
+                raw[j].clear();
+        }
+        uint32_t in = 0;
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int m = 0; m < SM_VEC; ++m)
+                in |= clean(raw[j].at(m), row.inf) >= low ? 1u << (j * SM_VEC + m) : 0u;
+        uint32_t at = wave_append(&sh.n_small, uint32_t(__builtin_popcount(in)));
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int m = 0; m < SM_VEC; ++m)
+                if (in >> (j * SM_VEC + m) & 1u) {
+                    if (at < SM_SMALL)
+                        sh.small[at] = place_of(row, key_hi, key_of(clean(raw[j].at(m), row.inf)),
+                                                uint32_t(step[j]) * SM_STEP + lane * SM_VEC + uint32_t(m));
+                    ++at;
+                }
+    }
+    __syncthreads();
+    const uint32_t n = uniform(sh.n_small);
+    if (n > SM_SMALL)
+        return false;
+    order_small(sh, n);
+    // Every wave for itself, 64 of the order at a time: the kept ones are its first `keep`, of weight `total`.
+    uint32_t keep = k < n ? k : n;
+    double total = 0.0;
+    if (p < 1.0) {
+        double sum = 0.0;
+        for (uint32_t i = lane; i < keep; i += 64)
+            sum += row.weight(value_of(key_at(row, key_hi, sh.sorted[i])));
+        const double goal = p * read_lane64(wave_inclusive_sum64(sum), 63);
+        for (uint32_t i = 0; i < keep; i += 64) {
+            const uint32_t at = i + lane;
+            const double w = at < keep ? row.weight(value_of(key_at(row, key_hi, sh.sorted[at]))) : 0.0;
+            const double up = total + wave_inclusive_sum64(w);
+            const uint64_t hits = __ballot(at < keep && up >= goal);
+            if (hits != 0)
+                keep = i + uint32_t(__builtin_ctzll(hits)) + 1u;
+            total = read_lane64(up, 63);
+        }
+        total = 0.0;
+    }
+    for (uint32_t i = 0; i < keep; i += 64) {
+        const uint32_t at = i + lane;
+        const double w = at < keep ? row.weight(value_of(key_at(row, key_hi, sh.sorted[at]))) : 0.0;
+        const uint64_t drops = __ballot(at > 0 && at < keep && !(w >= least));
+        if (drops != 0)
+            keep = i + uint32_t(__builtin_ctzll(drops));
+        if (at < keep && wave == 0)
+            sh.weight[at] = w;
+        total += read_lane64(wave_inclusive_sum64(at < keep ? w : 0.0), 63);
+    }
+    __syncthreads();
+    // running sums in index order, each by a group of lanes
+    uint32_t group = 64;
+    while (group > 1 && SM_BLOCK / group < keep)
+        group >>= 1;
+    const uint32_t e = tid / group, part = tid & (group - 1);
+    double run = 0.0;
+    uint32_t index = 0;
+    if (e < keep) {
+        index = index_at(row, sh.sorted[e]);
+        for (uint32_t j = part; j < keep; j += group)
+            run += index_at(row, sh.sorted[j]) <= index ? sh.weight[j] : 0.0;
+    }
+    for (uint32_t d = 1; d < group; d <<= 1)
+        run += __shfl_xor(run, int(d));
+    if (e < keep && part == 0) {
+        if (run > goal_of(u, total))
+            atomicMin(&sh.s.found, index);
+        if (sh.weight[e] > 0.0)
+            atomicMax(&sh.s.last, index);
+    }
+    __syncthreads();
+    if (wave == 0)
+        write_token(call, r, row, sh.s.found != ~0u ? sh.s.found : sh.s.last, total);
+    return true;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, SampleGrid g)
+{
+    __shared__ SharedCuts sh;
+    constexpr float NEG = -__builtin_inff();
+    constexpr int U = 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int64_t r = blockIdx.x % uint32_t(call.rows);
+    const int part = int(blockIdx.x / uint32_t(call.rows));
+    Row<TYPE> row = make_row<TYPE>(call, g, r);
+    for (int i = 0; i < g.per_wave; i += U) {
+        float top[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            top[u] = NEG;
+        for (int j = 0; j < g.seg_steps; ++j) {
+            Raw<TYPE> raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int seg = (part * g.per_wave + i + u) * SM_WAVES + wave, s = seg * g.seg_steps + j;
+                if (i + u < g.per_wave && s < g.steps)
+                    raw[u].load(row.p, int64_t(s) * SM_STEP + lane * SM_VEC, row.vocab);
+                else
+                    raw[u].clear();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < SM_VEC; ++k) {
+                    const float x = raw[u].at(k);
+                    top[u] = x > top[u] ? x : top[u];
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int seg = (part * g.per_wave + i + u) * SM_WAVES + wave;
+            const float m = wave_inclusive_scan<MaxF32>(top[u]);
+            if (lane == 63 && i + u < g.per_wave && seg < g.segs)
+                put(&g.tops[r * g.segs + seg], m);
+        }
+    }
+    stores_done();
+    __syncthreads();
+    if (tid == 0)
+        sh.s.arrived = count_in(&g.counters[r], uint32_t(g.parts)) ? 1u : 0u;
+    __syncthreads();
+    if (uniform(sh.s.arrived) == 0u)
+        return;
+
+    Tops tops;
+    const float top = tops.load(g, r);
+    if (settle(call, g, r, row, tops, top, wave == 0))
+        return;
     uint32_t k = ~0u;
     if (call.top_k != nullptr && call.top_k[r] > 0)
         k = uint32_t(call.top_k[r]);
-    double p = 2.0;
+    double p = 1.0;
     if (call.top_p != nullptr) {
         p = double(call.top_p[r]);
         p = p > 0.0 ? p : 0.0;
@@ -598,114 +1283,95 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_row_kernel(SampleCall call)
     double least = 0.0;
     if (call.min_p != nullptr && call.min_p[r] > 0.0f)
         least = __builtin_fmin(double(call.min_p[r]), 1.0);
-
-    Cut cut{0u, ~0u};  // keeps all
-    if (k < uint64_t(call.vocab) || p < 1.0) {
-        __syncthreads();
-        for (int i = tid; i < SM_BINS; i += SM_BLOCK) {
-            lds.mass[i] = 0;
-            lds.count[i] = 0;
-        }
-        __syncthreads();
-        row.for_each([&](const float(&x)[SM_VEC], int64_t) {
-#pragma unroll
-            for (int j = 0; j < SM_VEC; ++j) {
-                if (x[j] != -inf) {
-                    const double y = row.log2w(x[j]);
-                    const int b = row.bin(y);
-                    atomicAdd(&lds.count[b], 1u);
-                    if (p < 1.0)
-                        atomicAdd(reinterpret_cast<unsigned long long*>(&lds.mass[b]),
-                                  static_cast<unsigned long long>(row.fixed(exp2_neg(y), b)));
-                }
-            }
-        });
-        const auto in_bin = [&](uint64_t m, int b) { return row.unfixed(m, b); };
-        double total;
-        uint32_t elements;
-        pick_bin(lds, in_bin, true, k, 0.0, 0.0, total, elements);
-        const uint32_t kb = lds.bin, kn = lds.count[kb], k_above = lds.above_count;
-        const double m_above = lds.above;
-        const bool cut_k = k < elements;
-        double pmass = total;
-        uint32_t pb = 0, pn = 0, p_above = 0;
-        double p_m_above = 0.0;
-        // the histogram is reused by the refinements, so a cut by k that top-p follows keeps to its own copy:
-        // the weight up to the k-th element comes from the refinement, then the histogram is made again
-        if (cut_k) {
-            cut = cut_in_bin(row, lds, int(kb), kn, true, k, 0.0, k_above, m_above, pmass);
-            if (p < 1.0 && kn > SM_LIST) {
-                __syncthreads();
-                for (int i = tid; i < SM_BINS; i += SM_BLOCK) {
-                    lds.mass[i] = 0;
-                    lds.count[i] = 0;
-                }
-                __syncthreads();
-                row.for_each([&](const float(&x)[SM_VEC], int64_t) {
-#pragma unroll
-                    for (int j = 0; j < SM_VEC; ++j) {
-                        if (x[j] != -inf) {
-                            const double y = row.log2w(x[j]);
-                            const int b = row.bin(y);
-                            atomicAdd(&lds.count[b], 1u);
-                            atomicAdd(reinterpret_cast<unsigned long long*>(&lds.mass[b]),
-                                      static_cast<unsigned long long>(row.fixed(exp2_neg(y), b)));
-                        }
-                    }
-                });
-            }
-        }
-        if (p < 1.0) {
-            const double goal = p * pmass;
-            pick_bin(lds, in_bin, false, 0, goal, 0.0, total, elements);
-            pb = lds.bin;
-            pn = lds.count[pb];
-            p_above = lds.above_count;
-            p_m_above = lds.above;
-            double w;
-            const Cut by_p = cut_in_bin(row, lds, int(pb), pn, false, 0, goal, p_above, p_m_above, w);
-            if (cut.keeps(by_p.key, by_p.index))
-                cut = by_p;
-        }
-    }
-
-    double total;
-    const double u = double(call.uniforms[r]);
-    const int64_t token = find_in_order(
-        row, lds,
-        [&](float x, uint32_t i) {
-            if (!cut.keeps(key_of(x), i))
-                return 0.0;
-            const double w = row.weight(x);
-            return w >= least ? w : 0.0;
-        },
-        [&](double z) { return u > 0.0 ? u * z : 0.0; }, total);
-    if (tid == 0) {
-        call.tokens[r] = token;
-        if (call.logprobs != nullptr) {
-            float x;
-            if constexpr (TYPE == LOGITS_F32)
-                x = static_cast<const float*>(row.p)[token];
-            else
-                x = widen<TYPE>(static_cast<const uint16_t*>(row.p)[token]);
-            call.logprobs[r] = float(row.log2w(x) * 0x1.62e42fefa39efp-1 - ::log(total));
-        }
-    }
+    const double u = uniform(double(call.uniforms[r]));
+    // few enough that the k-th largest of the segments' values leaves few candidates
+    const bool few = uint64_t(k) * 4 <= uint64_t(g.segs) * 3;
+    bool done = false;
+    p = uniform(p);
+    least = uniform(least);
+    if (few || (p >= 1.0 && least > 0.0))
+        done = cut_candidates(call, g, r, row, sh, tops, few, k, p, least, u);
+    if (!done)
+        cut_row(call, r, row, sh, k, p, least, u);
 }
 
-size_t sample_workspace_bytes(int64_t, int64_t) { return 256; }
+// ---------------------------------------------------------------- host side
+static size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
-hipError_t launch_sample(const SampleCall& call, int type, void*, hipStream_t stream)
+static int64_t row_segs(int64_t vocab)
+{
+    const int64_t steps = (vocab + SM_STEP - 1) / SM_STEP;
+    return steps < SM_SEGS ? steps : SM_SEGS;
+}
+
+// header | a counter for each row of a launch | the segments' largest values | their sums.
+// The counters' place is the same for every call, so that nothing else is ever written
+// there and they stay 0 between calls of any sizes.
+static size_t row_cells(int64_t rows, int64_t vocab)
+{
+    return size_t(rows < SM_ROWS ? rows : SM_ROWS) * size_t(row_segs(vocab));
+}
+
+size_t sample_workspace_bytes(int64_t rows, int64_t vocab)
+{
+    const size_t cells = row_cells(rows, vocab);
+    return 256 + SM_ROWS * 4 + round256(cells * 4) + round256(cells * 8);
+}
+
+template <int TYPE>
+static void launch_type(const SampleCall& call, const SampleGrid& g, bool cuts, hipStream_t stream)
+{
+    const dim3 grid(unsigned(call.rows * g.parts));
+    if (cuts)
+        sample_cut_kernel<TYPE><<<grid, SM_BLOCK, 0, stream>>>(call, g);
+    else
+        sample_all_kernel<TYPE><<<grid, SM_ALL_BLOCK, 0, stream>>>(call, g);
+}
+
+hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t stream)
 {
     if (call.rows == 0)
         return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(call.rows));
-    if (type == LOGITS_F32)
-        sample_row_kernel<LOGITS_F32><<<grid, SM_BLOCK, 0, stream>>>(call);
-    else if (type == LOGITS_F16)
-        sample_row_kernel<LOGITS_F16><<<grid, SM_BLOCK, 0, stream>>>(call);
-    else
-        sample_row_kernel<LOGITS_BF16><<<grid, SM_BLOCK, 0, stream>>>(call);
+    const bool cuts = call.top_k != nullptr || call.top_p != nullptr || call.min_p != nullptr;
+    const int64_t rows = call.rows < SM_ROWS ? call.rows : SM_ROWS;  // of a launch
+    SampleGrid g;
+    g.steps = int((call.vocab + SM_STEP - 1) / SM_STEP);
+    g.seg_steps = g.steps > SM_SEGS ? (g.steps + SM_SEGS - 1) / SM_SEGS : 1;
+    // without cuts, where there are rows enough: four steps to a segment, for one sum across the wave to all four
+    if (!cuts && rows * g.steps >= 4 * 8192 && g.seg_steps < 4)
+        g.seg_steps = 4;
+    g.segs = (g.steps + g.seg_steps - 1) / g.seg_steps;
+    // segments to a wave: four once that leaves 8192 waves
+    const int waves = cuts ? SM_WAVES : SM_ALL_BLOCK / 64;
+    g.per_wave = int(rows * g.segs >= 4 * 8192 ? 4 : rows * g.segs >= 2 * 8192 ? 2 : 1);
+    g.parts = (g.segs + waves * g.per_wave - 1) / (waves * g.per_wave);
+    if (g.parts < 1)
+        g.parts = 1;
+    char* at = static_cast<char*>(ws) + 256;
+    g.counters = reinterpret_cast<uint32_t*>(at);
+    at += SM_ROWS * 4;
+    g.tops = reinterpret_cast<float*>(at);
+    at += round256(row_cells(call.rows, call.vocab) * 4);
+    g.sums = reinterpret_cast<double*>(at);
+    SampleCall now = call;
+    for (int64_t r = 0; r < call.rows; r += rows) {
+        now.rows = call.rows - r < rows ? call.rows - r : rows;
+        if (type == LOGITS_F32)
+            launch_type<LOGITS_F32>(now, g, cuts, stream);
+        else if (type == LOGITS_F16)
+            launch_type<LOGITS_F16>(now, g, cuts, stream);
+        else
+            launch_type<LOGITS_BF16>(now, g, cuts, stream);
+        const int64_t size = type == LOGITS_F32 ? 4 : 2;
+        now.logits = static_cast<const char*>(now.logits) + rows * now.stride * size;
+        now.uniforms += rows;
+        now.temperature += rows;
+        now.top_k += now.top_k != nullptr ? rows : 0;
+        now.top_p += now.top_p != nullptr ? rows : 0;
+        now.min_p += now.min_p != nullptr ? rows : 0;
+        now.tokens += rows;
+        now.logprobs += now.logprobs != nullptr ? rows : 0;
+    }
     return hipGetLastError();
 }
 

@@ -186,6 +186,17 @@ def test_many_rows():
         check(x, u, t, k=rng.integers(1, 100, rows), p=rng.uniform(0.5, 1.0, rows), m=rng.uniform(0, 0.1, rows))
 
 
+def test_one_workspace_for_calls_of_all_sizes():
+    """Calls of different numbers of rows and tokens one after the other, and more rows than a launch takes."""
+    for rows, vocab in ((3, 40000), (700, 600), (1, 9000), (40, 70001), (300, 1000), (20_000, 33), (5, 40000)):
+        print(f"rows={rows} vocab={vocab}", flush=True)
+        x = rows_of(rows, vocab, torch.float16, rows + vocab)
+        rng = np.random.default_rng(rows)
+        u, t = rng.random(rows).astype(np.float32), rng.uniform(0.5, 1.2, rows)
+        check(x, u, t)
+        check(x, u, t, k=rng.integers(1, 9, rows), p=rng.uniform(0.5, 1.0, rows))
+
+
 def test_empty():
     f = torch.zeros(0, device=DEV)
     tokens, lps = ps.sample_tokens(torch.zeros(0, 10, device=DEV), f, f)
