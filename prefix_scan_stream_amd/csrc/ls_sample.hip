@@ -42,12 +42,11 @@ constexpr int SM_STEP = 64 * SM_VEC;        // consecutive logits per wave and s
 constexpr int SM_PER_LANE = 8;
 constexpr int SM_SEGS = 64 * SM_PER_LANE;   // most segments of a row
 constexpr int SM_PER_OCTAVE = 8;            // bins per halving of the weight
-constexpr int SM_BINS = 256;
+constexpr int SM_BINS = 512;
 constexpr int SM_RANGES = 256;              // ranges of a refinement
 constexpr int SM_LIST = 4096;               // elements of one bin kept in LDS
 constexpr int SM_SMALL = 512;               // elements that are ordered by counting
 constexpr int SM_ROWS = 16384;              // most rows of a launch (at most 128 blocks each)
-static_assert(SM_BINS == SM_RANGES, "one search for both");
 
 constexpr double LOG2E = 0x1.71547652b82fep+0, LN2 = 0x1.62e42fefa39efp-1;
 constexpr double TO_INT = 0x1.8p52;  // adding it rounds to the nearest integer, into the low word
@@ -157,6 +156,18 @@ struct Raw {
             }
         }
     }
+    __device__ __forceinline__ void unpack(float (&x)[SM_VEC], bool inf) const
+    {
+#pragma unroll
+        for (int k = 0; k < SM_VEC; ++k)
+            x[k] = at(k);
+        if (inf) {
+            asm volatile("");  // a branch: hardly any row comes here
+#pragma unroll
+            for (int k = 0; k < SM_VEC; ++k)
+                x[k] = x[k] == __builtin_inff() ? 0.0f : -__builtin_inff();
+        }
+    }
     __device__ __forceinline__ float at(int k) const
     {
         if constexpr (TYPE == LOGITS_F32)
@@ -168,15 +179,11 @@ struct Raw {
     }
 };
 
-// NaN as -inf; where the row's largest value is +inf (`inf`), its elements are +inf or
-// not: 0 or -inf.
+// Where the row's largest value is +inf (`inf`), its elements are +inf or not: 0 or -inf.  NaN
+// stays: it fails every comparison with a bound, and as a weight counts as far below.
 __device__ __forceinline__ float clean(float x, bool inf)
 {
-    constexpr float INF = __builtin_inff();
-    x = x == x ? x : -INF;
-    if (inf)
-        x = x == INF ? 0.0f : -INF;
-    return x;
+    return inf ? (x == __builtin_inff() ? 0.0f : -__builtin_inff()) : x;
 }
 
 // One past the last kept element in the order: kept are keys above `key`, and equal
@@ -226,7 +233,7 @@ struct Row {
         const uint32_t b = uint32_t(__builtin_bit_cast(uint64_t, __builtin_fma(d, c * -double(SM_PER_OCTAVE), TO_INT)));
         return b < SM_BINS - 1 ? b : SM_BINS - 1;
     }
-    // a weight in bin b as an integer of 2^-frac of the bin's octave; below 2^(frac + 1/16)
+    // a weight in bin b as an integer of 2^-frac of the bin's octave, and back
     __device__ __forceinline__ uint64_t fixed(double d, uint32_t b) const
     {
         const double w = exp2_fast(d, c, int(b / SM_PER_OCTAVE) + frac) + 0x1p52;
@@ -259,9 +266,7 @@ struct Row {
                 const int at = s + u * stride;
                 if (at < end) {
                     float x[SM_VEC];
-#pragma unroll
-                    for (int k = 0; k < SM_VEC; ++k)
-                        x[k] = clean(raw[u].at(k), inf);
+                    raw[u].unpack(x, inf);
                     f(x, uint32_t(at) * SM_STEP + uint32_t(lane * SM_VEC));
                 }
                 __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
@@ -497,12 +502,11 @@ struct Tops {
 // temperature asks for it.  True when the row is done.
 template <int TYPE>
 __device__ __forceinline__ bool settle(const SampleCall& call, const SampleGrid& g, int64_t r, Row<TYPE>& row,
-                                       const Tops& tops, float top, bool writes)
+                                       const Tops& tops, float top)
 {
     row.set_top(top);
     if (top == -__builtin_inff()) {
-        if (writes)
-            write_result(call, r, -1, -double(__builtin_inff()));
+        write_result(call, r, -1, -double(__builtin_inff()));
         return true;
     }
     const float t = call.temperature[r];
@@ -510,8 +514,6 @@ __device__ __forceinline__ bool settle(const SampleCall& call, const SampleGrid&
         row.set_temperature(t);
         return false;
     }
-    if (!writes)
-        return true;
     uint32_t seg = ~0u;
 #pragma unroll
     for (int k = SM_PER_LANE - 1; k >= 0; --k)
@@ -531,8 +533,37 @@ __device__ __forceinline__ bool settle(const SampleCall& call, const SampleGrid&
 }
 
 // ---------------------------------------------------------------- no cuts
-// Waves work for themselves; the one that finishes a row last finds its token.  Bound by the
-// logits' bytes in float32 and by the multiply-adds (about 20 a logit) in 16 bits.
+// A segment's weights, relative to its own largest value `top`: two passes over its steps.
+// For greedy rows only `top` is found.
+template <int TYPE>
+__device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int s1, bool sums, double c, double far,
+                                              float& top)
+{
+    float m = -__builtin_inff();
+    row.template for_steps<4>(s0, s1, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+#pragma unroll
+        for (int k = 0; k < SM_VEC; ++k)
+            m = x[k] > m ? x[k] : m;
+    });
+    top = read_lane(wave_inclusive_scan<MaxF32>(m), 63);
+    if (!sums || top == -__builtin_inff())
+        return 0.0;
+    double sum = 0.0;
+    row.template for_steps<1>(s0, s1, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+#pragma unroll
+        for (int k = 0; k < SM_VEC; ++k) {
+            const float y = clean(x[k], top == __builtin_inff());
+            sum += exp2_fast(__builtin_fmax(double(y) - double(clean(top, top == __builtin_inff())), far), c);
+        }
+    });
+    return sum;
+}
+
+// Waves work for themselves; the one that finishes a row last finds its token.  A double
+// reaches from 2^-1000 to 2^1000, so a wave's weights can be taken relative to the largest
+// value of its first loads, whatever comes later: a sum that leaves 2^-800 .. 2^800 is made
+// again with the segment's own largest value.  Bound by the logits' bytes in float32 and by
+// the multiply-adds (about 19 a logit) in 16 bits.
 template <int TYPE>
 __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall call, SampleGrid g)
 {
@@ -546,60 +577,52 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
     const float t = call.temperature[r];
     const bool sums = t > 0.0f;
     const double c = uniform(LOG2E / finite_temperature(t)), far = uniform(-1000.0 * finite_temperature(t) / LOG2E);
+    float ref = NEG;
     for (int i = 0; i < g.per_wave; ++i) {
         const int seg = (part * WAVES + wave) * g.per_wave + i;
         if (seg >= g.segs)
             break;
         const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
-        float top = NEG;
         double sum = 0.0;
-        for (int s = s0; s < s1; s += U) {
-            Raw<TYPE> raw[U];
+        if (sums) {
+            for (int s = s0; s < s1; s += U) {
+                Raw<TYPE> raw[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (s + u < s1)
-                    raw[u].load(row.p, int64_t(s + u) * SM_STEP + lane * SM_VEC, row.vocab);
-                else
-                    raw[u].clear();
-            }
-            float m = top;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < SM_VEC; ++k) {
-                    const float x = raw[u].at(k);
-                    m = x > m ? x : m;
+                for (int u = 0; u < U; ++u) {
+                    if (s + u < s1)
+                        raw[u].load(row.p, int64_t(s + u) * SM_STEP + lane * SM_VEC, row.vocab);
+                    else
+                        raw[u].clear();
                 }
-            m = read_lane(wave_inclusive_scan<MaxF32>(m), 63);
-            if (m == NEG || !sums) {  // nothing yet, or only the largest is asked for
-                top = m;
-                continue;
-            }
-            // the running sum changes over to the new largest value
-            const bool inf = m == __builtin_inff();
-            if (m != top)
-                sum = inf || top == NEG ? 0.0 : sum * exp2_exact((double(top) - double(m)) * c);
-            top = m;
-            if (inf) {  // +inf counts 1 each, the rest nothing
-#pragma unroll
-                for (int u = 0; u < U; ++u)
+                if (ref == NEG) {
+                    float m = NEG;
 #pragma unroll
                     for (int k = 0; k < SM_VEC; ++k)
-                        sum += raw[u].at(k) == m ? 1.0 : 0.0;
-                continue;
-            }
-            const double m64 = double(m);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (s + u < s1) {
-#pragma unroll
-                    for (int k = 0; k < SM_VEC; ++k)
-                        sum += exp2_fast(__builtin_fmax(double(raw[u].at(k)) - m64, far), c);
+                        m = raw[0].at(k) > m ? raw[0].at(k) : m;
+                    ref = read_lane(wave_inclusive_scan<MaxF32>(m), 63);
                 }
-                __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
+                if (!(ref < __builtin_inff()) || ref == NEG) {
+                    sum = __builtin_inf();  // no finite value to go by
+                    break;
+                }
+                const double ref64 = double(ref);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (s + u < s1) {
+#pragma unroll
+                        for (int k = 0; k < SM_VEC; ++k) {
+                            const double d = __builtin_fmax(double(raw[u].at(k)) - ref64, far);
+                            sum += exp2_fast(__builtin_fmin(d, -far), c);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
+                }
             }
+            sum = read_lane64(wave_inclusive_sum64(sum), 63);
         }
-        sum = wave_inclusive_sum64(sum);
+        float top = ref;
+        if (!(sum > 0x1p-800 && sum < 0x1p800))
+            sum = read_lane64(wave_inclusive_sum64(careful_sum(row, s0, s1, sums, c, far, top)), 63);
         if (lane == 63) {
             put(&g.tops[r * g.segs + seg], top);
             put(&g.sums[r * g.segs + seg], sum);
@@ -614,7 +637,7 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
 
     Tops tops;
     const float top = tops.load(g, r);
-    if (settle(call, g, r, row, tops, top, true))
+    if (settle(call, g, r, row, tops, top))
         return;
     double v[SM_PER_LANE], incl, total, before = 0.0;
 #pragma unroll
@@ -637,8 +660,9 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
 // ---------------------------------------------------------------- cuts
 struct SharedCuts {
     SharedSums s;
-    uint64_t mass[SM_WAVES][SM_BINS];  // weight by bin of each sixteenth of the row, in units of the bin's octave
-    uint64_t bin_mass[SM_BINS];        // of all
+    uint64_t mass[SM_WAVES][SM_BINS];  // weight by bin of each sixteenth of the row, in 2^-frac of the bin's own
+    double bin_weight[SM_BINS];        // that unit
+    double bin_mass[SM_BINS];          // weight of the whole row
     uint32_t bin_count[SM_BINS];
     uint64_t range_mass[SM_RANGES];
     uint32_t range_count[SM_RANGES];
@@ -647,19 +671,34 @@ struct SharedCuts {
     double weight[SM_SMALL];
     double part_sum[SM_WAVES];
     uint64_t part_mass[SM_WAVES];
-    uint32_t n_list, n_small;
-    uint16_t segs[SM_WAVES][SM_SEGS / SM_WAVES];  // each wave's segments with candidates
+    uint32_t n_list, n_small, n_segs, keep;
+    float top, low;
+    double kept;
+    uint16_t segs[SM_SEGS];  // the segments with candidates
 };
 
-// Counts `mine` lanes' flagged elements into a shared counter, one addition for the wave:
-// the place of this lane's first.
-__device__ __forceinline__ uint32_t wave_append(uint32_t* counter, uint32_t mine)
+// write(place, x[k], k) for each element that a lane flags in `in`, places counted on from a
+// shared counter by one addition for the wave.
+template <class F>
+__device__ __forceinline__ void wave_append(uint32_t* counter, uint32_t in, const float (&x)[SM_VEC], F write)
 {
-    const uint32_t incl = wave_inclusive_scan<SumU32>(mine), all = read_lane(incl, 63);
-    uint32_t base = 0;
-    if (lane_id() == 0)
-        base = atomicAdd(counter, all);
-    return uniform(base) + incl - mine;
+    if (__ballot(in != 0) == 0)
+        return;
+    const uint32_t mine = uint32_t(__builtin_popcount(in));
+    const uint32_t incl = wave_inclusive_scan<SumU32>(mine);
+    uint32_t at = 0;
+    if (lane_id() == 63)
+        at = atomicAdd(counter, incl);
+    at = read_lane(at, 63) + incl - mine;
+    while (in != 0) {
+        const uint32_t k = uint32_t(__builtin_ctz(in));
+        in &= in - 1;
+        float v = x[0];
+#pragma unroll
+        for (uint32_t j = 1; j < SM_VEC; ++j)
+            v = k == j ? x[j] : v;
+        write(at++, v, k);
+    }
 }
 
 // Orders the n <= SM_SMALL distinct places of `small` into `sorted`: each place's rank is the
@@ -682,30 +721,26 @@ __device__ __forceinline__ void order_small(SharedCuts& sh, uint32_t n)
     __syncthreads();
 }
 
-// One wave (all of them alike): the first of 256 bins or ranges at which the running count
+// One wave (all of them alike): the first of 64 N bins or ranges at which the running count
 // reaches `want` (by_count) or the running weight `goal`, the last one that holds anything
 // if none does.  above_count and above become what lies before it, `n` what it holds.
-template <class W>
-__device__ __forceinline__ uint32_t pick(const uint32_t* counts, const uint64_t* masses, W weight_of, bool by_count,
-                                         uint32_t want, double goal, uint32_t& above_count, double& above,
-                                         double& total, uint32_t& n)
+template <int N, class W>
+__device__ __forceinline__ uint32_t pick(const uint32_t* counts, W weight_of, bool by_count, uint32_t want,
+                                         double goal, uint32_t& above_count, double& above, uint32_t& n)
 {
-    constexpr int N = SM_BINS / 64;
     const int first = lane_id() * N;
     uint32_t c[N], cs = 0;
     double m[N], ms = 0.0;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         c[k] = counts[first + k];
-        m[k] = weight_of(masses[first + k], uint32_t(first + k));
+        m[k] = weight_of(uint32_t(first + k));
         cs += c[k];
         ms += m[k];
     }
-    const uint32_t c_incl = wave_inclusive_scan<SumU32>(cs);
-    const double m_incl = wave_inclusive_sum64(ms);
-    total = read_lane64(m_incl, 63);
-    uint32_t cr = above_count + c_incl - cs, hit_c = 0, last_c = 0, hit_n = 0, last_n = 0;
-    double mr = above + (m_incl - ms), hit_m = 0.0, last_m = 0.0;
+    uint32_t cr = above_count + wave_shift_up<SumU32>(wave_inclusive_scan<SumU32>(cs));
+    uint32_t hit_c = 0, last_c = 0, hit_n = 0, last_n = 0;
+    double mr = above + dpp_move64<DPP_WAVE_SHR1, 0xf>(wave_inclusive_sum64(ms)), hit_m = 0.0, last_m = 0.0;
     int hit = -1, last = -1;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -792,11 +827,11 @@ __device__ __forceinline__ uint32_t index_at(const Row<TYPE>& row, uint64_t plac
     return uint32_t(place) & ((1u << row.index_bits) - 1u);
 }
 
-// Collects the places in [lo, hi] of a bin's elements into the list; their number (the list
-// holds SM_LIST).
+// Collects a bin's elements, `all` or those with a place in [lo, hi], into the list; their
+// number (the list holds SM_LIST).
 template <int TYPE>
-__device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, uint64_t lo,
-                                            uint64_t hi)
+__device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, bool all,
+                                            uint64_t lo, uint64_t hi)
 {
     const float x_lo = value_of(bin.key_lo), x_hi = value_of(bin.key_hi);
     __syncthreads();
@@ -808,24 +843,18 @@ __device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh
 #pragma unroll
         for (int k = 0; k < SM_VEC; ++k)
             in |= x[k] >= x_lo && x[k] <= x_hi ? 1u << k : 0u;
-        if (__ballot(in != 0) == 0)
-            return;
-        uint64_t v[SM_VEC];
+        if (!all) {
 #pragma unroll
-        for (int k = 0; k < SM_VEC; ++k) {
-            v[k] = place_of(row, bin.key_hi, key_of(x[k]), idx + k);
-            if (v[k] < lo || v[k] > hi)
-                in &= ~(1u << k);
-        }
-        uint32_t at = wave_append(&sh.n_list, uint32_t(__builtin_popcount(in)));
-#pragma unroll
-        for (int k = 0; k < SM_VEC; ++k) {
-            if (in >> k & 1u) {
-                if (at < SM_LIST)
-                    sh.list[at] = v[k];
-                ++at;
+            for (int k = 0; k < SM_VEC; ++k) {
+                const uint64_t v = place_of(row, bin.key_hi, key_of(x[k]), idx + k);
+                if (v < lo || v > hi)
+                    in &= ~(1u << k);
             }
         }
+        wave_append(&sh.n_list, in, x, [&](uint32_t at, float v, uint32_t k) {
+            if (at < SM_LIST)
+                sh.list[at] = place_of(row, bin.key_hi, key_of(v), idx + k);
+        });
     });
     __syncthreads();
     return uniform(sh.n_list);
@@ -844,7 +873,7 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
 {
     const uint32_t tid = threadIdx.x;
     uint64_t lo = 0, hi = place_of(row, bin.key_hi, bin.key_lo, (1u << row.index_bits) - 1u);
-    uint32_t n = collect(row, sh, bin, lo, hi);
+    uint32_t n = collect(row, sh, bin, true, lo, hi);
     listed = n <= SM_LIST;
     bool in_list = listed;
     while (n > SM_SMALL) {
@@ -883,16 +912,15 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
             });
         }
         __syncthreads();
-        double total;
-        const uint32_t b = pick(
-            sh.range_count, sh.range_mass, [&](uint64_t m, uint32_t) { return row.unfixed(m, bin.bin); }, by_count,
-            want, goal, above_count, above, total, n);
+        const uint32_t b = pick<SM_RANGES / 64>(
+            sh.range_count, [&](uint32_t i) { return row.unfixed(sh.range_mass[i], bin.bin); }, by_count, want, goal,
+            above_count, above, n);
         lo += uint64_t(b) << shift;
         const uint64_t last = lo + ((uint64_t(1) << shift) - 1);
         hi = hi < last ? hi : last;
         __syncthreads();
         if (!in_list && n <= SM_LIST) {
-            collect(row, sh, bin, lo, hi);
+            collect(row, sh, bin, false, lo, hi);
             in_list = true;
         }
     }
@@ -926,10 +954,44 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
     return place;
 }
 
+// The histogram of one wave's share of a row.  A weight is the weight 2^(-b/8) of its bin
+// times 2^(z/8), |z| <= 1/2, and the bin counts the second factor in units of 2^-frac: a
+// polynomial of degree 6 (relative error 2^-48.9) into whose last step the rounding to an
+// integer is folded, with no exponent to insert.  Below 2^-63.8 everything is in the last bin and
+// counts as its weight, less than 2^-46 of the sum for a row of 2^17.
+template <bool COUNTS, int TYPE>
+__device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, uint32_t* count, int first, int end)
+{
+    const double one = __builtin_ldexp(1.0, row.frac);
+    const double c8 = uniform(row.c * SM_PER_OCTAVE), c0 = uniform(one + 0x1p52);
+    const double c1 = uniform(one * 0x1.62e42fefa3aefp-4), c2 = uniform(one * 0x1.ebfbdff82c5e7p-9);
+    const double c3 = uniform(one * 0x1.c6b08d5e4bb3bp-14), c4 = uniform(one * 0x1.3b2ab6f5687a9p-19);
+    const double c5 = uniform(one * 0x1.5d8dfde822453p-25), c6 = uniform(one * 0x1.430d3b3f37695p-31);
+    row.template for_steps<2>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+#pragma unroll
+        for (int j = 0; j < SM_VEC; ++j) {
+            const double d = row.below(x[j]);
+            const double t = __builtin_fma(d, -c8, TO_INT);
+            const double z = __builtin_fma(d, c8, t - TO_INT);
+            double w = __builtin_fma(c6, z, c5);
+            w = __builtin_fma(w, z, c4);
+            w = __builtin_fma(w, z, c3);
+            w = __builtin_fma(w, z, c2);
+            w = __builtin_fma(w, z, c1);
+            w = __builtin_fma(w, z, c0);
+            const uint32_t n = uint32_t(__builtin_bit_cast(uint64_t, t)), b = n < SM_BINS - 1 ? n : SM_BINS - 1;
+            atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
+                      static_cast<unsigned long long>(__builtin_bit_cast(uint64_t, w) & ((uint64_t(1) << 52) - 1)));
+            if (COUNTS && x[j] > -__builtin_inff())
+                atomicAdd(&count[b], 1u);
+        }
+    });
+}
+
 // The cuts of a row that are not settled by a few candidates: a histogram of weights (and
 // counts, for top-k) by log2 w, eight bins to the octave, tells which bin the cut lies in,
 // and only that bin's elements are collected and ordered.  Weights are added to bins as
-// integers of the bin's octave, so that sums do not depend on the order of the atomics.
+// integers, so that sums do not depend on the order of the atomics.
 // Each wave takes a sixteenth of the row and keeps its own bins: with the cut known, the
 // kept weight of each sixteenth is known too, and only the one with the token is read
 // for the running sums.
@@ -947,40 +1009,38 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
     if (by_k || by_p) {
         for (int i = lane; i < SM_BINS; i += 64)
             sh.mass[wave][i] = 0;
-        if (tid < SM_BINS)
+        if (tid < SM_BINS) {
             sh.bin_count[tid] = 0;
+            sh.bin_weight[tid] = exp2_exact(-double(tid) / SM_PER_OCTAVE - double(row.frac));
+        }
         if (tid < SM_WAVES)
             sh.part_mass[tid] = 0;
         __syncthreads();
         const int first = wave * share, end = first + share < row.steps ? first + share : row.steps;
-        uint64_t* mass = sh.mass[wave];
-        row.template for_steps<2>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
-#pragma unroll
-            for (int j = 0; j < SM_VEC; ++j) {
-                const double d = row.below(x[j]);
-                const uint32_t b = row.bin(d);
-                atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
-                          static_cast<unsigned long long>(row.fixed(d, b)));
-                if (by_k && x[j] != -__builtin_inff())
-                    atomicAdd(&sh.bin_count[b], 1u);
-            }
-        });
+        if (by_k)
+            fill_bins<true>(row, sh.mass[wave], sh.bin_count, first, end);
+        else
+            fill_bins<false>(row, sh.mass[wave], sh.bin_count, first, end);
         __syncthreads();
         if (tid < SM_BINS) {
             uint64_t m = 0;
 #pragma unroll
             for (int w = 0; w < SM_WAVES; ++w)
                 m += sh.mass[w][tid];
-            sh.bin_mass[tid] = m;
+            sh.bin_mass[tid] = double(m) * sh.bin_weight[tid];
             if (!by_k)
                 sh.bin_count[tid] = m != 0 ? 1u : 0u;
         }
         __syncthreads();
-        const auto in_bin = [&](uint64_t m, uint32_t b) { return row.unfixed(m, b); };
-        uint32_t above_count = 0, n;
-        double above = 0.0, total;
-        uint32_t b = pick(sh.bin_count, sh.bin_mass, in_bin, by_k, k, p * 0.0, above_count, above, total, n);
-        double kept = total;
+        constexpr int N = SM_BINS / 64;
+        const auto in_bin = [&](uint32_t b) { return sh.bin_mass[b]; };
+        uint32_t above_count = 0, n = 0, b = 0;
+        double above = 0.0, kept = 0.0;
+        for (int i = 0; i < N; ++i)
+            kept += sh.bin_mass[lane * N + i];
+        kept = read_lane64(wave_inclusive_sum64(kept), 63);
+        if (by_k)
+            b = pick<N>(sh.bin_count, in_bin, true, k, 0.0, above_count, above, n);
         if (by_k && above_count + n >= k) {
             bin = make_bin(row, b);
             place = cut_in_bin(row, sh, bin, true, k, 0.0, above_count, above, kept, in_parts);
@@ -993,7 +1053,7 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
             const Cut k_cut = cut;
             above_count = 0;
             above = 0.0;
-            b = pick(sh.bin_count, sh.bin_mass, in_bin, false, 0, goal, above_count, above, total, n);
+            b = pick<N>(sh.bin_count, in_bin, false, 0, goal, above_count, above, n);
             bin = make_bin(row, b);
             double weight;
             place = cut_in_bin(row, sh, bin, false, 0, goal, 0, above, weight, in_parts);
@@ -1025,7 +1085,7 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
         }
         double sum = 0.0;
         for (uint32_t b = lane; b < bin.bin; b += 64)
-            sum += row.unfixed(sh.mass[wave][b], b);
+            sum += double(sh.mass[wave][b]) * sh.bin_weight[b];
         sum = wave_inclusive_sum64(sum);
         if (lane == 63)
             sh.part_sum[wave] = sum;
@@ -1064,32 +1124,32 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
         write_token(call, r, row, token, total);
 }
 
-// Rows whose cut lies within a few candidates: at least the k largest elements (few), or all
-// that min-p may keep.  False when they are more than SM_SMALL.
+// One wave: where the candidates of a row begin.  few: at most the k-th largest logit, which is the
+// k-th largest of the segments' largest values to 16 bits of its key; else a little below the
+// smallest logit that min-p may keep.  The segments with candidates go into sh.segs.
 template <int TYPE>
-__device__ __forceinline__ bool cut_candidates(const SampleCall& call, const SampleGrid& g, int64_t r,
-                                               const Row<TYPE>& row, SharedCuts& sh, const Tops& tops, bool few,
-                                               uint32_t k, double p, double least, double u)
+__device__ __forceinline__ void find_segments(const SampleGrid& g, const Row<TYPE>& row, SharedCuts& sh,
+                                              const Tops& tops, bool few, uint32_t k, double least)
 {
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    if (tid == 0)
-        sh.n_small = 0, sh.s.found = ~0u, sh.s.last = 0;
-    __syncthreads();
-    // every wave for itself up to the reading of the segments
     float low;
     if (few) {
-        // the k-th largest of the segments' largest values, to 16 bits of its key
         uint32_t key[SM_PER_LANE], at = 0;
 #pragma unroll
         for (int j = 0; j < SM_PER_LANE; ++j)
             key[j] = key_of(clean(tops.v[j], row.inf)) >> 16;
-        const auto narrow = [&](auto lanes) {
-            for (uint32_t bit = 1u << 15; bit != 0; bit >>= 1) {
-                uint32_t n = 0;
+        const auto count = [&](auto lanes, uint32_t v) {
+            uint32_t n = 0;
 #pragma unroll
-                for (int j = 0; j < decltype(lanes)::value; ++j)
-                    n += uint32_t(__builtin_popcountll(__ballot(key[j] >= (at | bit))));
-                at = n >= k ? at | bit : at;
+            for (int j = 0; j < decltype(lanes)::value; ++j)
+                n += uint32_t(__builtin_popcountll(__ballot(key[j] >= v)));
+            return n;
+        };
+        // two bits of the key at a time: the three counts do not wait for each other
+        const auto narrow = [&](auto lanes) {
+            for (int bit = 14; bit >= 0; bit -= 2) {
+                const uint32_t a = at | 1u << bit, b = at | 2u << bit, c = at | 3u << bit;
+                const uint32_t na = count(lanes, a), nb = count(lanes, b), nc = count(lanes, c);
+                at = nc >= k ? c : nb >= k ? b : na >= k ? a : at;
             }
         };
         if (tops.per_lane <= 4)
@@ -1099,7 +1159,6 @@ __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const Sam
         const uint32_t lowest = at << 16;
         low = value_of(lowest > KEY_NEG_INF ? lowest : KEY_NEG_INF + 1);
     } else {
-        // a little below the smallest logit that min-p may keep
         const double x = double(row.top) + ::log(least) * LOG2E / row.c;
         low = float(x - 1e-6 * (__builtin_fabs(x) + __builtin_fabs(double(row.top))) - 1e-30);
         low = low > -__builtin_inff() ? low : value_of(KEY_NEG_INF + 1);
@@ -1109,91 +1168,104 @@ __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const Sam
     for (int j = 0; j < SM_PER_LANE; ++j)
         flags |= clean(tops.v[j], row.inf) >= low ? 1u << j : 0u;
     const uint32_t mine = uint32_t(__builtin_popcount(flags));
-    const uint32_t incl = wave_inclusive_scan<SumU32>(mine), n_segs = read_lane(incl, 63);
-    if (n_segs > SM_SMALL)
-        return false;
+    const uint32_t incl = wave_inclusive_scan<SumU32>(mine);
     uint32_t q = incl - mine;
-#pragma unroll
-    for (int j = 0; j < SM_PER_LANE; ++j) {
-        if (flags >> j & 1u) {
-            if ((q & (SM_WAVES - 1)) == wave)
-                sh.segs[wave][q / SM_WAVES] = uint16_t(tops.seg(j));
-            ++q;
-        }
-    }
-    __builtin_amdgcn_wave_barrier();
+    for (; flags != 0; flags &= flags - 1)
+        sh.segs[q++] = uint16_t(tops.seg(__builtin_ctz(flags)));
+    if (lane_id() == 63)
+        sh.n_segs = incl;
+    sh.low = low;
+}
+
+// Rows whose cut lies within a few candidates (find_segments).  False when they are more
+// than SM_SMALL.
+template <int TYPE>
+__device__ __forceinline__ bool cut_candidates(const SampleCall& call, const SampleGrid& g, int64_t r,
+                                               const Row<TYPE>& row, SharedCuts& sh, uint32_t k, double p,
+                                               double least, double u)
+{
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(int(tid >> 6));
+    const float low = uniform(sh.low);
     const uint32_t key_hi = key_of(row.top);
-    constexpr int U = TYPE == LOGITS_F32 ? 2 : 4;
-    const int todo = int((n_segs + SM_WAVES - 1 - wave) / SM_WAVES) * g.seg_steps;  // this wave's steps
-    for (int i = 0; i < todo; i += U) {
+    constexpr int U = 4;
+    const int todo = int(uniform(sh.n_segs)) * g.seg_steps;
+    for (int i = wave; i < todo; i += U * SM_WAVES) {
         Raw<TYPE> raw[U];
         int step[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
+            const int q = i + j * SM_WAVES;
             step[j] = g.steps;
-            if (i + j < todo) {
-                const int s = (i + j) / g.seg_steps;
-                step[j] = uniform(int(sh.segs[wave][s])) * g.seg_steps + (i + j - s * g.seg_steps);
+            if (q < todo) {
+                const int seg = g.seg_steps == 1 ? q : q / g.seg_steps;
+                step[j] = uniform(int(sh.segs[seg])) * g.seg_steps + (q - seg * g.seg_steps);
             }
             if (step[j] < g.steps)
                 raw[j].load(row.p, int64_t(step[j]) * SM_STEP + lane * SM_VEC, row.vocab);
             else
                 raw[j].clear();
         }
-        uint32_t in = 0;
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-            for (int m = 0; m < SM_VEC; ++m)
-                in |= clean(raw[j].at(m), row.inf) >= low ? 1u << (j * SM_VEC + m) : 0u;
-        uint32_t at = wave_append(&sh.n_small, uint32_t(__builtin_popcount(in)));
-#pragma unroll
-        for (int j = 0; j < U; ++j)
+        for (int j = 0; j < U; ++j) {
+            float x[SM_VEC];
+            raw[j].unpack(x, row.inf);
+            uint32_t in = 0;
 #pragma unroll
             for (int m = 0; m < SM_VEC; ++m)
-                if (in >> (j * SM_VEC + m) & 1u) {
-                    if (at < SM_SMALL)
-                        sh.small[at] = place_of(row, key_hi, key_of(clean(raw[j].at(m), row.inf)),
-                                                uint32_t(step[j]) * SM_STEP + lane * SM_VEC + uint32_t(m));
-                    ++at;
-                }
+                in |= x[m] >= low ? 1u << m : 0u;
+            wave_append(&sh.n_small, in, x, [&](uint32_t at, float v, uint32_t m) {
+                if (at < SM_SMALL)
+                    sh.small[at] =
+                        place_of(row, key_hi, key_of(v), uint32_t(step[j]) * SM_STEP + lane * SM_VEC + m);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
     __syncthreads();
     const uint32_t n = uniform(sh.n_small);
     if (n > SM_SMALL)
         return false;
     order_small(sh, n);
-    // Every wave for itself, 64 of the order at a time: the kept ones are its first `keep`, of weight `total`.
-    uint32_t keep = k < n ? k : n;
-    double total = 0.0;
-    if (p < 1.0) {
-        double sum = 0.0;
-        for (uint32_t i = lane; i < keep; i += 64)
-            sum += row.weight(value_of(key_at(row, key_hi, sh.sorted[i])));
-        const double goal = p * read_lane64(wave_inclusive_sum64(sum), 63);
+    // one wave, 64 of the order at a time: the kept ones are its first `keep`, of weight `total`
+    if (wave == 0) {
+        uint32_t keep = k < n ? k : n;
+        double total = 0.0;
         for (uint32_t i = 0; i < keep; i += 64) {
             const uint32_t at = i + lane;
             const double w = at < keep ? row.weight(value_of(key_at(row, key_hi, sh.sorted[at]))) : 0.0;
-            const double up = total + wave_inclusive_sum64(w);
-            const uint64_t hits = __ballot(at < keep && up >= goal);
-            if (hits != 0)
-                keep = i + uint32_t(__builtin_ctzll(hits)) + 1u;
-            total = read_lane64(up, 63);
+            if (at < keep)
+                sh.weight[at] = w;
+            total += w;
+        }
+        if (p < 1.0) {
+            const double goal = p * read_lane64(wave_inclusive_sum64(total), 63);
+            double run = 0.0;
+            for (uint32_t i = 0; i < keep; i += 64) {
+                const uint32_t at = i + lane;
+                const double up = run + wave_inclusive_sum64(at < keep ? sh.weight[at] : 0.0);
+                const uint64_t hits = __ballot(at < keep && up >= goal);
+                if (hits != 0)
+                    keep = i + uint32_t(__builtin_ctzll(hits)) + 1u;
+                run = read_lane64(up, 63);
+            }
         }
         total = 0.0;
-    }
-    for (uint32_t i = 0; i < keep; i += 64) {
-        const uint32_t at = i + lane;
-        const double w = at < keep ? row.weight(value_of(key_at(row, key_hi, sh.sorted[at]))) : 0.0;
-        const uint64_t drops = __ballot(at > 0 && at < keep && !(w >= least));
-        if (drops != 0)
-            keep = i + uint32_t(__builtin_ctzll(drops));
-        if (at < keep && wave == 0)
-            sh.weight[at] = w;
-        total += read_lane64(wave_inclusive_sum64(at < keep ? w : 0.0), 63);
+        for (uint32_t i = 0; i < keep; i += 64) {
+            const uint32_t at = i + lane;
+            const double w = at < keep ? sh.weight[at] : 0.0;
+            const uint64_t drops = __ballot(at > 0 && at < keep && !(w >= least));
+            if (drops != 0)
+                keep = i + uint32_t(__builtin_ctzll(drops));
+            total += at < keep ? w : 0.0;
+        }
+        sh.keep = keep;
+        sh.kept = read_lane64(wave_inclusive_sum64(total), 63);
     }
     __syncthreads();
     // running sums in index order, each by a group of lanes
+    const uint32_t keep = uniform(sh.keep);
+    const double total = uniform(sh.kept);
     uint32_t group = 64;
     while (group > 1 && SM_BLOCK / group < keep)
         group >>= 1;
@@ -1268,30 +1340,38 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
     if (uniform(sh.s.arrived) == 0u)
         return;
 
-    Tops tops;
-    const float top = tops.load(g, r);
-    if (settle(call, g, r, row, tops, top, wave == 0))
-        return;
     uint32_t k = ~0u;
     if (call.top_k != nullptr && call.top_k[r] > 0)
         k = uint32_t(call.top_k[r]);
     double p = 1.0;
     if (call.top_p != nullptr) {
         p = double(call.top_p[r]);
-        p = p > 0.0 ? p : 0.0;
+        p = uniform(p > 0.0 ? p : 0.0);
     }
     double least = 0.0;
     if (call.min_p != nullptr && call.min_p[r] > 0.0f)
-        least = __builtin_fmin(double(call.min_p[r]), 1.0);
+        least = uniform(__builtin_fmin(double(call.min_p[r]), 1.0));
     const double u = uniform(double(call.uniforms[r]));
     // few enough that the k-th largest of the segments' values leaves few candidates
     const bool few = uint64_t(k) * 4 <= uint64_t(g.segs) * 3;
-    bool done = false;
-    p = uniform(p);
-    least = uniform(least);
-    if (few || (p >= 1.0 && least > 0.0))
-        done = cut_candidates(call, g, r, row, sh, tops, few, k, p, least, u);
-    if (!done)
+    const bool candidates = few || (p >= 1.0 && least > 0.0);
+    // one wave (the others would only take its turns), then all
+    if (wave == 0) {
+        Tops tops;
+        const float top = tops.load(g, r);
+        const bool done = settle(call, g, r, row, tops, top);
+        sh.n_small = 0, sh.s.found = ~0u, sh.s.last = 0;
+        sh.s.arrived = done ? 0u : 1u;
+        sh.top = top;
+        if (!done && candidates)
+            find_segments(g, row, sh, tops, few, k, least);
+    }
+    __syncthreads();
+    if (uniform(sh.s.arrived) == 0u)
+        return;
+    row.set_top(uniform(sh.top));
+    row.set_temperature(call.temperature[r]);
+    if (!(candidates && cut_candidates(call, g, r, row, sh, k, p, least, u)))
         cut_row(call, r, row, sh, k, p, least, u);
 }
 
