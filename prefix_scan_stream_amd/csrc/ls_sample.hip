@@ -34,6 +34,22 @@
 
 namespace ls {
 
+#ifndef LS_PW
+#define LS_PW 4
+#endif
+#ifndef LS_U32
+#define LS_U32 2
+#endif
+#ifndef LS_U16
+#define LS_U16 4
+#endif
+#ifndef LS_UC
+#define LS_UC 2
+#endif
+#ifndef LS_UB
+#define LS_UB 2
+#endif
+
 constexpr int SM_BLOCK = 1024;              // threads of a block that makes cuts
 constexpr int SM_WAVES = SM_BLOCK / 64;
 constexpr int SM_ALL_BLOCK = 256;           // without cuts
@@ -45,7 +61,9 @@ constexpr int SM_PER_OCTAVE = 8;            // bins per halving of the weight
 constexpr int SM_BINS = 512;
 constexpr int SM_RANGES = 256;              // ranges of a refinement
 constexpr int SM_LIST = 4096;               // elements of one bin kept in LDS
+constexpr int SM_NOTES = 256;               // loads of one wave that hold such elements
 constexpr int SM_SMALL = 512;               // elements that are ordered by counting
+constexpr int SM_CUS = 256;
 constexpr int SM_ROWS = 16384;              // most rows of a launch (at most 128 blocks each)
 
 constexpr double LOG2E = 0x1.71547652b82fep+0, LN2 = 0x1.62e42fefa39efp-1;
@@ -72,9 +90,12 @@ __device__ __forceinline__ double exp2_poly(double f)
 __device__ __forceinline__ double exp2_fast(double d, double c, int e = 0)
 {
     const double t = __builtin_fma(d, c, TO_INT);
-    const uint64_t b = __builtin_bit_cast(uint64_t, exp2_poly(__builtin_fma(d, c, TO_INT - t)));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 p = __builtin_bit_cast(u32x2, exp2_poly(__builtin_fma(d, c, TO_INT - t)));
     const uint32_t n = uint32_t(__builtin_bit_cast(uint64_t, t)) + uint32_t(e);
-    return __builtin_bit_cast(double, (uint64_t(uint32_t(b >> 32) + (n << 20)) << 32) | uint32_t(b));
+    // one instruction, where the compiler made five of a 64-bit addition
+    asm("v_lshl_add_u32 %0, %1, 20, %2" : "=v"(p.y) : "v"(n), "v"(p.y));
+    return __builtin_bit_cast(double, p);
 }
 
 // 2^y for y <= 0 (NaN counts as -inf), 0 below 2^-1074.
@@ -143,16 +164,14 @@ struct Raw {
                     w[k + j] = a[j];
             }
         } else {
-            clear();
+            // the row's end: one element at a time, last first (a loop: this code stands at every load)
+#pragma unroll 1
+            for (int k = SM_VEC - 1; k >= 0; --k) {
+                const uint32_t e = idx + k < vocab ? uint32_t(p[k]) : NEG & (E(~E(0)));
 #pragma unroll
-            for (int k = 0; k < SM_VEC; ++k) {
-                if (idx + k < vocab) {
-                    if constexpr (TYPE == LOGITS_F32)
-                        w[k] = p[k];
-                    else
-                        w[k / 2] = k % 2 ? (w[k / 2] & 0xffffu) | (uint32_t(p[k]) << 16)
-                                         : (w[k / 2] & 0xffff0000u) | p[k];
-                }
+                for (int j = WORDS - 1; j > 0; --j)
+                    w[j] = TYPE == LOGITS_F32 ? w[j - 1] : (w[j] << 16) | (w[j - 1] >> 16);
+                w[0] = TYPE == LOGITS_F32 ? e : (w[0] << 16) | e;
             }
         }
     }
@@ -387,7 +406,7 @@ __device__ __forceinline__ uint32_t find_in_order(const Row<TYPE>& row, SharedSu
         for (int k = 0; k < N; ++k)
             v[k] = sh.sums[lane * N + k];
         wave_sums(v, incl, total);
-        const int s = wave_first_over(v, goal_of(u, total), incl, before, over);
+        const int over_at = wave_first_over(v, goal_of(u, total), incl, before, over), s = over_at < 0 ? 0 : over_at;
         const uint32_t token = wave_find_token(row, s * per, s * per + per < row.steps ? s * per + per : row.steps,
                                                before, goal_of(u, total), f);
         if (lane == 0) {
@@ -462,6 +481,7 @@ template <int TYPE>
 __device__ __forceinline__ void write_token(const SampleCall& call, int64_t r, const Row<TYPE>& row, uint32_t token,
                                             double total)
 {
+    token = token < row.vocab ? token : 0u;  // within the row, whatever the sums were
     if (lane_id() == 0) {
         float x;
         if constexpr (TYPE == LOGITS_F32)
@@ -561,14 +581,15 @@ __device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int 
 
 // Waves work for themselves; the one that finishes a row last finds its token.  A double
 // reaches from 2^-1000 to 2^1000, so a wave's weights can be taken relative to the largest
-// value of its first loads, whatever comes later: a sum that leaves 2^-800 .. 2^800 is made
-// again with the segment's own largest value.  Bound by the logits' bytes in float32 and by
-// the multiply-adds (about 19 a logit) in 16 bits.
+// value of its first loads, whatever comes later: logits are held within 2^+-1000 of it, and a
+// sum that leaves 2^-800 .. 2^800 (as one with NaN in it may) is made again with the
+// segment's own largest value.  Bound by the logits' bytes in float32 and by the
+// multiply-adds (18 instructions a logit) in 16 bits.
 template <int TYPE>
 __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall call, SampleGrid g)
 {
     constexpr float NEG = -__builtin_inff();
-    constexpr int U = 4;
+    constexpr int U = TYPE == LOGITS_F32 ? LS_U32 : LS_U16;
     constexpr int WAVES = SM_ALL_BLOCK / 64;
     const int lane = lane_id(), wave = uniform(int(threadIdx.x >> 6));
     const int64_t r = blockIdx.x % uint32_t(call.rows);
@@ -577,55 +598,80 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
     const float t = call.temperature[r];
     const bool sums = t > 0.0f;
     const double c = uniform(LOG2E / finite_temperature(t)), far = uniform(-1000.0 * finite_temperature(t) / LOG2E);
-    float ref = NEG;
-    for (int i = 0; i < g.per_wave; ++i) {
-        const int seg = (part * WAVES + wave) * g.per_wave + i;
-        if (seg >= g.segs)
-            break;
-        const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
-        double sum = 0.0;
-        if (sums) {
-            for (int s = s0; s < s1; s += U) {
-                Raw<TYPE> raw[U];
+    const int seg0 = (part * WAVES + wave) * g.per_wave;
+    const int seg1 = seg0 + g.per_wave < g.segs ? seg0 + g.per_wave : g.segs;
+    const auto seg_end = [&](int seg) { return (seg + 1) * g.seg_steps < g.steps ? (seg + 1) * g.seg_steps : g.steps; };
+    float ref = NEG, low = 0.0f, high = 0.0f;
+    if (sums && seg0 < seg1) {
+        // U steps at a time, the next ones on their way meanwhile
+        Raw<TYPE> raw[U], next[U];
+        const auto load = [&](Raw<TYPE>(&to)[U], int s, int end) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (s + u < s1)
-                        raw[u].load(row.p, int64_t(s + u) * SM_STEP + lane * SM_VEC, row.vocab);
-                    else
-                        raw[u].clear();
-                }
-                if (ref == NEG) {
-                    float m = NEG;
+            for (int u = 0; u < U; ++u) {
+                if (s + u < end)
+                    to[u].load(row.p, int64_t(s + u) * SM_STEP + lane * SM_VEC, row.vocab);
+                else
+                    to[u].clear();
+            }
+        };
+        int seg = seg0, s = seg0 * g.seg_steps, s1 = seg_end(seg0);
+        double sum = 0.0;
+        load(raw, s, s1);
+        while (true) {
+            const bool ends = s + U >= s1;
+            const int next_seg = ends ? seg + 1 : seg, next_s = ends ? next_seg * g.seg_steps : s + U;
+            const int next_s1 = ends ? seg_end(next_seg) : s1;
+            if (next_seg < seg1)
+                load(next, next_s, next_s1);
+            if (ref == NEG) {
+                float m = NEG;
+#pragma unroll
+                for (int k = 0; k < SM_VEC; ++k)
+                    m = raw[0].at(k) > m ? raw[0].at(k) : m;
+                ref = read_lane(wave_inclusive_scan<MaxF32>(m), 63);
+                low = uniform(float(double(ref) + far));
+                high = uniform(float(double(ref) - far));
+            }
+            // no finite value to go by, or no float near enough to 2^-1000 of it (a very low or high temperature)
+            const double off = (double(low) - double(ref)) * c;
+            if (!(off > -1010.0 && off < -900.0 && double(high) - double(ref) < -1.01 * far))
+                sum = __builtin_inf();
+            const double ref64 = uniform(double(ref));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (s + u < s1) {
 #pragma unroll
                     for (int k = 0; k < SM_VEC; ++k)
-                        m = raw[0].at(k) > m ? raw[0].at(k) : m;
-                    ref = read_lane(wave_inclusive_scan<MaxF32>(m), 63);
+                        sum += exp2_fast(double(__builtin_amdgcn_fmed3f(raw[u].at(k), low, high)) - ref64, c);
                 }
-                if (!(ref < __builtin_inff()) || ref == NEG) {
-                    sum = __builtin_inf();  // no finite value to go by
-                    break;
-                }
-                const double ref64 = double(ref);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (s + u < s1) {
-#pragma unroll
-                        for (int k = 0; k < SM_VEC; ++k) {
-                            const double d = __builtin_fmax(double(raw[u].at(k)) - ref64, far);
-                            sum += exp2_fast(__builtin_fmin(d, -far), c);
-                        }
-                    }
-                    __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
-                }
+                __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
             }
-            sum = read_lane64(wave_inclusive_sum64(sum), 63);
+            if (ends) {
+                sum = read_lane64(wave_inclusive_sum64(sum), 63);
+                float top = ref;
+                if (!(sum > 0x1p-800 && sum < 0x1p800))
+                    sum = read_lane64(wave_inclusive_sum64(careful_sum(row, seg * g.seg_steps, s1, true, c, far, top)), 63);
+                if (lane == 63) {
+                    put(&g.tops[r * g.segs + seg], top);
+                    put(&g.sums[r * g.segs + seg], sum);
+                }
+                sum = 0.0;
+            }
+            if (next_seg >= seg1)
+                break;
+            seg = next_seg;
+            s = next_s;
+            s1 = next_s1;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                raw[u] = next[u];
         }
-        float top = ref;
-        if (!(sum > 0x1p-800 && sum < 0x1p800))
-            sum = read_lane64(wave_inclusive_sum64(careful_sum(row, s0, s1, sums, c, far, top)), 63);
-        if (lane == 63) {
-            put(&g.tops[r * g.segs + seg], top);
-            put(&g.sums[r * g.segs + seg], sum);
+    } else {
+        for (int seg = seg0; seg < seg1; ++seg) {
+            float top;
+            careful_sum(row, seg * g.seg_steps, seg_end(seg), false, c, far, top);
+            if (lane == 63)
+                put(&g.tops[r * g.segs + seg], top);
         }
     }
     stores_done();
@@ -650,7 +696,7 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
     const double goal = goal_of(double(call.uniforms[r]), total);
     bool over;
     const int at = wave_first_over(v, goal, incl, before, over);
-    const int seg = at / SM_PER_LANE * tops.per_lane + at % SM_PER_LANE;
+    const int seg = at < 0 ? 0 : at / SM_PER_LANE * tops.per_lane + at % SM_PER_LANE;
     const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
     const uint32_t token =
         wave_find_token(row, s0, s1, before, goal, [&](float x, uint32_t) { return row.weight(x); });
@@ -658,6 +704,16 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
 }
 
 // ---------------------------------------------------------------- cuts
+struct Bin {
+    uint32_t bin, key_lo, key_hi;
+};
+
+struct Pick {
+    Bin bin;
+    uint32_t above_count, reached;
+    double above, goal;
+};
+
 struct SharedCuts {
     SharedSums s;
     uint64_t mass[SM_WAVES][SM_BINS];  // weight by bin of each sixteenth of the row, in 2^-frac of the bin's own
@@ -666,7 +722,8 @@ struct SharedCuts {
     uint32_t bin_count[SM_BINS];
     uint64_t range_mass[SM_RANGES];
     uint32_t range_count[SM_RANGES];
-    uint64_t list[SM_LIST];    // places in the order: (largest key - key) << index_bits | index
+    uint32_t notes[SM_WAVES][SM_NOTES];  // indexes of loads that hold elements of a bin
+    uint64_t list[SM_LIST];              // their places in the order: (largest key - key) << index_bits | index
     uint64_t small[SM_SMALL], sorted[SM_SMALL];
     double weight[SM_SMALL];
     double part_sum[SM_WAVES];
@@ -674,30 +731,36 @@ struct SharedCuts {
     uint32_t n_list, n_small, n_segs, keep;
     float top, low;
     double kept;
+    Pick pick;
     uint16_t segs[SM_SEGS];  // the segments with candidates
 };
 
-// write(place, x[k], k) for each element that a lane flags in `in`, places counted on from a
-// shared counter by one addition for the wave.
-template <class F>
-__device__ __forceinline__ void wave_append(uint32_t* counter, uint32_t in, const float (&x)[SM_VEC], F write)
+// write(place, x[k], k) for each element with in(x[k], k), places counted on from a shared
+// counter by one addition for the wave.
+template <class P, class F>
+__device__ __forceinline__ void wave_append(uint32_t* counter, const float (&x)[SM_VEC], P in, F write)
 {
-    if (__ballot(in != 0) == 0)
-        return;
-    const uint32_t mine = uint32_t(__builtin_popcount(in));
-    const uint32_t incl = wave_inclusive_scan<SumU32>(mine);
-    uint32_t at = 0;
-    if (lane_id() == 63)
-        at = atomicAdd(counter, incl);
-    at = read_lane(at, 63) + incl - mine;
-    while (in != 0) {
-        const uint32_t k = uint32_t(__builtin_ctz(in));
-        in &= in - 1;
-        float v = x[0];
+    uint64_t m[SM_VEC];
+    int all = 0;
 #pragma unroll
-        for (uint32_t j = 1; j < SM_VEC; ++j)
-            v = k == j ? x[j] : v;
-        write(at++, v, k);
+    for (int k = 0; k < SM_VEC; ++k) {
+        m[k] = __ballot(in(x[k], k));
+        all += __builtin_popcountll(m[k]);
+    }
+    if (all == 0)
+        return;
+    uint32_t at = 0;
+    if (lane_id() == 0)
+        at = atomicAdd(counter, uint32_t(all));
+    at = uniform(at);
+#pragma unroll
+    for (int k = 0; k < SM_VEC; ++k) {
+        if (m[k] != 0) {
+            if (in(x[k], k))
+                write(at + __builtin_amdgcn_mbcnt_hi(uint32_t(m[k] >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m[k]), 0u)),
+                      x[k], k);
+            at += uint32_t(__builtin_popcountll(m[k]));
+        }
     }
 }
 
@@ -796,10 +859,6 @@ __device__ __forceinline__ uint32_t lowest_key(const Row<TYPE>& row, uint32_t b)
     return hi;
 }
 
-struct Bin {
-    uint32_t bin, key_lo, key_hi;
-};
-
 template <int TYPE>
 __device__ __forceinline__ Bin make_bin(const Row<TYPE>& row, uint32_t b)
 {
@@ -827,35 +886,73 @@ __device__ __forceinline__ uint32_t index_at(const Row<TYPE>& row, uint64_t plac
     return uint32_t(place) & ((1u << row.index_bits) - 1u);
 }
 
-// Collects a bin's elements, `all` or those with a place in [lo, hi], into the list; their
-// number (the list holds SM_LIST).
+// Collects a bin's elements with a place in [lo, hi] into the list; their number, or more than
+// SM_LIST where they are too many.  First each wave notes which lanes' loads hold any of them
+// (one test for eight elements: few hold any), then it reads only these again.
 template <int TYPE>
-__device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, bool all,
-                                            uint64_t lo, uint64_t hi)
+__device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, uint64_t lo,
+                                            uint64_t hi)
 {
-    const float x_lo = value_of(bin.key_lo), x_hi = value_of(bin.key_hi);
+    const uint32_t lane = uint32_t(lane_id());
+    const int wave = uniform(int(threadIdx.x >> 6));
+    const uint32_t k_lo = key_at(row, bin.key_hi, hi), k_hi = key_at(row, bin.key_hi, lo);
+    const float x_lo = value_of(k_lo), x_hi = value_of(k_hi);
+    // a range within one value is one of indexes; any other takes its values whole (cut_in_bin)
+    const uint32_t i_lo = k_lo == k_hi ? index_at(row, lo) : 0u;
+    const uint32_t i_hi = k_lo == k_hi ? index_at(row, hi) : ~0u - SM_VEC;
+    const int begin = int(i_lo / SM_STEP);
+    const int end = i_hi / SM_STEP < uint32_t(row.steps) ? int(i_hi / SM_STEP) + 1 : row.steps;
     __syncthreads();
     if (threadIdx.x == 0)
         sh.n_list = 0;
-    __syncthreads();
-    row.template for_steps<2>(int(threadIdx.x >> 6), row.steps, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
-        uint32_t in = 0;
+    uint32_t n = 0;
+    uint32_t* notes = sh.notes[wave];
+    row.template for_steps<TYPE == LOGITS_F32 ? 1 : LS_UC>(begin + wave, end, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+        uint64_t m = 0;
 #pragma unroll
         for (int k = 0; k < SM_VEC; ++k)
-            in |= x[k] >= x_lo && x[k] <= x_hi ? 1u << k : 0u;
-        if (!all) {
+            m |= __ballot(x[k] >= x_lo && x[k] <= x_hi);
+        m &= __ballot(idx + SM_VEC > i_lo && idx <= i_hi);
+        if (m == 0)
+            return;
+        const uint32_t at =
+            n + __builtin_amdgcn_mbcnt_hi(uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0u));
+        if ((m >> lane & 1u) && at < SM_NOTES)
+            notes[at] = idx;
+        n += uint32_t(__builtin_popcountll(m));
+    });
+    __syncthreads();
+    if (n > SM_NOTES && lane == 0)
+        atomicAdd(&sh.n_list, uint32_t(SM_LIST) + 1u);
+#pragma unroll 1
+    for (uint32_t j = lane; uniform(j) < n && n <= SM_NOTES; j += 64) {
+        Raw<TYPE> raw;
+        raw.clear();
+        const uint32_t note = j < n ? notes[j] : 0u;
+        if (j < n)
+            raw.load(row.p, note, row.vocab);
+        float x[SM_VEC];
+        raw.unpack(x, row.inf);
+        uint32_t in = 0;
 #pragma unroll
-            for (int k = 0; k < SM_VEC; ++k) {
-                const uint64_t v = place_of(row, bin.key_hi, key_of(x[k]), idx + k);
-                if (v < lo || v > hi)
-                    in &= ~(1u << k);
+        for (uint32_t k = 0; k < SM_VEC; ++k) {
+            const uint64_t v = place_of(row, bin.key_hi, key_of(x[k]), note + k);
+            in |= x[k] >= x_lo && x[k] <= x_hi && v >= lo && v <= hi ? 1u << k : 0u;
+        }
+        const uint32_t mine = uint32_t(__builtin_popcount(in)), incl = wave_inclusive_scan<SumU32>(mine);
+        uint32_t at = 0;
+        if (lane == 63)
+            at = atomicAdd(&sh.n_list, incl);
+        at = read_lane(at, 63) + incl - mine;
+#pragma unroll
+        for (uint32_t k = 0; k < SM_VEC; ++k) {
+            if (in >> k & 1u) {
+                if (at < SM_LIST)
+                    sh.list[at] = place_of(row, bin.key_hi, key_of(x[k]), note + k);
+                ++at;
             }
         }
-        wave_append(&sh.n_list, in, x, [&](uint32_t at, float v, uint32_t k) {
-            if (at < SM_LIST)
-                sh.list[at] = place_of(row, bin.key_hi, key_of(v), idx + k);
-        });
-    });
+    }
     __syncthreads();
     return uniform(sh.n_list);
 }
@@ -863,8 +960,10 @@ __device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh
 // The element of a bin that makes the count reach `want` (by_count) or the weight reach
 // `goal`, where above_count and above lie in front of the bin.  Its elements are
 // collected; while they are too many, the range of places is cut into SM_RANGES and the
-// one the cut lies in is kept (at one place to a range there is one element left, so this
-// ends).  Returns the place; `weight`: the weight up to and including it; `listed`:
+// one the cut lies in is kept.  A range is a power of two of places and starts at a multiple
+// of it, so it is whole values, or indexes of one value.  At most eight bits of 64 go at a
+// time, and one place is one element, so eight rounds and the one that collects suffice.
+// Returns the place; `weight`: the weight up to and including it; `listed`:
 // whether the list holds the whole bin.
 template <int TYPE>
 __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, bool by_count,
@@ -873,10 +972,17 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
 {
     const uint32_t tid = threadIdx.x;
     uint64_t lo = 0, hi = place_of(row, bin.key_hi, bin.key_lo, (1u << row.index_bits) - 1u);
-    uint32_t n = collect(row, sh, bin, true, lo, hi);
-    listed = n <= SM_LIST;
-    bool in_list = listed;
-    while (n > SM_SMALL) {
+    uint32_t n = 0;
+    bool in_list = false, first = true;
+    for (int round = 0; round < 10; ++round) {
+        if (!in_list && n <= SM_LIST) {
+            n = collect(row, sh, bin, lo, hi);
+            in_list = n <= SM_LIST;
+            listed = first && in_list;
+            first = false;
+        }
+        if (in_list && n <= SM_SMALL)
+            break;
         const uint64_t span = hi - lo;
         const int bits = 64 - __builtin_clzll(span | 1u);
         const int shift = bits > 8 ? bits - 8 : 0;
@@ -900,7 +1006,7 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
             }
         } else {
             const float x_lo = value_of(bin.key_lo), x_hi = value_of(bin.key_hi);
-            row.template for_steps<2>(int(tid >> 6), row.steps, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+            row.template for_steps<1>(int(tid >> 6), row.steps, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
 #pragma unroll
                 for (int k = 0; k < SM_VEC; ++k) {
                     if (x[k] >= x_lo && x[k] <= x_hi) {
@@ -919,20 +1025,20 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
         const uint64_t last = lo + ((uint64_t(1) << shift) - 1);
         hi = hi < last ? hi : last;
         __syncthreads();
-        if (!in_list && n <= SM_LIST) {
-            collect(row, sh, bin, false, lo, hi);
-            in_list = true;
-        }
     }
     if (tid == 0)
         sh.n_small = 0;
     __syncthreads();
-    for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
+    for (uint32_t i = tid; i < sh.n_list && i < SM_LIST; i += SM_BLOCK) {
         const uint64_t v = sh.list[i];
-        if (v >= lo && v <= hi)
-            sh.small[atomicAdd(&sh.n_small, 1u)] = v;
+        if (v >= lo && v <= hi) {
+            const uint32_t at = atomicAdd(&sh.n_small, 1u);
+            if (at < SM_SMALL)
+                sh.small[at] = v;
+        }
     }
     __syncthreads();
+    n = n < SM_SMALL ? n : SM_SMALL;
     order_small(sh, n);
     // 64 of the order at a time, by every wave for itself
     uint64_t place = 0;
@@ -954,6 +1060,37 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
     return place;
 }
 
+// One wave: the bin in which the count reaches `want` (by_count) or the weight `goal` (of the
+// whole row's weight, its share -goal where it is negative), into sh.pick; the whole
+// weight into sh.kept.
+template <int TYPE>
+__device__ __forceinline__ void choose_bin(const Row<TYPE>& row, SharedCuts& sh, bool by_count, uint32_t want,
+                                           double goal)
+{
+    constexpr int N = SM_BINS / 64;
+    double all = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        all += sh.bin_mass[lane_id() * N + i];
+    all = read_lane64(wave_inclusive_sum64(all), 63);
+    goal = goal > 0.0 ? goal : -goal * all;
+    uint32_t above_count = 0, n = 0;
+    double above = 0.0;
+    const uint32_t b = pick<N>(
+        sh.bin_count, [&](uint32_t i) { return sh.bin_mass[i]; }, by_count, want, goal, above_count, above, n);
+    const Bin bin = make_bin(row, b);
+    sh.kept = all;
+    sh.pick.bin = bin;
+    sh.pick.above_count = above_count;
+    sh.pick.above = above;
+    sh.pick.goal = goal;
+    sh.pick.reached = above_count + n >= want ? 1u : 0u;
+}
+__device__ __forceinline__ Bin uniform_bin(const SharedCuts& sh)
+{
+    return Bin{uniform(sh.pick.bin.bin), uniform(sh.pick.bin.key_lo), uniform(sh.pick.bin.key_hi)};
+}
+
 // The histogram of one wave's share of a row.  A weight is the weight 2^(-b/8) of its bin
 // times 2^(z/8), |z| <= 1/2, and the bin counts the second factor in units of 2^-frac: a
 // polynomial of degree 6 (relative error 2^-48.9) into whose last step the rounding to an
@@ -967,7 +1104,7 @@ __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, 
     const double c1 = uniform(one * 0x1.62e42fefa3aefp-4), c2 = uniform(one * 0x1.ebfbdff82c5e7p-9);
     const double c3 = uniform(one * 0x1.c6b08d5e4bb3bp-14), c4 = uniform(one * 0x1.3b2ab6f5687a9p-19);
     const double c5 = uniform(one * 0x1.5d8dfde822453p-25), c6 = uniform(one * 0x1.430d3b3f37695p-31);
-    row.template for_steps<2>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+    row.template for_steps<TYPE == LOGITS_F32 ? 2 : LS_UB>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
 #pragma unroll
         for (int j = 0; j < SM_VEC; ++j) {
             const double d = row.below(x[j]);
@@ -997,7 +1134,7 @@ __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, 
 // for the running sums.
 template <int TYPE>
 __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const Row<TYPE>& row, SharedCuts& sh,
-                                        uint32_t k, double p, double least, double u)
+                                        uint32_t k, double p, double least)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int share = (row.steps + SM_WAVES - 1) / SM_WAVES;
@@ -1032,37 +1169,30 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
                 sh.bin_count[tid] = m != 0 ? 1u : 0u;
         }
         __syncthreads();
-        constexpr int N = SM_BINS / 64;
-        const auto in_bin = [&](uint32_t b) { return sh.bin_mass[b]; };
-        uint32_t above_count = 0, n = 0, b = 0;
-        double above = 0.0, kept = 0.0;
-        for (int i = 0; i < N; ++i)
-            kept += sh.bin_mass[lane * N + i];
-        kept = read_lane64(wave_inclusive_sum64(kept), 63);
-        if (by_k)
-            b = pick<N>(sh.bin_count, in_bin, true, k, 0.0, above_count, above, n);
-        if (by_k && above_count + n >= k) {
-            bin = make_bin(row, b);
-            place = cut_in_bin(row, sh, bin, true, k, 0.0, above_count, above, kept, in_parts);
+        // top-k's cut first, then top-p's by the weight up to it
+        double kept = 0.0;
+        for (int which = by_k ? 0 : 1; which < (by_p ? 2 : 1); ++which) {
+            const Bin last_bin = bin;
+            const uint64_t last_place = place;
+            const Cut last_cut = cut;
+            __syncthreads();
+            if (wave == 0)
+                choose_bin(row, sh, which == 0, k, which == 0 ? 0.0 : last_cut.key != 0 ? p * kept : -p);
+            __syncthreads();
+            if (which == 0) {
+                kept = uniform(sh.kept);
+                if (uniform(sh.pick.reached) == 0u)
+                    continue;  // no more elements than k
+            }
+            bin = uniform_bin(sh);
+            place = cut_in_bin(row, sh, bin, which == 0, k, uniform(sh.pick.goal), uniform(sh.pick.above_count),
+                               uniform(sh.pick.above), kept, in_parts);
             cut = Cut{key_at(row, bin.key_hi, place), index_at(row, place)};
-        }
-        if (by_p) {
-            const double goal = p * kept;
-            const Bin k_bin = bin;
-            const uint64_t k_place = place;
-            const Cut k_cut = cut;
-            above_count = 0;
-            above = 0.0;
-            b = pick<N>(sh.bin_count, in_bin, false, 0, goal, above_count, above, n);
-            bin = make_bin(row, b);
-            double weight;
-            place = cut_in_bin(row, sh, bin, false, 0, goal, 0, above, weight, in_parts);
-            cut = Cut{key_at(row, bin.key_hi, place), index_at(row, place)};
-            if (k_cut.key != 0 && cut.keeps(k_cut.key, k_cut.index)) {
+            if (which == 1 && last_cut.key != 0 && cut.keeps(last_cut.key, last_cut.index)) {
                 // no later than top-k's own cut, which rounding may have put first
-                in_parts = in_parts && k_bin.bin == bin.bin;
-                place = k_place;
-                cut = k_cut;
+                in_parts = in_parts && last_bin.bin == bin.bin;
+                place = last_place;
+                cut = last_cut;
             }
         }
     }
@@ -1074,6 +1204,7 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
         return w >= least ? w : 0.0;
     };
     double total;
+    const double u = double(call.uniforms[r]);
     if (in_parts && least == 0.0 && u > 0.0) {
         for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
             const uint64_t v = sh.list[i];
@@ -1096,7 +1227,7 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
         bool over;
         wave_sums(v, incl, total);
         const double goal = goal_of(u, total);
-        const int part = wave_first_over(v, goal, incl, before, over);
+        const int over_at = wave_first_over(v, goal, incl, before, over), part = over_at < 0 ? 0 : over_at;
         const int begin = part * share, end = begin + share < row.steps ? begin + share : row.steps;
         // a wave takes one step in sixteen of it, adds up and hands the sums round
         const int per = (share + SM_WAVES - 1) / SM_WAVES;
@@ -1182,13 +1313,13 @@ __device__ __forceinline__ void find_segments(const SampleGrid& g, const Row<TYP
 template <int TYPE>
 __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const SampleGrid& g, int64_t r,
                                                const Row<TYPE>& row, SharedCuts& sh, uint32_t k, double p,
-                                               double least, double u)
+                                               double least)
 {
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(int(tid >> 6));
     const float low = uniform(sh.low);
     const uint32_t key_hi = key_of(row.top);
-    constexpr int U = 4;
+    constexpr int U = TYPE == LOGITS_F32 ? 2 : 4;
     const int todo = int(uniform(sh.n_segs)) * g.seg_steps;
     for (int i = wave; i < todo; i += U * SM_WAVES) {
         Raw<TYPE> raw[U];
@@ -1210,15 +1341,13 @@ __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const Sam
         for (int j = 0; j < U; ++j) {
             float x[SM_VEC];
             raw[j].unpack(x, row.inf);
-            uint32_t in = 0;
-#pragma unroll
-            for (int m = 0; m < SM_VEC; ++m)
-                in |= x[m] >= low ? 1u << m : 0u;
-            wave_append(&sh.n_small, in, x, [&](uint32_t at, float v, uint32_t m) {
-                if (at < SM_SMALL)
-                    sh.small[at] =
-                        place_of(row, key_hi, key_of(v), uint32_t(step[j]) * SM_STEP + lane * SM_VEC + m);
-            });
+            wave_append(
+                &sh.n_small, x, [&](float v, int) { return v >= low; },
+                [&](uint32_t at, float v, int m) {
+                    if (at < SM_SMALL)
+                        sh.small[at] = place_of(row, key_hi, key_of(v),
+                                                uint32_t(step[j]) * SM_STEP + lane * SM_VEC + uint32_t(m));
+                });
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -1280,7 +1409,7 @@ __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const Sam
     for (uint32_t d = 1; d < group; d <<= 1)
         run += __shfl_xor(run, int(d));
     if (e < keep && part == 0) {
-        if (run > goal_of(u, total))
+        if (run > goal_of(double(call.uniforms[r]), total))
             atomicMin(&sh.s.found, index);
         if (sh.weight[e] > 0.0)
             atomicMax(&sh.s.last, index);
@@ -1296,7 +1425,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
 {
     __shared__ SharedCuts sh;
     constexpr float NEG = -__builtin_inff();
-    constexpr int U = 4;
+    constexpr int U = TYPE == LOGITS_F32 ? 2 : 4;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int64_t r = blockIdx.x % uint32_t(call.rows);
     const int part = int(blockIdx.x / uint32_t(call.rows));
@@ -1351,7 +1480,6 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
     double least = 0.0;
     if (call.min_p != nullptr && call.min_p[r] > 0.0f)
         least = uniform(__builtin_fmin(double(call.min_p[r]), 1.0));
-    const double u = uniform(double(call.uniforms[r]));
     // few enough that the k-th largest of the segments' values leaves few candidates
     const bool few = uint64_t(k) * 4 <= uint64_t(g.segs) * 3;
     const bool candidates = few || (p >= 1.0 && least > 0.0);
@@ -1371,8 +1499,8 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
         return;
     row.set_top(uniform(sh.top));
     row.set_temperature(call.temperature[r]);
-    if (!(candidates && cut_candidates(call, g, r, row, sh, k, p, least, u)))
-        cut_row(call, r, row, sh, k, p, least, u);
+    if (!(candidates && cut_candidates(call, g, r, row, sh, k, p, least)))
+        cut_row(call, r, row, sh, k, p, least);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1421,9 +1549,17 @@ hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t
     if (!cuts && rows * g.steps >= 4 * 8192 && g.seg_steps < 4)
         g.seg_steps = 4;
     g.segs = (g.steps + g.seg_steps - 1) / g.seg_steps;
-    // segments to a wave: four once that leaves 8192 waves
+    // Without cuts one segment to a wave.  With cuts no more blocks than CUs (the LDS holds one block a CU) where
+    // that leaves each row one, in parts that fill the waves.
+    if (cuts) {
+        const int64_t blocks = rows < SM_CUS ? SM_CUS / rows : 1, shares = (g.segs + SM_WAVES - 1) / SM_WAVES;
+        g.per_wave = int((shares + blocks - 1) / blocks);
+    } else {
+        g.per_wave = LS_PW;
+    }
     const int waves = cuts ? SM_WAVES : SM_ALL_BLOCK / 64;
-    g.per_wave = int(rows * g.segs >= 4 * 8192 ? 4 : rows * g.segs >= 2 * 8192 ? 2 : 1);
+    if (g.per_wave < 1)
+        g.per_wave = 1;
     g.parts = (g.segs + waves * g.per_wave - 1) / (waves * g.per_wave);
     if (g.parts < 1)
         g.parts = 1;
