@@ -43,6 +43,9 @@ namespace ls {
 #ifndef LS_U16
 #define LS_U16 4
 #endif
+#ifndef LS_OCC
+#define LS_OCC 4
+#endif
 #ifndef LS_UC
 #define LS_UC 2
 #endif
@@ -98,6 +101,51 @@ __device__ __forceinline__ double exp2_fast(double d, double c, int e = 0)
     return __builtin_bit_cast(double, p);
 }
 
+// The sum of 2^(x c - R) over four logits, for an integer R given as k = TO_INT - R: rounding x c + k leaves
+// the exponent in the low word, and the fraction x c less its nearest integer is one multiply-add
+// with no subtraction of a reference from x.  The polynomial has one degree less than
+// exp2_poly's, its relative error is 2^-44.6.  Four side by side, as a multiply-add's result
+// is ready some issues later.
+__device__ __forceinline__ double exp2_sum4(const double (&x)[4], double c, double k)
+{
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    constexpr double C[10] = {1.0,
+                              0x1.62e42fefa39efp-1,
+                              0x1.ebfbdff823cedp-3,
+                              0x1.c6b08d7047e52p-5,
+                              0x1.3b2ab7181b755p-7,
+                              0x1.5d87fe86fe88ep-10,
+                              0x1.4308ac85aa947p-13,
+                              0x1.ffcb9515a8016p-17,
+                              0x1.63d136366db24p-20,
+                              0x1.b63880a30e9ffp-24};
+    double t[4], f[4], p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        t[i] = __builtin_fma(x[i], c, k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = __builtin_fma(x[i], c, k - t[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        p[i] = __builtin_fma(C[9], f[i], C[8]);
+#pragma unroll
+    for (int j = 7; j >= 0; --j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = __builtin_fma(p[i], f[i], C[j]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        u32x2 w = __builtin_bit_cast(u32x2, p[i]);
+        asm("v_lshl_add_u32 %0, %1, 20, %2" : "=v"(w.y) : "v"(uint32_t(__builtin_bit_cast(uint64_t, t[i]))), "v"(w.y));
+        sum += __builtin_bit_cast(double, w);
+    }
+    return sum;
+}
+
 // 2^y for y <= 0 (NaN counts as -inf), 0 below 2^-1074.
 __device__ __forceinline__ double exp2_exact(double y)
 {
@@ -149,20 +197,24 @@ struct Raw {
         for (int k = 0; k < WORDS; ++k)
             w[k] = NEG;
     }
+    using E = typename std::conditional<TYPE == LOGITS_F32, uint32_t, uint16_t>::type;
+    using V = typename std::conditional<TYPE == LOGITS_F32, u32x4_by4, u32x4_by2>::type;
+    __device__ __forceinline__ void load_all(const E* p)
+    {
+#pragma unroll
+        for (int k = 0; k < WORDS; k += 4) {
+            const V a = *reinterpret_cast<const V*>(reinterpret_cast<const uint32_t*>(p) + k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[k + j] = a[j];
+        }
+    }
     // Logits idx .. idx+7; rows start at any multiple of the element's size.
     __device__ __forceinline__ void load(const void* row, int64_t idx, int64_t vocab)
     {
-        using E = typename std::conditional<TYPE == LOGITS_F32, uint32_t, uint16_t>::type;
-        using V = typename std::conditional<TYPE == LOGITS_F32, u32x4_by4, u32x4_by2>::type;
         const E* p = static_cast<const E*>(row) + idx;
         if (idx + SM_VEC <= vocab) {
-#pragma unroll
-            for (int k = 0; k < WORDS; k += 4) {
-                const V a = *reinterpret_cast<const V*>(reinterpret_cast<const uint32_t*>(p) + k);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[k + j] = a[j];
-            }
+            load_all(p);
         } else {
             // the row's end: one element at a time, last first (a loop: this code stands at every load)
 #pragma unroll 1
@@ -174,6 +226,16 @@ struct Raw {
                 w[0] = TYPE == LOGITS_F32 ? e : (w[0] << 16) | e;
             }
         }
+    }
+    // A lane's logits of one step.  Whether the step is whole is the same for all lanes, so that whole ones
+    // take a scalar address and no test per lane.
+    __device__ __forceinline__ void load_step(const void* row, int step, int64_t vocab)
+    {
+        const int64_t first = int64_t(step) * SM_STEP;
+        if (first + SM_STEP <= vocab)
+            load_all(static_cast<const E*>(row) + first + uint32_t(lane_id()) * SM_VEC);
+        else
+            load(row, first + lane_id() * SM_VEC, vocab);
     }
     __device__ __forceinline__ void unpack(float (&x)[SM_VEC], bool inf) const
     {
@@ -267,18 +329,19 @@ struct Row {
     template <int U, class F>
     __device__ __forceinline__ void for_steps(int first, int end, int stride, F f) const
     {
-        const int lane = lane_id();
+        first = uniform(first);  // the same in all lanes, as the addresses want it
+        end = uniform(end);
         Raw<TYPE> raw[U], next[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (first + u * stride < end)
-                raw[u].load(p, int64_t(first + u * stride) * SM_STEP + lane * SM_VEC, vocab);
+                raw[u].load_step(p, first + u * stride, vocab);
         for (int s = first; s < end; s += U * stride) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int at = s + (U + u) * stride;
                 if (at < end)
-                    next[u].load(p, int64_t(at) * SM_STEP + lane * SM_VEC, vocab);
+                    next[u].load_step(p, at, vocab);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -286,7 +349,7 @@ struct Row {
                 if (at < end) {
                     float x[SM_VEC];
                     raw[u].unpack(x, inf);
-                    f(x, uint32_t(at) * SM_STEP + uint32_t(lane * SM_VEC));
+                    f(x, uint32_t(at) * SM_STEP + uint32_t(lane_id() * SM_VEC));
                 }
                 __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
             }
@@ -347,13 +410,13 @@ __device__ __forceinline__ int wave_first_over(const double (&v)[N], double goal
 
 // One wave: the first index in steps [first, end) at which `run` and the running sum of
 // f(x, index) exceed `goal`, or the last of positive weight; ~0 if there is none.
-template <int TYPE, class F>
+template <int U, int TYPE, class F>
 __device__ __forceinline__ uint32_t wave_find_token(const Row<TYPE>& row, int first, int end, double run, double goal,
                                                     F f)
 {
     uint32_t found = ~0u;
     bool over = false;
-    row.template for_steps<1>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
+    row.template for_steps<U>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
         if (over)
             return;
         double w[SM_VEC], incl, total, before = run;
@@ -407,7 +470,7 @@ __device__ __forceinline__ uint32_t find_in_order(const Row<TYPE>& row, SharedSu
             v[k] = sh.sums[lane * N + k];
         wave_sums(v, incl, total);
         const int over_at = wave_first_over(v, goal_of(u, total), incl, before, over), s = over_at < 0 ? 0 : over_at;
-        const uint32_t token = wave_find_token(row, s * per, s * per + per < row.steps ? s * per + per : row.steps,
+        const uint32_t token = wave_find_token<1>(row, s * per, s * per + per < row.steps ? s * per + per : row.steps,
                                                before, goal_of(u, total), f);
         if (lane == 0) {
             sh.found = token;
@@ -560,7 +623,7 @@ __device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int 
                                               float& top)
 {
     float m = -__builtin_inff();
-    row.template for_steps<4>(s0, s1, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+    row.template for_steps<TYPE == LOGITS_F32 ? 2 : 4>(s0, s1, 1, [&](const float(&x)[SM_VEC], uint32_t) {
 #pragma unroll
         for (int k = 0; k < SM_VEC; ++k)
             m = x[k] > m ? x[k] : m;
@@ -586,7 +649,7 @@ __device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int 
 // segment's own largest value.  Bound by the logits' bytes in float32 and by the
 // multiply-adds (18 instructions a logit) in 16 bits.
 template <int TYPE>
-__global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall call, SampleGrid g)
+__global__ __launch_bounds__(SM_ALL_BLOCK, LS_OCC) void sample_all_kernel(SampleCall call, SampleGrid g)
 {
     constexpr float NEG = -__builtin_inff();
     constexpr int U = TYPE == LOGITS_F32 ? LS_U32 : LS_U16;
@@ -602,22 +665,30 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
     const int seg1 = seg0 + g.per_wave < g.segs ? seg0 + g.per_wave : g.segs;
     const auto seg_end = [&](int seg) { return (seg + 1) * g.seg_steps < g.steps ? (seg + 1) * g.seg_steps : g.steps; };
     float ref = NEG, low = 0.0f, high = 0.0f;
+    double k = TO_INT, scale = 1.0;  // sums are relative to 2^R; times `scale`, to ref's weight
     if (sums && seg0 < seg1) {
-        // U steps at a time, the next ones on their way meanwhile
-        Raw<TYPE> raw[U], next[U];
+        // U steps at a time, the next ones on their way meanwhile, in two sets of registers by turns
+        Raw<TYPE> set0[U], set1[U];
         const auto load = [&](Raw<TYPE>(&to)[U], int s, int end) {
+            const int64_t first = int64_t(s) * SM_STEP;
+            if (s + U <= end && first + U * SM_STEP <= row.vocab) {
+                const auto* at = static_cast<const typename Raw<TYPE>::E*>(row.p) + first + uint32_t(lane) * SM_VEC;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (s + u < end)
-                    to[u].load(row.p, int64_t(s + u) * SM_STEP + lane * SM_VEC, row.vocab);
-                else
+                for (int u = 0; u < U; ++u)
+                    to[u].load_all(at + u * SM_STEP);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
                     to[u].clear();
+                    if (s + u < end)
+                        to[u].load_step(row.p, s + u, row.vocab);
+                }
             }
         };
         int seg = seg0, s = seg0 * g.seg_steps, s1 = seg_end(seg0);
         double sum = 0.0;
-        load(raw, s, s1);
-        while (true) {
+        // adds up the loaded steps with the next ones under way; false after the last
+        const auto turn = [&](Raw<TYPE>(&raw)[U], Raw<TYPE>(&next)[U]) {
             const bool ends = s + U >= s1;
             const int next_seg = ends ? seg + 1 : seg, next_s = ends ? next_seg * g.seg_steps : s + U;
             const int next_s1 = ends ? seg_end(next_seg) : s1;
@@ -626,45 +697,55 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
             if (ref == NEG) {
                 float m = NEG;
 #pragma unroll
-                for (int k = 0; k < SM_VEC; ++k)
-                    m = raw[0].at(k) > m ? raw[0].at(k) : m;
+                for (int j = 0; j < SM_VEC; ++j)
+                    m = raw[0].at(j) > m ? raw[0].at(j) : m;
                 ref = read_lane(wave_inclusive_scan<MaxF32>(m), 63);
                 low = uniform(float(double(ref) + far));
                 high = uniform(float(double(ref) - far));
+                const double whole = __builtin_rint(double(ref) * c), off = (double(low) - double(ref)) * c;
+                k = uniform(TO_INT - whole);
+                scale = uniform(exp2_exact(-__builtin_fma(double(ref), c, -whole)));
+                // not so where there is no finite value to go by, no float near enough to 2^-1000 of it, or no
+                // room for R beside the fractions (very low and high temperatures)
+                if (!(off > -1010.0 && off < -900.0 && double(high) - double(ref) < -1.01 * far &&
+                      __builtin_fabs(double(ref) * c) < 0x1p40))
+                    scale = __builtin_nan("");
             }
-            // no finite value to go by, or no float near enough to 2^-1000 of it (a very low or high temperature)
-            const double off = (double(low) - double(ref)) * c;
-            if (!(off > -1010.0 && off < -900.0 && double(high) - double(ref) < -1.01 * far))
-                sum = __builtin_inf();
-            const double ref64 = uniform(double(ref));
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (s + u < s1) {
 #pragma unroll
-                    for (int k = 0; k < SM_VEC; ++k)
-                        sum += exp2_fast(double(__builtin_amdgcn_fmed3f(raw[u].at(k), low, high)) - ref64, c);
+                    for (int j = 0; j < SM_VEC; j += 4) {
+                        double x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = double(__builtin_amdgcn_fmed3f(raw[u].at(j + i), low, high));
+                        sum += exp2_sum4(x, c, k);
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
             }
             if (ends) {
-                sum = read_lane64(wave_inclusive_sum64(sum), 63);
+                sum = read_lane64(wave_inclusive_sum64(sum), 63) * scale;
                 float top = ref;
-                if (!(sum > 0x1p-800 && sum < 0x1p800))
+                if (!(sum > 0x1p-800 && sum < 0x1p800)) {
                     sum = read_lane64(wave_inclusive_sum64(careful_sum(row, seg * g.seg_steps, s1, true, c, far, top)), 63);
+                    if (scale != scale)
+                        ref = NEG;  // the next loads may do
+                }
                 if (lane == 63) {
                     put(&g.tops[r * g.segs + seg], top);
                     put(&g.sums[r * g.segs + seg], sum);
                 }
                 sum = 0.0;
             }
-            if (next_seg >= seg1)
-                break;
             seg = next_seg;
             s = next_s;
             s1 = next_s1;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                raw[u] = next[u];
+            return next_seg < seg1;
+        };
+        load(set0, s, s1);
+        while (turn(set0, set1) && turn(set1, set0)) {
         }
     } else {
         for (int seg = seg0; seg < seg1; ++seg) {
@@ -699,7 +780,7 @@ __global__ __launch_bounds__(SM_ALL_BLOCK) void sample_all_kernel(SampleCall cal
     const int seg = at < 0 ? 0 : at / SM_PER_LANE * tops.per_lane + at % SM_PER_LANE;
     const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
     const uint32_t token =
-        wave_find_token(row, s0, s1, before, goal, [&](float x, uint32_t) { return row.weight(x); });
+        wave_find_token<TYPE == LOGITS_F32 ? 2 : 4>(row, s0, s1, before, goal, [&](float x, uint32_t) { return row.weight(x); });
     write_token(call, r, row, token, total);
 }
 
@@ -1247,7 +1328,7 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
         v[0] = lane < SM_WAVES ? sh.part_sum[lane] : 0.0;
         wave_sums(v, incl, rest);
         if (wave_first_over(v, goal, incl, before, over) == wave)
-            write_token(call, r, row, wave_find_token(row, mine, mine_end, before, goal, kept_weight), total);
+            write_token(call, r, row, wave_find_token<1>(row, mine, mine_end, before, goal, kept_weight), total);
         return;
     }
     const uint32_t token = find_in_order(row, sh.s, u, kept_weight, total);
@@ -1333,7 +1414,7 @@ __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const Sam
                 step[j] = uniform(int(sh.segs[seg])) * g.seg_steps + (q - seg * g.seg_steps);
             }
             if (step[j] < g.steps)
-                raw[j].load(row.p, int64_t(step[j]) * SM_STEP + lane * SM_VEC, row.vocab);
+                raw[j].load_step(row.p, step[j], row.vocab);
             else
                 raw[j].clear();
         }
@@ -1441,7 +1522,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
             for (int u = 0; u < U; ++u) {
                 const int seg = (part * g.per_wave + i + u) * SM_WAVES + wave, s = seg * g.seg_steps + j;
                 if (i + u < g.per_wave && s < g.steps)
-                    raw[u].load(row.p, int64_t(s) * SM_STEP + lane * SM_VEC, row.vocab);
+                    raw[u].load_step(row.p, s, row.vocab);
                 else
                     raw[u].clear();
             }
