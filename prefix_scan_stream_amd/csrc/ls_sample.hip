@@ -34,9 +34,6 @@
 
 namespace ls {
 
-#ifndef LS_PW
-#define LS_PW 4
-#endif
 #ifndef LS_U32
 #define LS_U32 2
 #endif
@@ -46,8 +43,11 @@ namespace ls {
 #ifndef LS_OCC
 #define LS_OCC 4
 #endif
+#ifndef LS_AB
+#define LS_AB true
+#endif
 #ifndef LS_UC
-#define LS_UC 2
+#define LS_UC 4
 #endif
 #ifndef LS_UB
 #define LS_UB 2
@@ -67,7 +67,8 @@ constexpr int SM_LIST = 4096;               // elements of one bin kept in LDS
 constexpr int SM_NOTES = 256;               // loads of one wave that hold such elements
 constexpr int SM_SMALL = 512;               // elements that are ordered by counting
 constexpr int SM_CUS = 256;
-constexpr int SM_ROWS = 16384;              // most rows of a launch (at most 128 blocks each)
+constexpr int SM_ROWS = 4096;               // most rows of a launch
+constexpr int SM_COUNTER = 32;              // 32-bit words from one row's counter to the next
 
 constexpr double LOG2E = 0x1.71547652b82fep+0, LN2 = 0x1.62e42fefa39efp-1;
 constexpr double TO_INT = 0x1.8p52;  // adding it rounds to the nearest integer, into the low word
@@ -324,25 +325,27 @@ struct Row {
     {
         return __builtin_ldexp(double(m), -(int(b / SM_PER_OCTAVE) + frac));
     }
-    // f(x[8], index of x[0]) over steps first, first + stride, ... below end, by one wave; the next U loads are
-    // in flight while f works on these.
-    template <int U, class F>
+    // f(x[8], index of x[0]) over steps first, first + stride, ... below end, by one wave, U loads at a time.
+    // AHEAD: the next U are in flight while f works on these, for twice the registers.
+    template <int U, bool AHEAD = true, class F>
     __device__ __forceinline__ void for_steps(int first, int end, int stride, F f) const
     {
         first = uniform(first);  // the same in all lanes, as the addresses want it
         end = uniform(end);
         Raw<TYPE> raw[U], next[U];
+        const auto load = [&](Raw<TYPE>(&to)[U], int s) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (first + u * stride < end)
-                raw[u].load_step(p, first + u * stride, vocab);
+            for (int u = 0; u < U; ++u)
+                if (s + u * stride < end)
+                    to[u].load_step(p, s + u * stride, vocab);
+        };
+        if (AHEAD)
+            load(raw, first);
         for (int s = first; s < end; s += U * stride) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int at = s + (U + u) * stride;
-                if (at < end)
-                    next[u].load_step(p, at, vocab);
-            }
+            if (AHEAD)
+                load(next, s + U * stride);
+            else
+                load(raw, s);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int at = s + u * stride;
@@ -353,9 +356,11 @@ struct Row {
                 }
                 __builtin_amdgcn_sched_barrier(0);  // one load's work at a time, for the registers
             }
+            if (AHEAD) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                raw[u] = next[u];
+                for (int u = 0; u < U; ++u)
+                    raw[u] = next[u];
+            }
         }
     }
 };
@@ -416,7 +421,7 @@ __device__ __forceinline__ uint32_t wave_find_token(const Row<TYPE>& row, int fi
 {
     uint32_t found = ~0u;
     bool over = false;
-    row.template for_steps<U>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
+    row.template for_steps<U, false>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
         if (over)
             return;
         double w[SM_VEC], incl, total, before = run;
@@ -498,6 +503,9 @@ __device__ __forceinline__ T get(const T* p)
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Counts the caller in; whether it is the last of `parts`, which leaves the counter at 0.
+// Additions to one 128-byte line take turns (about 10 ns each): a line to each row, and one
+// addition to a block.  With counters side by side and one addition to a wave, 16 rows of
+// 131072 without cuts took 54 us against 13.
 __device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t parts)
 {
     const bool last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u == parts;
@@ -623,7 +631,7 @@ __device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int 
                                               float& top)
 {
     float m = -__builtin_inff();
-    row.template for_steps<TYPE == LOGITS_F32 ? 2 : 4>(s0, s1, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+    row.template for_steps<TYPE == LOGITS_F32 ? 2 : 4, false>(s0, s1, 1, [&](const float(&x)[SM_VEC], uint32_t) {
 #pragma unroll
         for (int k = 0; k < SM_VEC; ++k)
             m = x[k] > m ? x[k] : m;
@@ -642,7 +650,7 @@ __device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int 
     return sum;
 }
 
-// Waves work for themselves; the one that finishes a row last finds its token.  A double
+// Waves work for themselves; the first of the row's last block finds its token.  A double
 // reaches from 2^-1000 to 2^1000, so a wave's weights can be taken relative to the largest
 // value of its first loads, whatever comes later: logits are held within 2^+-1000 of it, and a
 // sum that leaves 2^-800 .. 2^800 (as one with NaN in it may) is made again with the
@@ -755,11 +763,13 @@ __global__ __launch_bounds__(SM_ALL_BLOCK, LS_OCC) void sample_all_kernel(Sample
                 put(&g.tops[r * g.segs + seg], top);
         }
     }
+    __shared__ uint32_t s_last;
     stores_done();
-    bool last = false;
-    if (lane == 0)
-        last = count_in(&g.counters[r], uint32_t(g.parts * WAVES));
-    if (__ballot(last) == 0)
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = count_in(&g.counters[r * SM_COUNTER], uint32_t(g.parts)) ? 1u : 0u;
+    __syncthreads();
+    if (uniform(s_last) == 0u || wave != 0)
         return;
 
     Tops tops;
@@ -983,17 +993,20 @@ __device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh
     const uint32_t i_hi = k_lo == k_hi ? index_at(row, hi) : ~0u - SM_VEC;
     const int begin = int(i_lo / SM_STEP);
     const int end = i_hi / SM_STEP < uint32_t(row.steps) ? int(i_hi / SM_STEP) + 1 : row.steps;
+    // a little more than half the values' range about its middle, for the roundings of x - mid
+    const float mid = uniform(0.5f * x_lo + 0.5f * x_hi);
+    const float half = uniform((0.5f * x_hi - 0.5f * x_lo) * 1.000001f + (__builtin_fabsf(x_lo) + __builtin_fabsf(x_hi)) * 1e-6f + 1e-37f);
     __syncthreads();
     if (threadIdx.x == 0)
         sh.n_list = 0;
     uint32_t n = 0;
     uint32_t* notes = sh.notes[wave];
-    row.template for_steps<TYPE == LOGITS_F32 ? 1 : LS_UC>(begin + wave, end, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
-        uint64_t m = 0;
+    row.template for_steps<TYPE == LOGITS_F32 ? LS_UC / 2 : LS_UC, false>(begin + wave, end, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+        float near = __builtin_inff();
 #pragma unroll
         for (int k = 0; k < SM_VEC; ++k)
-            m |= __ballot(x[k] >= x_lo && x[k] <= x_hi);
-        m &= __ballot(idx + SM_VEC > i_lo && idx <= i_hi);
+            near = __builtin_fminf(near, __builtin_fabsf(x[k] - mid));
+        const uint64_t m = __ballot(near <= half && idx + SM_VEC > i_lo && idx <= i_hi);
         if (m == 0)
             return;
         const uint32_t at =
@@ -1005,33 +1018,47 @@ __device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh
     __syncthreads();
     if (n > SM_NOTES && lane == 0)
         atomicAdd(&sh.n_list, uint32_t(SM_LIST) + 1u);
+    constexpr uint32_t U = TYPE == LOGITS_F32 ? 2 : 4;
+    static_assert(SM_NOTES == 256, "64 at a time, U on their way");
 #pragma unroll 1
-    for (uint32_t j = lane; uniform(j) < n && n <= SM_NOTES; j += 64) {
-        Raw<TYPE> raw;
-        raw.clear();
-        const uint32_t note = j < n ? notes[j] : 0u;
-        if (j < n)
-            raw.load(row.p, note, row.vocab);
-        float x[SM_VEC];
-        raw.unpack(x, row.inf);
-        uint32_t in = 0;
+    for (uint32_t j = 0; j < n && n <= SM_NOTES; j += 64 * U) {
+        Raw<TYPE> raw[U];
+        uint32_t note[U];
 #pragma unroll
-        for (uint32_t k = 0; k < SM_VEC; ++k) {
-            const uint64_t v = place_of(row, bin.key_hi, key_of(x[k]), note + k);
-            in |= x[k] >= x_lo && x[k] <= x_hi && v >= lo && v <= hi ? 1u << k : 0u;
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t at = j + u * 64 + lane;
+            raw[u].clear();
+            note[u] = at < n ? notes[at] : 0u;
+            if (at < n)
+                raw[u].load(row.p, note[u], row.vocab);
         }
-        const uint32_t mine = uint32_t(__builtin_popcount(in)), incl = wave_inclusive_scan<SumU32>(mine);
-        uint32_t at = 0;
-        if (lane == 63)
-            at = atomicAdd(&sh.n_list, incl);
-        at = read_lane(at, 63) + incl - mine;
 #pragma unroll
-        for (uint32_t k = 0; k < SM_VEC; ++k) {
-            if (in >> k & 1u) {
+        for (uint32_t u = 0; u < U; ++u) {
+            if (j + u * 64 >= n)
+                break;
+            float x[SM_VEC];
+            raw[u].unpack(x, row.inf);
+            uint32_t in = 0;
+#pragma unroll
+            for (uint32_t k = 0; k < SM_VEC; ++k)
+                in |= x[k] >= x_lo && x[k] <= x_hi && note[u] + k - i_lo <= i_hi - i_lo ? 1u << k : 0u;
+            const uint32_t mine = uint32_t(__builtin_popcount(in)), incl = wave_inclusive_scan<SumU32>(mine);
+            uint32_t at = 0;
+            if (lane == 63)
+                at = atomicAdd(&sh.n_list, incl);
+            at = read_lane(at, 63) + incl - mine;
+            while (in != 0) {
+                const uint32_t k = uint32_t(__builtin_ctz(in));
+                in &= in - 1;
+                float v = x[0];
+#pragma unroll
+                for (uint32_t i = 1; i < SM_VEC; ++i)
+                    v = k == i ? x[i] : v;
                 if (at < SM_LIST)
-                    sh.list[at] = place_of(row, bin.key_hi, key_of(x[k]), note + k);
+                    sh.list[at] = place_of(row, bin.key_hi, key_of(v), note[u] + k);
                 ++at;
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     __syncthreads();
@@ -1185,7 +1212,7 @@ __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, 
     const double c1 = uniform(one * 0x1.62e42fefa3aefp-4), c2 = uniform(one * 0x1.ebfbdff82c5e7p-9);
     const double c3 = uniform(one * 0x1.c6b08d5e4bb3bp-14), c4 = uniform(one * 0x1.3b2ab6f5687a9p-19);
     const double c5 = uniform(one * 0x1.5d8dfde822453p-25), c6 = uniform(one * 0x1.430d3b3f37695p-31);
-    row.template for_steps<TYPE == LOGITS_F32 ? 2 : LS_UB>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+    row.template for_steps<TYPE == LOGITS_F32 ? LS_UB / 2 : LS_UB, LS_AB>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
 #pragma unroll
         for (int j = 0; j < SM_VEC; ++j) {
             const double d = row.below(x[j]);
@@ -1545,7 +1572,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
     stores_done();
     __syncthreads();
     if (tid == 0)
-        sh.s.arrived = count_in(&g.counters[r], uint32_t(g.parts)) ? 1u : 0u;
+        sh.s.arrived = count_in(&g.counters[r * SM_COUNTER], uint32_t(g.parts)) ? 1u : 0u;
     __syncthreads();
     if (uniform(sh.s.arrived) == 0u)
         return;
@@ -1604,7 +1631,7 @@ static size_t row_cells(int64_t rows, int64_t vocab)
 size_t sample_workspace_bytes(int64_t rows, int64_t vocab)
 {
     const size_t cells = row_cells(rows, vocab);
-    return 256 + SM_ROWS * 4 + round256(cells * 4) + round256(cells * 8);
+    return 256 + SM_ROWS * SM_COUNTER * 4 + round256(cells * 4) + round256(cells * 8);
 }
 
 template <int TYPE>
@@ -1630,13 +1657,13 @@ hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t
     if (!cuts && rows * g.steps >= 4 * 8192 && g.seg_steps < 4)
         g.seg_steps = 4;
     g.segs = (g.steps + g.seg_steps - 1) / g.seg_steps;
-    // Without cuts one segment to a wave.  With cuts no more blocks than CUs (the LDS holds one block a CU) where
+    // Without cuts up to four segments to a wave, once that leaves 8192 waves.  With cuts no more blocks than CUs (the LDS holds one block a CU) where
     // that leaves each row one, in parts that fill the waves.
     if (cuts) {
         const int64_t blocks = rows < SM_CUS ? SM_CUS / rows : 1, shares = (g.segs + SM_WAVES - 1) / SM_WAVES;
         g.per_wave = int((shares + blocks - 1) / blocks);
     } else {
-        g.per_wave = LS_PW;
+        g.per_wave = int(rows * g.segs >= 4 * 8192 ? 4 : rows * g.segs >= 2 * 8192 ? 2 : 1);
     }
     const int waves = cuts ? SM_WAVES : SM_ALL_BLOCK / 64;
     if (g.per_wave < 1)
@@ -1646,7 +1673,7 @@ hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t
         g.parts = 1;
     char* at = static_cast<char*>(ws) + 256;
     g.counters = reinterpret_cast<uint32_t*>(at);
-    at += SM_ROWS * 4;
+    at += SM_ROWS * SM_COUNTER * 4;
     g.tops = reinterpret_cast<float*>(at);
     at += round256(row_cells(call.rows, call.vocab) * 4);
     g.sums = reinterpret_cast<double*>(at);
