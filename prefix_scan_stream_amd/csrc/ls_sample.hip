@@ -34,24 +34,6 @@
 
 namespace ls {
 
-#ifndef LS_U32
-#define LS_U32 2
-#endif
-#ifndef LS_U16
-#define LS_U16 4
-#endif
-#ifndef LS_OCC
-#define LS_OCC 4
-#endif
-#ifndef LS_AB
-#define LS_AB true
-#endif
-#ifndef LS_UC
-#define LS_UC 4
-#endif
-#ifndef LS_UB
-#define LS_UB 2
-#endif
 
 constexpr int SM_BLOCK = 1024;              // threads of a block that makes cuts
 constexpr int SM_WAVES = SM_BLOCK / 64;
@@ -657,10 +639,10 @@ __device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int 
 // segment's own largest value.  Bound by the logits' bytes in float32 and by the
 // multiply-adds (18 instructions a logit) in 16 bits.
 template <int TYPE>
-__global__ __launch_bounds__(SM_ALL_BLOCK, LS_OCC) void sample_all_kernel(SampleCall call, SampleGrid g)
+__global__ __launch_bounds__(SM_ALL_BLOCK, 4) void sample_all_kernel(SampleCall call, SampleGrid g)
 {
     constexpr float NEG = -__builtin_inff();
-    constexpr int U = TYPE == LOGITS_F32 ? LS_U32 : LS_U16;
+    constexpr int U = TYPE == LOGITS_F32 ? 2 : 4;
     constexpr int WAVES = SM_ALL_BLOCK / 64;
     const int lane = lane_id(), wave = uniform(int(threadIdx.x >> 6));
     const int64_t r = blockIdx.x % uint32_t(call.rows);
@@ -1001,7 +983,7 @@ __device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh
         sh.n_list = 0;
     uint32_t n = 0;
     uint32_t* notes = sh.notes[wave];
-    row.template for_steps<TYPE == LOGITS_F32 ? LS_UC / 2 : LS_UC, false>(begin + wave, end, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+    row.template for_steps<TYPE == LOGITS_F32 ? 2 : 4, false>(begin + wave, end, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
         float near = __builtin_inff();
 #pragma unroll
         for (int k = 0; k < SM_VEC; ++k)
@@ -1212,7 +1194,7 @@ __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, 
     const double c1 = uniform(one * 0x1.62e42fefa3aefp-4), c2 = uniform(one * 0x1.ebfbdff82c5e7p-9);
     const double c3 = uniform(one * 0x1.c6b08d5e4bb3bp-14), c4 = uniform(one * 0x1.3b2ab6f5687a9p-19);
     const double c5 = uniform(one * 0x1.5d8dfde822453p-25), c6 = uniform(one * 0x1.430d3b3f37695p-31);
-    row.template for_steps<TYPE == LOGITS_F32 ? LS_UB / 2 : LS_UB, LS_AB>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
+    row.template for_steps<TYPE == LOGITS_F32 ? 1 : 2>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
 #pragma unroll
         for (int j = 0; j < SM_VEC; ++j) {
             const double d = row.below(x[j]);
