@@ -618,9 +618,9 @@ def radix_sort(keys: torch.Tensor, values: torch.Tensor | None = None,
 # ------------------------------------------------------------ a decoding step
 
 # A step makes these calls many times a second, each for a few microseconds of GPU work, so
-# the checks are kept to what one comparison each can tell (10 us a call with
-# torch.cuda.current_stream and a check per attribute, 6 us so); what is wrong is found out
-# after one has failed.
+# the checks are kept to what one comparison each can tell, with no helper between them and
+# the library (10 us a call with torch.cuda.current_stream and a check per attribute, 6.5 us
+# so, of which 4 are the launch); what is wrong is found out after one has failed.
 
 def _vector(t, name: str, dtype, n: int, index: int) -> int:
     """Address of a contiguous vector of n elements of `dtype` on GPU `index`."""
@@ -663,20 +663,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 if _raw_stream is None:  # pragma: no cover - a torch build without it
     def _raw_stream(index: int) -> int:
         return torch.cuda.current_stream(index).cuda_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on(index: int, name: str, call, *args) -> None:
-    """call(*args, stream) on the current stream of GPU `index`."""
-    if torch.cuda.current_device() == index:
-        st = call(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            st = call(*args, _raw_stream(index))
-    if st != LS_OK:
-        raise LibscanError(st, name)
-
-
-_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_I32, _I64, _F32, _BOOL = torch.int32, torch.int64, torch.float32, torch.bool
 
 
 def ls_sample_workspace_bytes(rows: int, vocab: int) -> int:
@@ -709,18 +699,24 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature: tor
     if code is None:
         raise TypeError(f"libscan: unsupported dtype {logits.dtype} (float32, float16, bfloat16)")
     index = logits.get_device()
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return sample_tokens(logits, uniforms, temperature, top_k, top_p, min_p, out, logprobs)
     if out is None:
         out = torch.empty(rows, dtype=torch.int64, device=logits.device)
     if logprobs is None:
         logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
     ws = _sample_workspace(index, rows, vocab)
-    _on(index, "sample_tokens", lib.sample_tokens, logits.data_ptr(), rows, vocab, stride, code,
-        _vector(uniforms, "uniforms", _F32, rows, index), _vector(temperature, "temperature", _F32, rows, index),
+    st = lib.sample_tokens(
+        logits.data_ptr(), rows, vocab, stride, code, _vector(uniforms, "uniforms", _F32, rows, index),
+        _vector(temperature, "temperature", _F32, rows, index),
         None if top_k is None else _vector(top_k, "top_k", _I32, rows, index),
         None if top_p is None else _vector(top_p, "top_p", _F32, rows, index),
         None if min_p is None else _vector(min_p, "min_p", _F32, rows, index),
         _vector(out, "out", _I64, rows, index), _vector(logprobs, "logprobs", _F32, rows, index),
-        ws.data_ptr(), ws.numel())
+        ws.data_ptr(), ws.numel(), _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, "sample_tokens")
     return out, logprobs
 
 
@@ -732,13 +728,6 @@ def _sample_workspace(index: int, rows: int, vocab: int) -> torch.Tensor:
         device = torch.device("cuda", index)
         buf = workspace_for(device, torch.cuda.current_stream(device), need, "sample")
     return buf
-
-
-def _page_size(page_size) -> int:
-    page_size = int(page_size)
-    if not 1 <= page_size < 1 << 31:
-        raise ValueError("libscan: page_size must be in [1, 2^31)")
-    return page_size
 
 
 def pages_append(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tensor, free_pages: torch.Tensor,
@@ -754,16 +743,23 @@ def pages_append(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tenso
     request.  count_out may not be free_count itself."""
     lib = _lib or load_library()
     requests, columns, stride, index = _table(tables, False)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return pages_append(lens, new_lens, tables, free_pages, free_count, page_size, count_out, granted)
     if count_out is None:
         count_out = torch.empty(1, dtype=torch.int64, device=tables.device)
     if granted is None:
         granted = torch.empty(requests, dtype=torch.bool, device=tables.device)
     capacity = free_pages.numel()
-    _on(index, "pages_append", lib.pages_append, _vector(lens, "lens", _I32, requests, index),
-        _vector(new_lens, "new_lens", _I32, requests, index), requests, tables.data_ptr(), columns, stride,
-        _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
-        _vector(free_count, "free_count", _I64, 1, index), _page_size(page_size),
-        _vector(count_out, "count_out", _I64, 1, index), _vector(granted, "granted", torch.bool, requests, index))
+    if not 1 <= page_size < 1 << 31:
+        raise ValueError("libscan: page_size must be in [1, 2^31)")
+    st = lib.pages_append(
+        _vector(lens, "lens", _I32, requests, index), _vector(new_lens, "new_lens", _I32, requests, index), requests,
+        tables.data_ptr(), columns, stride, _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
+        _vector(free_count, "free_count", _I64, 1, index), page_size, _vector(count_out, "count_out", _I64, 1, index),
+        _vector(granted, "granted", _BOOL, requests, index), _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, "pages_append")
     return count_out, granted
 
 
@@ -779,20 +775,26 @@ def slot_map(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tensor, p
     where given."""
     lib = _lib or load_library()
     requests, columns, stride, index = _table(tables, True)
-    n = int(capacity)
-    if n < 0:
-        raise ValueError("libscan: capacity must not be negative")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return slot_map(lens, new_lens, tables, page_size, capacity, out)
     if out is None:
-        device = tables.device
+        n, device = max(0, capacity), tables.device
         out = (torch.empty(n, dtype=torch.int64, device=device), torch.empty(n, dtype=torch.int32, device=device),
                torch.empty(n, dtype=torch.int32, device=device),
                torch.empty(requests + 1, dtype=torch.int64, device=device))
     slots, positions, ids, offsets = out
-    _on(index, "slot_map", lib.slot_map, _vector(lens, "lens", _I32, requests, index),
-        _vector(new_lens, "new_lens", _I32, requests, index), requests, tables.data_ptr(), columns, stride,
-        _page_size(page_size), n, _vector(slots, "slots", _I64, n, index),
-        _vector(positions, "positions", _I32, n, index), _vector(ids, "requests", _I32, n, index),
-        _vector(offsets, "offsets", _I64, requests + 1, index))
+    if capacity < 0:
+        raise ValueError("libscan: capacity must not be negative")
+    if not 1 <= page_size < 1 << 31:
+        raise ValueError("libscan: page_size must be in [1, 2^31)")
+    st = lib.slot_map(
+        _vector(lens, "lens", _I32, requests, index), _vector(new_lens, "new_lens", _I32, requests, index), requests,
+        tables.data_ptr(), columns, stride, page_size, capacity, _vector(slots, "slots", _I64, capacity, index),
+        _vector(positions, "positions", _I32, capacity, index), _vector(ids, "requests", _I32, capacity, index),
+        _vector(offsets, "offsets", _I64, requests + 1, index), _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, "slot_map")
     return slots, positions, ids, offsets
 
 
@@ -803,12 +805,19 @@ def pages_release(lens: torch.Tensor, finished: torch.Tensor, tables: torch.Tens
     number of free pages (one int64; not free_count itself)."""
     lib = _lib or load_library()
     requests, columns, stride, index = _table(tables, True)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return pages_release(lens, finished, tables, free_pages, free_count, page_size, count_out)
     if count_out is None:
         count_out = torch.empty(1, dtype=torch.int64, device=tables.device)
     capacity = free_pages.numel()
-    _on(index, "pages_release", lib.pages_release, _vector(lens, "lens", _I32, requests, index),
-        _vector(finished, "finished", torch.bool, requests, index), requests, tables.data_ptr(), columns, stride,
-        _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
-        _vector(free_count, "free_count", _I64, 1, index), _page_size(page_size),
-        _vector(count_out, "count_out", _I64, 1, index))
+    if not 1 <= page_size < 1 << 31:
+        raise ValueError("libscan: page_size must be in [1, 2^31)")
+    st = lib.pages_release(
+        _vector(lens, "lens", _I32, requests, index), _vector(finished, "finished", _BOOL, requests, index), requests,
+        tables.data_ptr(), columns, stride, _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
+        _vector(free_count, "free_count", _I64, 1, index), page_size, _vector(count_out, "count_out", _I64, 1, index),
+        _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, "pages_release")
     return count_out
