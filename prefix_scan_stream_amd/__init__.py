@@ -618,20 +618,19 @@ def radix_sort(keys: torch.Tensor, values: torch.Tensor | None = None,
 # ------------------------------------------------------------ a decoding step
 
 # A step makes these calls many times a second, each for a few microseconds of GPU work, so
-# the checks are kept to what one comparison each can tell, with no helper between them and
-# the library (10 us a call with torch.cuda.current_stream and a check per attribute, 6.5 us
-# so, of which 4 are the launch); what is wrong is found out after one has failed.
+# an entry point asks all it wants of its tensors in one expression, and goes through them
+# one by one (_vector) only to name what is wrong: 10 us a call with
+# torch.cuda.current_stream and a helper per tensor, 6 us so, of which 4 are the launch.
 
-def _vector(t, name: str, dtype, n: int, index: int) -> int:
-    """Address of a contiguous vector of n elements of `dtype` on GPU `index`."""
-    if t.dtype is dtype and t.get_device() == index and t.shape == (n,) and t.is_contiguous():
-        return t.data_ptr()
+def _vector(t, name: str, dtype, n: int, index: int) -> None:
+    """Raises unless t is a contiguous vector of n elements of `dtype` on GPU `index`."""
     _require_gpu(t)
     if t.get_device() != index:
         raise ValueError(f"libscan: {name} is on {t.device}, not on cuda:{index}")
     if t.dtype is not dtype:
         raise TypeError(f"libscan: {name} must be {dtype}, not {t.dtype}")
-    raise ValueError(f"libscan: {name} must be a contiguous vector of {n} elements")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"libscan: {name} must be a contiguous vector of {n} elements")
 
 
 def _matrix(t, name: str, overlapping: bool) -> tuple:
@@ -653,10 +652,13 @@ def _matrix(t, name: str, overlapping: bool) -> tuple:
 
 
 def _table(tables, overlapping: bool) -> tuple:
-    """(requests, columns, row stride, GPU index) of a block table."""
+    """(requests, columns, row stride) of a block table."""
     if tables.dtype is not torch.int32:
         raise TypeError(f"libscan: tables must be torch.int32, not {tables.dtype}")
-    return *_matrix(tables, "tables", overlapping), tables.get_device()
+    if tables.is_cuda and tables.dim() == 2 and tables.is_contiguous():
+        requests, columns = tables.shape
+        return requests, columns, columns
+    return _matrix(tables, "tables", overlapping)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -706,15 +708,24 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature: tor
         out = torch.empty(rows, dtype=torch.int64, device=logits.device)
     if logprobs is None:
         logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    one = (rows,)
+    if not (uniforms.dtype is _F32 and temperature.dtype is _F32 and out.dtype is _I64 and logprobs.dtype is _F32
+            and index == uniforms.get_device() == temperature.get_device() == out.get_device() == logprobs.get_device()
+            and one == uniforms.shape == temperature.shape == out.shape == logprobs.shape
+            and uniforms.is_contiguous() and temperature.is_contiguous() and out.is_contiguous()
+            and logprobs.is_contiguous()):
+        for t, name, dtype in ((uniforms, "uniforms", _F32), (temperature, "temperature", _F32), (out, "out", _I64),
+                               (logprobs, "logprobs", _F32)):
+            _vector(t, name, dtype, rows, index)
+    for t, name, dtype in ((top_k, "top_k", _I32), (top_p, "top_p", _F32), (min_p, "min_p", _F32)):
+        if t is not None and not (t.dtype is dtype and t.get_device() == index and t.shape == one and t.is_contiguous()):
+            _vector(t, name, dtype, rows, index)
     ws = _sample_workspace(index, rows, vocab)
     st = lib.sample_tokens(
-        logits.data_ptr(), rows, vocab, stride, code, _vector(uniforms, "uniforms", _F32, rows, index),
-        _vector(temperature, "temperature", _F32, rows, index),
-        None if top_k is None else _vector(top_k, "top_k", _I32, rows, index),
-        None if top_p is None else _vector(top_p, "top_p", _F32, rows, index),
-        None if min_p is None else _vector(min_p, "min_p", _F32, rows, index),
-        _vector(out, "out", _I64, rows, index), _vector(logprobs, "logprobs", _F32, rows, index),
-        ws.data_ptr(), ws.numel(), _raw_stream(index))
+        logits.data_ptr(), rows, vocab, stride, code, uniforms.data_ptr(), temperature.data_ptr(),
+        None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+        None if min_p is None else min_p.data_ptr(), out.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(index))
     if st != LS_OK:
         raise LibscanError(st, "sample_tokens")
     return out, logprobs
@@ -742,7 +753,8 @@ def pages_append(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tenso
     Returns (count_out, granted): free pages left (one int64) and a bool for each
     request.  count_out may not be free_count itself."""
     lib = _lib or load_library()
-    requests, columns, stride, index = _table(tables, False)
+    requests, columns, stride = _table(tables, False)
+    index = tables.get_device()
     if _current_device() != index:
         with torch.cuda.device(index):
             return pages_append(lens, new_lens, tables, free_pages, free_count, page_size, count_out, granted)
@@ -753,11 +765,21 @@ def pages_append(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tenso
     capacity = free_pages.numel()
     if not 1 <= page_size < 1 << 31:
         raise ValueError("libscan: page_size must be in [1, 2^31)")
-    st = lib.pages_append(
-        _vector(lens, "lens", _I32, requests, index), _vector(new_lens, "new_lens", _I32, requests, index), requests,
-        tables.data_ptr(), columns, stride, _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
-        _vector(free_count, "free_count", _I64, 1, index), page_size, _vector(count_out, "count_out", _I64, 1, index),
-        _vector(granted, "granted", _BOOL, requests, index), _raw_stream(index))
+    one = (requests,)
+    if not (lens.dtype is _I32 and new_lens.dtype is _I32 and free_pages.dtype is _I32 and free_count.dtype is _I64
+            and count_out.dtype is _I64 and granted.dtype is _BOOL
+            and index == lens.get_device() == new_lens.get_device() == free_pages.get_device()
+            == free_count.get_device() == count_out.get_device() == granted.get_device()
+            and one == lens.shape == new_lens.shape == granted.shape and free_pages.shape == (capacity,)
+            and (1,) == free_count.shape == count_out.shape and lens.is_contiguous() and new_lens.is_contiguous()
+            and free_pages.is_contiguous() and granted.is_contiguous()):
+        for t, name, dtype, n in ((lens, "lens", _I32, requests), (new_lens, "new_lens", _I32, requests),
+                                  (free_pages, "free_pages", _I32, capacity), (free_count, "free_count", _I64, 1),
+                                  (count_out, "count_out", _I64, 1), (granted, "granted", _BOOL, requests)):
+            _vector(t, name, dtype, n, index)
+    st = lib.pages_append(lens.data_ptr(), new_lens.data_ptr(), requests, tables.data_ptr(), columns, stride,
+                          free_pages.data_ptr(), capacity, free_count.data_ptr(), page_size, count_out.data_ptr(),
+                          granted.data_ptr(), _raw_stream(index))
     if st != LS_OK:
         raise LibscanError(st, "pages_append")
     return count_out, granted
@@ -774,7 +796,8 @@ def slot_map(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tensor, p
     Returns (slots, positions, requests, offsets), written into the tensors of `out`
     where given."""
     lib = _lib or load_library()
-    requests, columns, stride, index = _table(tables, True)
+    requests, columns, stride = _table(tables, True)
+    index = tables.get_device()
     if _current_device() != index:
         with torch.cuda.device(index):
             return slot_map(lens, new_lens, tables, page_size, capacity, out)
@@ -788,11 +811,22 @@ def slot_map(lens: torch.Tensor, new_lens: torch.Tensor, tables: torch.Tensor, p
         raise ValueError("libscan: capacity must not be negative")
     if not 1 <= page_size < 1 << 31:
         raise ValueError("libscan: page_size must be in [1, 2^31)")
-    st = lib.slot_map(
-        _vector(lens, "lens", _I32, requests, index), _vector(new_lens, "new_lens", _I32, requests, index), requests,
-        tables.data_ptr(), columns, stride, page_size, capacity, _vector(slots, "slots", _I64, capacity, index),
-        _vector(positions, "positions", _I32, capacity, index), _vector(ids, "requests", _I32, capacity, index),
-        _vector(offsets, "offsets", _I64, requests + 1, index), _raw_stream(index))
+    one, room = (requests,), (capacity,)
+    if not (lens.dtype is _I32 and new_lens.dtype is _I32 and slots.dtype is _I64 and positions.dtype is _I32
+            and ids.dtype is _I32 and offsets.dtype is _I64
+            and index == lens.get_device() == new_lens.get_device() == slots.get_device()
+            == positions.get_device() == ids.get_device() == offsets.get_device()
+            and one == lens.shape == new_lens.shape and room == slots.shape == positions.shape == ids.shape
+            and offsets.shape == (requests + 1,) and lens.is_contiguous() and new_lens.is_contiguous()
+            and slots.is_contiguous() and positions.is_contiguous() and ids.is_contiguous()
+            and offsets.is_contiguous()):
+        for t, name, dtype, n in ((lens, "lens", _I32, requests), (new_lens, "new_lens", _I32, requests),
+                                  (slots, "slots", _I64, capacity), (positions, "positions", _I32, capacity),
+                                  (ids, "requests", _I32, capacity), (offsets, "offsets", _I64, requests + 1)):
+            _vector(t, name, dtype, n, index)
+    st = lib.slot_map(lens.data_ptr(), new_lens.data_ptr(), requests, tables.data_ptr(), columns, stride, page_size,
+                      capacity, slots.data_ptr(), positions.data_ptr(), ids.data_ptr(), offsets.data_ptr(),
+                      _raw_stream(index))
     if st != LS_OK:
         raise LibscanError(st, "slot_map")
     return slots, positions, ids, offsets
@@ -804,7 +838,8 @@ def pages_release(lens: torch.Tensor, finished: torch.Tensor, tables: torch.Tens
     its free_count entries, in order of request and column.  Returns count_out: the new
     number of free pages (one int64; not free_count itself)."""
     lib = _lib or load_library()
-    requests, columns, stride, index = _table(tables, True)
+    requests, columns, stride = _table(tables, True)
+    index = tables.get_device()
     if _current_device() != index:
         with torch.cuda.device(index):
             return pages_release(lens, finished, tables, free_pages, free_count, page_size, count_out)
@@ -813,11 +848,21 @@ def pages_release(lens: torch.Tensor, finished: torch.Tensor, tables: torch.Tens
     capacity = free_pages.numel()
     if not 1 <= page_size < 1 << 31:
         raise ValueError("libscan: page_size must be in [1, 2^31)")
-    st = lib.pages_release(
-        _vector(lens, "lens", _I32, requests, index), _vector(finished, "finished", _BOOL, requests, index), requests,
-        tables.data_ptr(), columns, stride, _vector(free_pages, "free_pages", _I32, capacity, index), capacity,
-        _vector(free_count, "free_count", _I64, 1, index), page_size, _vector(count_out, "count_out", _I64, 1, index),
-        _raw_stream(index))
+    one = (requests,)
+    if not (lens.dtype is _I32 and finished.dtype is _BOOL and free_pages.dtype is _I32 and free_count.dtype is _I64
+            and count_out.dtype is _I64
+            and index == lens.get_device() == finished.get_device() == free_pages.get_device()
+            == free_count.get_device() == count_out.get_device()
+            and one == lens.shape == finished.shape and free_pages.shape == (capacity,)
+            and (1,) == free_count.shape == count_out.shape and lens.is_contiguous() and finished.is_contiguous()
+            and free_pages.is_contiguous()):
+        for t, name, dtype, n in ((lens, "lens", _I32, requests), (finished, "finished", _BOOL, requests),
+                                  (free_pages, "free_pages", _I32, capacity), (free_count, "free_count", _I64, 1),
+                                  (count_out, "count_out", _I64, 1)):
+            _vector(t, name, dtype, n, index)
+    st = lib.pages_release(lens.data_ptr(), finished.data_ptr(), requests, tables.data_ptr(), columns, stride,
+                           free_pages.data_ptr(), capacity, free_count.data_ptr(), page_size, count_out.data_ptr(),
+                           _raw_stream(index))
     if st != LS_OK:
         raise LibscanError(st, "pages_release")
     return count_out
