@@ -502,8 +502,8 @@ __device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t parts)
 // `per_wave` segments of seg_steps steps.
 struct SampleGrid {
     uint32_t* counters;  // one per row, 0 between calls
-    float* tops;         // rows x segs: each segment's largest value
-    double* sums;        // rows x segs: and its weights relative to that
+    float* tops;         // rows x segs: each segment's largest value, or (with cuts) x 4: that of each quarter
+    double* sums;        // rows x segs: without cuts, and its weights relative to that
     int steps, seg_steps, segs, per_wave, parts;
 };
 
@@ -567,6 +567,38 @@ struct Tops {
 #pragma unroll
         for (int k = 0; k < SM_PER_LANE; ++k)
             m = v[k] > m ? v[k] : m;
+        return read_lane(wave_inclusive_scan<MaxF32>(m), 63);
+    }
+};
+
+// With cuts: the largest values of the segments' quarters (16 lanes of each step), and of the
+// segments.
+struct QuarterTops : Tops {
+    float quarter[SM_PER_LANE][4];
+    __device__ __forceinline__ float load(const SampleGrid& g, int64_t r)
+    {
+        per_lane = (g.segs + 63) / 64;
+        float m = -__builtin_inff();
+        uint64_t w[SM_PER_LANE][2];
+#pragma unroll
+        for (int k = 0; k < SM_PER_LANE; ++k) {
+            w[k][0] = w[k][1] = 0xff800000ff800000ull;
+            if (k < per_lane && seg(k) < g.segs) {
+                const uint64_t* p = reinterpret_cast<const uint64_t*>(g.tops) + (r * g.segs + seg(k)) * 2;
+                w[k][0] = get(p);
+                w[k][1] = get(p + 1);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < SM_PER_LANE; ++k) {
+            v[k] = -__builtin_inff();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                quarter[k][q] = from_bits<float>(uint32_t(w[k][q / 2] >> (q % 2 * 32)));
+                v[k] = quarter[k][q] > v[k] ? quarter[k][q] : v[k];
+            }
+            m = v[k] > m ? v[k] : m;
+        }
         return read_lane(wave_inclusive_scan<MaxF32>(m), 63);
     }
 };
@@ -801,11 +833,11 @@ struct SharedCuts {
     double weight[SM_SMALL];
     double part_sum[SM_WAVES];
     uint64_t part_mass[SM_WAVES];
-    uint32_t n_list, n_small, n_segs, keep;
+    uint32_t n_list, n_small, n_quarters, keep;
     float top, low;
     double kept;
     Pick pick;
-    uint16_t segs[SM_SEGS];  // the segments with candidates
+    uint16_t quarters[SM_SEGS * 4];  // segment * 4 + quarter: those with candidates
 };
 
 // write(place, x[k], k) for each element with in(x[k], k), places counted on from a shared
@@ -1347,10 +1379,11 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
 
 // One wave: where the candidates of a row begin.  few: at most the k-th largest logit, which is the
 // k-th largest of the segments' largest values to 16 bits of its key; else a little below the
-// smallest logit that min-p may keep.  The segments with candidates go into sh.segs.
+// smallest logit that min-p may keep.  The segments' quarters with candidates go into
+// sh.quarters (a quarter is the most that is read for one candidate).
 template <int TYPE>
 __device__ __forceinline__ void find_segments(const SampleGrid& g, const Row<TYPE>& row, SharedCuts& sh,
-                                              const Tops& tops, bool few, uint32_t k, double least)
+                                              const QuarterTops& tops, bool few, uint32_t k, double least)
 {
     float low;
     if (few) {
@@ -1387,14 +1420,19 @@ __device__ __forceinline__ void find_segments(const SampleGrid& g, const Row<TYP
     uint32_t flags = 0;
 #pragma unroll
     for (int j = 0; j < SM_PER_LANE; ++j)
-        flags |= clean(tops.v[j], row.inf) >= low ? 1u << j : 0u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            flags |= clean(tops.quarter[j][q], row.inf) >= low ? 1u << (j * 4 + q) : 0u;
+    static_assert(SM_PER_LANE * 4 <= 32, "a lane's quarters are bits of one word");
     const uint32_t mine = uint32_t(__builtin_popcount(flags));
     const uint32_t incl = wave_inclusive_scan<SumU32>(mine);
     uint32_t q = incl - mine;
-    for (; flags != 0; flags &= flags - 1)
-        sh.segs[q++] = uint16_t(tops.seg(__builtin_ctz(flags)));
+    for (; flags != 0; flags &= flags - 1) {
+        const int bit = __builtin_ctz(flags);
+        sh.quarters[q++] = uint16_t(tops.seg(bit / 4) * 4 + bit % 4);
+    }
     if (lane_id() == 63)
-        sh.n_segs = incl;
+        sh.n_quarters = incl;
     sh.low = low;
 }
 
@@ -1410,33 +1448,35 @@ __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const Sam
     const float low = uniform(sh.low);
     const uint32_t key_hi = key_of(row.top);
     constexpr int U = TYPE == LOGITS_F32 ? 2 : 4;
-    const int todo = int(uniform(sh.n_segs)) * g.seg_steps;
+    // four quarters to a load of the wave, 16 lanes each
+    const int quarters = int(uniform(sh.n_quarters)), todo = (quarters + 3) / 4 * g.seg_steps;
     for (int i = wave; i < todo; i += U * SM_WAVES) {
         Raw<TYPE> raw[U];
-        int step[U];
+        uint32_t idx[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int q = i + j * SM_WAVES;
-            step[j] = g.steps;
-            if (q < todo) {
-                const int seg = g.seg_steps == 1 ? q : q / g.seg_steps;
-                step[j] = uniform(int(sh.segs[seg])) * g.seg_steps + (q - seg * g.seg_steps);
+            const int t = i + j * SM_WAVES, four = g.seg_steps == 1 ? t : t / g.seg_steps;
+            const int q = four * 4 + int(lane >> 4);
+            raw[j].clear();
+            idx[j] = 0;
+            if (t < todo && q < quarters) {
+                const int at = sh.quarters[q], step = (at >> 2) * g.seg_steps + (t - four * g.seg_steps);
+                idx[j] = uint32_t(step) * SM_STEP + uint32_t(at & 3) * (SM_STEP / 4) + (lane & 15) * SM_VEC;
+                if (idx[j] < row.vocab)
+                    raw[j].load(row.p, idx[j], row.vocab);
             }
-            if (step[j] < g.steps)
-                raw[j].load_step(row.p, step[j], row.vocab);
-            else
-                raw[j].clear();
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
+            if (i + j * SM_WAVES >= todo)
+                break;
             float x[SM_VEC];
             raw[j].unpack(x, row.inf);
             wave_append(
                 &sh.n_small, x, [&](float v, int) { return v >= low; },
                 [&](uint32_t at, float v, int m) {
                     if (at < SM_SMALL)
-                        sh.small[at] = place_of(row, key_hi, key_of(v),
-                                                uint32_t(step[j]) * SM_STEP + lane * SM_VEC + uint32_t(m));
+                        sh.small[at] = place_of(row, key_hi, key_of(v), idx[j] + uint32_t(m));
                 });
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -1546,9 +1586,9 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int seg = (part * g.per_wave + i + u) * SM_WAVES + wave;
-            const float m = wave_inclusive_scan<MaxF32>(top[u]);
-            if (lane == 63 && i + u < g.per_wave && seg < g.segs)
-                put(&g.tops[r * g.segs + seg], m);
+            const float m = row16_inclusive_scan<MaxF32>(top[u]);
+            if ((lane & 15) == 15 && i + u < g.per_wave && seg < g.segs)
+                put(&g.tops[(r * g.segs + seg) * 4 + (lane >> 4)], m);
         }
     }
     stores_done();
@@ -1575,7 +1615,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
     const bool candidates = few || (p >= 1.0 && least > 0.0);
     // one wave (the others would only take its turns), then all
     if (wave == 0) {
-        Tops tops;
+        QuarterTops tops;
         const float top = tops.load(g, r);
         const bool done = settle(call, g, r, row, tops, top);
         sh.n_small = 0, sh.s.found = ~0u, sh.s.last = 0;
@@ -1602,7 +1642,8 @@ static int64_t row_segs(int64_t vocab)
     return steps < SM_SEGS ? steps : SM_SEGS;
 }
 
-// header | a counter for each row of a launch | the segments' largest values | their sums.
+// header | a counter for each row of a launch | 16 bytes for each segment: the segments' sums and
+// behind them their largest values, or their quarters' largest values.
 // The counters' place is the same for every call, so that nothing else is ever written
 // there and they stay 0 between calls of any sizes.
 static size_t row_cells(int64_t rows, int64_t vocab)
@@ -1613,7 +1654,7 @@ static size_t row_cells(int64_t rows, int64_t vocab)
 size_t sample_workspace_bytes(int64_t rows, int64_t vocab)
 {
     const size_t cells = row_cells(rows, vocab);
-    return 256 + SM_ROWS * SM_COUNTER * 4 + round256(cells * 4) + round256(cells * 8);
+    return 256 + SM_ROWS * SM_COUNTER * 4 + round256(cells * 16);
 }
 
 template <int TYPE>
@@ -1656,9 +1697,8 @@ hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t
     char* at = static_cast<char*>(ws) + 256;
     g.counters = reinterpret_cast<uint32_t*>(at);
     at += SM_ROWS * SM_COUNTER * 4;
-    g.tops = reinterpret_cast<float*>(at);
-    at += round256(row_cells(call.rows, call.vocab) * 4);
     g.sums = reinterpret_cast<double*>(at);
+    g.tops = reinterpret_cast<float*>(cuts ? at : at + size_t(rows) * size_t(g.segs) * 8);
     SampleCall now = call;
     for (int64_t r = 0; r < call.rows; r += rows) {
         now.rows = call.rows - r < rows ? call.rows - r : rows;
