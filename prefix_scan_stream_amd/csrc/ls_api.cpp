@@ -214,7 +214,9 @@ size_t matrix_bytes(int64_t rows, int64_t columns, int64_t stride, size_t size)
 // `broadcast` allows it), within the address range.
 bool matrix_ok(int64_t rows, int64_t columns, int64_t stride, bool broadcast)
 {
-    if (!count_ok(rows) || !count_ok(columns) || stride < 0 || stride > LS_MAX_N)
+    if (!count_ok(rows) || !count_ok(columns) || stride < 0)
+        return false;
+    if (rows > 1 && stride > (INT64_MAX / 16 - columns) / (rows - 1))
         return false;
     return rows <= 1 || stride >= columns || (broadcast && stride == 0);
 }

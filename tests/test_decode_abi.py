@@ -56,6 +56,15 @@ def test_sample_workspace(lib):
         ps.ls_sample_workspace_bytes(-1, 5)
 
 
+def test_strides_past_the_address_range(lib):
+    """(rows - 1) * stride elements must not wrap round to a small matrix."""
+    for rows, stride in ((1 << 30, 1 << 40), ((1 << 24) + 1, 1 << 40), (3, 1 << 62), (2, (1 << 63) - 1)):
+        assert status(lib, "sample_tokens", SAMPLE, rows=rows, stride=stride) == INV
+        assert status(lib, "slot_map", SLOTS, requests=rows, stride=stride) == INV
+        assert status(lib, "pages_append", APPEND, requests=rows, stride=stride) == INV
+        assert status(lib, "pages_release", RELEASE, requests=rows, stride=stride) == INV
+
+
 COMMON = [dict(requests=-1), dict(requests=1 << 31), dict(columns=-1), dict(columns=1 << 31), dict(stride=9),
           dict(stride=-1), dict(page=0), dict(page=-16), dict(page=1 << 31), dict(lens=None), dict(lens=A[0] + 2),
           dict(tables=None), dict(tables=A[2] + 2)]

@@ -142,6 +142,28 @@ def test_masked(dtype):
         check(x, u[::-1].copy(), t, m=np.full(12, 1e-4))
 
 
+NAN_BITS = {"f32": (0x7F800001, 0x7FC00000, -0x7FFFFF, -0x400000), "f16": (0x7C01, 0x7E00, -0x3FF, -0x200),
+            "bf16": (0x7F81, 0x7FC0, -0x7F, -0x40)}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_every_kind_of_nan(dtype):
+    """NaN of both signs, quiet and signalling, among other logits and all over a row."""
+    x = rows_of(6, 9001, DTYPES[dtype], 55)
+    ints = x.view(torch.int32 if dtype == "f32" else torch.int16)
+    where = np.random.default_rng(5).random((6, 9001)) < 0.3
+    which = np.random.default_rng(6).choice(NAN_BITS[dtype], (6, 9001))
+    ints[torch.tensor(where, device=DEV)] = torch.tensor(which[where], device=DEV).to(ints.dtype)
+    ints[3] = torch.tensor(which[3], device=DEV).to(ints.dtype)
+    u, t = uniforms(6, 8), [1.0, 0.7, 1.3, 1.0, 0.0, 0.9]
+    assert bool(x[3].isnan().all()) and int(x[0].isnan().sum()) > 1000
+    check(x, u, t)
+    check(x, u, t, k=np.full(6, 9))
+    check(x, u, t, k=np.full(6, 4000), p=np.full(6, 0.9))
+    check(x, u, t, p=np.full(6, 0.8), m=np.full(6, 0.001))
+    check(x, u, t, m=np.full(6, 0.01))
+
+
 def test_infinite_logits():
     """+inf logits share everything; the first of them is the greedy choice."""
     x = rows_of(4, 700, torch.float32, 4)
