@@ -13,20 +13,31 @@
 //
 // Neighbouring sums of a row lie about 2^-17 Z apart and u has 24 bits, so sums in 32
 // bits would pick another token in some percents of the rows.  Weights and sums are in
-// 64 bits: a double multiply-add issues at the rate of a single one on this GPU, and 2^f
-// is a polynomial of degree 10.
+// 64 bits: a double multiply-add issues at the rate of a single one here (5.5 cycles a
+// wave and SIMD against 5.3, measured), and 2^f is a polynomial: of degree 10 where single
+// weights count (exp2_poly, 2^-50.6), of degree 9 in the sums of a whole row (exp2_sum4,
+// 2^-44.6), of degree 6 in the bins (fill_bins, 2^-48.9).
 //
 // One launch.  A row is cut into segments, and its segments are shared out to blocks, so
 // that few rows still use the whole GPU.  Every block leaves what its segments hold in
 // the workspace; the block of a row that arrives last at the row's counter goes on alone.
-//   No cuts: the segments hold their largest value and the sum of their weights (relative
-//   to it).  The last block has the running sums of the segments, so it knows the one
-//   the token lies in, and reads only that again.
-//   Cuts: the segments hold their largest value.  The k-th largest of these values is at
-//   most the k-th largest logit, so for a small k the candidates are the elements at or
-//   above it, which lie in about k segments: these are read again and a few more than k
-//   elements sorted in LDS.  min-p alone has its threshold from M the same way.
-//   Otherwise the cut is found by value without sorting the row (cut_row below).
+//   No cuts (sample_all_kernel): the segments hold the sum of their weights, relative to a
+//   value of theirs.  The last block has the running sums of the segments, so it knows the
+//   one the token lies in, and reads only that again.
+//   Cuts (sample_cut_kernel): the segments hold the largest values of their quarters.  The
+//   k-th largest of the segments' values is at most the k-th largest logit, so for a small
+//   k the candidates are the elements at or above it, which lie in a few more than k quarters:
+//   these are read again and ordered in LDS.  min-p alone has its threshold from M the
+//   same way.  Otherwise the cut is found by value without sorting the row (cut_row).
+//
+// Measured, in a graph, 131072 logits to a row:
+//   1 row, bfloat16, top-k 50, top-p, min-p: 12.2 us, the latency of the chain of steps: 2 us the launch, 2 the
+//   first read, 1 the counter, 4.5 one wave's search for the candidates' quarters, 2 their reading, 3 order
+//   and sums.  64 rows, top-k 100, top-p, min-p: 15.9 us.
+//   256 rows, bfloat16, top-p alone: 69 us, a row to a CU: 11 us the first read (6 TB/s over all), 25 the bins
+//   (16.5 vector instructions a logit), 14 the bin's elements, the rest the steps between.
+//   512 rows, no cuts: bfloat16 51 us, bound by vector instructions (22 a logit, 50 us at the measured rate);
+//   float32 58-62 us, with 268 MB to read beside them (4.5 TB/s).
 #include <type_traits>
 
 #include "ls_device.hpp"
@@ -34,13 +45,12 @@
 
 namespace ls {
 
-
 constexpr int SM_BLOCK = 1024;              // threads of a block that makes cuts
 constexpr int SM_WAVES = SM_BLOCK / 64;
 constexpr int SM_ALL_BLOCK = 256;           // without cuts
 constexpr int SM_VEC = 8;                   // consecutive logits per lane and step
 constexpr int SM_STEP = 64 * SM_VEC;        // consecutive logits per wave and step
-constexpr int SM_PER_LANE = 8;
+constexpr int SM_PER_LANE = 8;              // segments of a row that one lane of a wave takes
 constexpr int SM_SEGS = 64 * SM_PER_LANE;   // most segments of a row
 constexpr int SM_PER_OCTAVE = 8;            // bins per halving of the weight
 constexpr int SM_BINS = 512;
@@ -48,7 +58,7 @@ constexpr int SM_RANGES = 256;              // ranges of a refinement
 constexpr int SM_LIST = 4096;               // elements of one bin kept in LDS
 constexpr int SM_NOTES = 256;               // loads of one wave that hold such elements
 constexpr int SM_SMALL = 512;               // elements that are ordered by counting
-constexpr int SM_CUS = 256;
+constexpr int SM_CUS = 256;                 // of an MI355X
 constexpr int SM_ROWS = 4096;               // most rows of a launch
 constexpr int SM_COUNTER = 32;              // 32-bit words from one row's counter to the next
 
