@@ -58,9 +58,20 @@ constexpr int SM_RANGES = 256;              // ranges of a refinement
 constexpr int SM_LIST = 4096;               // elements of one bin kept in LDS
 constexpr int SM_NOTES = 256;               // loads of one wave that hold such elements
 constexpr int SM_SMALL = 512;               // elements that are ordered by counting
+// More than these of a bin are divided by value once more before that, since counting takes the square
+// of their number (512: 12 us, one division 3).  Top-p alone, 4 rows of 32000: 26.1 us with 64 or 128,
+// 26.3 with 256, 38.5 with 512; 131072: 53.7, 50.6, 50.0, 48.8.
+constexpr int SM_FEW = 256;
 constexpr int SM_CUS = 256;                 // of an MI355X
 constexpr int SM_ROWS = 4096;               // most rows of a launch
 constexpr int SM_COUNTER = 32;              // 32-bit words from one row's counter to the next
+// Most rows, and least steps of a row, for its bins to be made by SM_WAVES blocks in a launch of their
+// own (sample_bins_kernel), which costs about 8 us and divides the bins' time by the waves.  Top-p alone,
+// bfloat16, with it against without: 131072 logits 1 row 40.2 against 49.8 us, 32 rows 44.0 against 50.9,
+// 64 rows 51.7 both, 128 rows 72 against 55; 64000 logits 1 row 31.5 against 32.8, 32 rows 34.4
+// against 33.8; 32000 logits 1 row 27.8 against 25.7.
+constexpr int SM_SPLIT_ROWS = 32;
+constexpr int SM_SPLIT_STEPS = 128;
 
 constexpr double LOG2E = 0x1.71547652b82fep+0, LN2 = 0x1.62e42fefa39efp-1;
 constexpr double TO_INT = 0x1.8p52;  // adding it rounds to the nearest integer, into the low word
@@ -514,7 +525,10 @@ struct SampleGrid {
     uint32_t* counters;  // one per row, 0 between calls
     float* tops;         // rows x segs: each segment's largest value, or (with cuts) x 4: that of each quarter
     double* sums;        // rows x segs: without cuts, and its weights relative to that
+    float* split_tops;   // rows: the largest value where sample_bins_kernel makes the cut, else NaN
+    uint64_t* masses;    // rows x SM_WAVES x SM_BINS: the bins of each sixteenth of a row
     int steps, seg_steps, segs, per_wave, parts;
+    bool split;
 };
 
 template <int TYPE>
@@ -890,8 +904,15 @@ __device__ __forceinline__ void order_small(SharedCuts& sh, uint32_t n)
     uint32_t rank = 0;
     const uint64_t v = e < n ? sh.small[e] : 0;
     if (e < n)
-        for (uint32_t j = part; j < n; j += group)
-            rank += sh.small[j] < v ? 1u : 0u;
+        for (uint32_t j = part; j < n; j += 4 * group) {
+            uint64_t w[4];  // four at a time on their way
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                w[i] = sh.small[(j + i * group) % SM_SMALL];
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                rank += j + i * group < n && w[i] < v ? 1u : 0u;
+        }
     for (uint32_t d = 1; d < group; d <<= 1)
         rank += __shfl_xor(rank, int(d));
     if (e < n && part == 0)
@@ -1001,6 +1022,15 @@ __device__ __forceinline__ uint32_t index_at(const Row<TYPE>& row, uint64_t plac
     return uint32_t(place) & ((1u << row.index_bits) - 1u);
 }
 
+__device__ __forceinline__ float choose(const float (&x)[SM_VEC], uint32_t k)
+{
+    float v = x[0];
+#pragma unroll
+    for (uint32_t i = 1; i < SM_VEC; ++i)
+        v = k == i ? x[i] : v;
+    return v;
+}
+
 // Collects a bin's elements with a place in [lo, hi] into the list; their number, or more than
 // SM_LIST where they are too many.  First each wave notes which lanes' loads hold any of them
 // (one test for eight elements: few hold any), then it reads only these again.
@@ -1074,12 +1104,8 @@ __device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh
             while (in != 0) {
                 const uint32_t k = uint32_t(__builtin_ctz(in));
                 in &= in - 1;
-                float v = x[0];
-#pragma unroll
-                for (uint32_t i = 1; i < SM_VEC; ++i)
-                    v = k == i ? x[i] : v;
                 if (at < SM_LIST)
-                    sh.list[at] = place_of(row, bin.key_hi, key_of(v), note[u] + k);
+                    sh.list[at] = place_of(row, bin.key_hi, key_of(choose(x, k)), note[u] + k);
                 ++at;
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -1113,7 +1139,7 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
             listed = first && in_list;
             first = false;
         }
-        if (in_list && n <= SM_SMALL)
+        if (in_list && n <= SM_FEW)
             break;
         const uint64_t span = hi - lo;
         const int bits = 64 - __builtin_clzll(span | 1u);
@@ -1139,13 +1165,18 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
         } else {
             const float x_lo = value_of(bin.key_lo), x_hi = value_of(bin.key_hi);
             row.template for_steps<1>(int(tid >> 6), row.steps, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+                uint32_t in = 0;
 #pragma unroll
-                for (int k = 0; k < SM_VEC; ++k) {
-                    if (x[k] >= x_lo && x[k] <= x_hi) {
-                        const uint64_t v = place_of(row, bin.key_hi, key_of(x[k]), idx + k);
-                        if (v >= lo && v <= hi)
-                            add(v, x[k]);
-                    }
+                for (uint32_t k = 0; k < SM_VEC; ++k)
+                    in |= x[k] >= x_lo && x[k] <= x_hi ? 1u << k : 0u;
+                // few lanes have more than one or two: as many turns as the one with the most
+                while (in != 0) {
+                    const uint32_t k = uint32_t(__builtin_ctz(in));
+                    in &= in - 1;
+                    const float y = choose(x, k);
+                    const uint64_t v = place_of(row, bin.key_hi, key_of(y), idx + k);
+                    if (v >= lo && v <= hi)
+                        add(v, y);
                 }
             });
         }
@@ -1265,8 +1296,8 @@ __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, 
 // integers, so that sums do not depend on the order of the atomics.
 // Each wave takes a sixteenth of the row and keeps its own bins: with the cut known, the
 // kept weight of each sixteenth is known too, and only the one with the token is read
-// for the running sums.
-template <int TYPE>
+// for the running sums.  FILLED: the bins of the sixteenths are there (sample_bins_kernel).
+template <bool FILLED, int TYPE>
 __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const Row<TYPE>& row, SharedCuts& sh,
                                         uint32_t k, double p, double least)
 {
@@ -1278,8 +1309,9 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
     Bin bin{0, 0, 0};
     uint64_t place = 0;
     if (by_k || by_p) {
-        for (int i = lane; i < SM_BINS; i += 64)
-            sh.mass[wave][i] = 0;
+        if (!FILLED)
+            for (int i = lane; i < SM_BINS; i += 64)
+                sh.mass[wave][i] = 0;
         if (tid < SM_BINS) {
             sh.bin_count[tid] = 0;
             sh.bin_weight[tid] = exp2_exact(-double(tid) / SM_PER_OCTAVE - double(row.frac));
@@ -1287,12 +1319,14 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
         if (tid < SM_WAVES)
             sh.part_mass[tid] = 0;
         __syncthreads();
-        const int first = wave * share, end = first + share < row.steps ? first + share : row.steps;
-        if (by_k)
-            fill_bins<true>(row, sh.mass[wave], sh.bin_count, first, end);
-        else
-            fill_bins<false>(row, sh.mass[wave], sh.bin_count, first, end);
-        __syncthreads();
+        if (!FILLED) {
+            const int first = wave * share, end = first + share < row.steps ? first + share : row.steps;
+            if (by_k)
+                fill_bins<true>(row, sh.mass[wave], sh.bin_count, first, end);
+            else
+                fill_bins<false>(row, sh.mass[wave], sh.bin_count, first, end);
+            __syncthreads();
+        }
         if (tid < SM_BINS) {
             uint64_t m = 0;
 #pragma unroll
@@ -1562,6 +1596,18 @@ __device__ __forceinline__ bool cut_candidates(const SampleCall& call, const Sam
     return true;
 }
 
+// What top-p and min-p ask for in row r.
+__device__ __forceinline__ double share_of(const SampleCall& call, int64_t r)
+{
+    const double p = call.top_p != nullptr ? double(call.top_p[r]) : 1.0;
+    return uniform(p > 0.0 ? p : 0.0);
+}
+__device__ __forceinline__ double least_of(const SampleCall& call, int64_t r)
+{
+    const float p = call.min_p != nullptr ? call.min_p[r] : 0.0f;
+    return uniform(p > 0.0f ? __builtin_fmin(double(p), 1.0) : 0.0);
+}
+
 template <int TYPE>
 __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, SampleGrid g)
 {
@@ -1614,14 +1660,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
     uint32_t k = ~0u;
     if (call.top_k != nullptr && call.top_k[r] > 0)
         k = uint32_t(call.top_k[r]);
-    double p = 1.0;
-    if (call.top_p != nullptr) {
-        p = double(call.top_p[r]);
-        p = uniform(p > 0.0 ? p : 0.0);
-    }
-    double least = 0.0;
-    if (call.min_p != nullptr && call.min_p[r] > 0.0f)
-        least = uniform(__builtin_fmin(double(call.min_p[r]), 1.0));
+    const double p = share_of(call, r), least = least_of(call, r);
     // few enough that the k-th largest of the segments' values leaves few candidates
     const bool few = uint64_t(k) * 4 <= uint64_t(g.segs) * 3;
     const bool candidates = few || (p >= 1.0 && least > 0.0);
@@ -1631,8 +1670,11 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
         const float top = tops.load(g, r);
         const bool done = settle(call, g, r, row, tops, top);
         sh.n_small = 0, sh.s.found = ~0u, sh.s.last = 0;
-        sh.s.arrived = done ? 0u : 1u;
+        const bool later = !done && g.split && p < 1.0;
+        sh.s.arrived = done || later ? 0u : 1u;
         sh.top = top;
+        if (g.split && lane == 0)
+            g.split_tops[r] = later ? top : __builtin_nanf("");
         if (!done && candidates)
             find_segments(g, row, sh, tops, few, k, least);
     }
@@ -1642,7 +1684,54 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
     row.set_top(uniform(sh.top));
     row.set_temperature(call.temperature[r]);
     if (!(candidates && cut_candidates(call, g, r, row, sh, k, p, least)))
-        cut_row(call, r, row, sh, k, p, least);
+        cut_row<false>(call, r, row, sh, k, p, least);
+}
+
+// A second launch for few rows with top-p alone: the rows' bins, each sixteenth of a row by a block,
+// and the cut by the row's last one.  The bins are integers, so they are those that one block makes.
+template <int TYPE>
+__global__ __launch_bounds__(SM_BLOCK) void sample_bins_kernel(SampleCall call, SampleGrid g)
+{
+    __shared__ SharedCuts sh;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int64_t r = blockIdx.x % uint32_t(call.rows);
+    const int part = int(blockIdx.x / uint32_t(call.rows));
+    const float top = uniform(g.split_tops[r]);
+    if (top != top)
+        return;
+    Row<TYPE> row = make_row<TYPE>(call, g, r);
+    row.set_top(top);
+    row.set_temperature(call.temperature[r]);
+    for (int i = lane; i < SM_BINS; i += 64)
+        sh.mass[wave][i] = 0;
+    __syncthreads();
+    // a sixteenth of the row, as in cut_row, and a sixteenth of that to a wave
+    const int share = (row.steps + SM_WAVES - 1) / SM_WAVES, begin = part * share;
+    const int end = begin + share < row.steps ? begin + share : row.steps;
+    const int per = (share + SM_WAVES - 1) / SM_WAVES, first = begin + wave * per;
+    fill_bins<false>(row, sh.mass[wave], sh.bin_count, first, first + per < end ? first + per : end);
+    __syncthreads();
+    uint64_t* const masses = g.masses + r * (SM_WAVES * SM_BINS);
+    if (tid < SM_BINS) {
+        uint64_t m = 0;
+#pragma unroll
+        for (int w = 0; w < SM_WAVES; ++w)
+            m += sh.mass[w][tid];
+        put(&masses[part * SM_BINS + tid], m);
+    }
+    stores_done();
+    __syncthreads();
+    if (tid == 0) {
+        sh.s.arrived = count_in(&g.counters[r * SM_COUNTER], uint32_t(SM_WAVES)) ? 1u : 0u;
+        sh.n_small = 0, sh.s.found = ~0u, sh.s.last = 0;
+    }
+    __syncthreads();
+    if (uniform(sh.s.arrived) == 0u)
+        return;
+#pragma unroll
+    for (int i = 0; i < SM_WAVES * SM_BINS / SM_BLOCK; ++i)
+        (&sh.mass[0][0])[i * SM_BLOCK + tid] = get(&masses[i * SM_BLOCK + tid]);
+    cut_row<true>(call, r, row, sh, ~0u, share_of(call, r), least_of(call, r));
 }
 
 // ---------------------------------------------------------------- host side
@@ -1655,28 +1744,34 @@ static int64_t row_segs(int64_t vocab)
 }
 
 // header | a counter for each row of a launch | 16 bytes for each segment: the segments' sums and
-// behind them their largest values, or their quarters' largest values.
-// The counters' place is the same for every call, so that nothing else is ever written
+// behind them their largest values, or their quarters' largest values | the largest value and the
+// bins of the rows that sample_bins_kernel may take.  The counters' place is the same for every call, so that nothing else is ever written
 // there and they stay 0 between calls of any sizes.
 static size_t row_cells(int64_t rows, int64_t vocab)
 {
     return size_t(rows < SM_ROWS ? rows : SM_ROWS) * size_t(row_segs(vocab));
 }
 
+constexpr size_t SM_MASSES = size_t(SM_WAVES) * SM_BINS * 8;  // bytes of a row
+static size_t split_rows(int64_t rows) { return size_t(rows < SM_SPLIT_ROWS ? rows : SM_SPLIT_ROWS); }
+
 size_t sample_workspace_bytes(int64_t rows, int64_t vocab)
 {
     const size_t cells = row_cells(rows, vocab);
-    return 256 + SM_ROWS * SM_COUNTER * 4 + round256(cells * 16);
+    return 256 + SM_ROWS * SM_COUNTER * 4 + round256(cells * 16) + SM_SPLIT_ROWS * 4 + split_rows(rows) * SM_MASSES;
 }
 
 template <int TYPE>
 static void launch_type(const SampleCall& call, const SampleGrid& g, bool cuts, hipStream_t stream)
 {
     const dim3 grid(unsigned(call.rows * g.parts));
-    if (cuts)
+    if (cuts) {
         sample_cut_kernel<TYPE><<<grid, SM_BLOCK, 0, stream>>>(call, g);
-    else
+        if (g.split)
+            sample_bins_kernel<TYPE><<<dim3(unsigned(call.rows * SM_WAVES)), SM_BLOCK, 0, stream>>>(call, g);
+    } else {
         sample_all_kernel<TYPE><<<grid, SM_ALL_BLOCK, 0, stream>>>(call, g);
+    }
 }
 
 hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t stream)
@@ -1711,6 +1806,10 @@ hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t
     at += SM_ROWS * SM_COUNTER * 4;
     g.sums = reinterpret_cast<double*>(at);
     g.tops = reinterpret_cast<float*>(cuts ? at : at + size_t(rows) * size_t(g.segs) * 8);
+    at += round256(row_cells(call.rows, call.vocab) * 16);
+    g.split_tops = reinterpret_cast<float*>(at);
+    g.masses = reinterpret_cast<uint64_t*>(at + SM_SPLIT_ROWS * 4);
+    g.split = call.top_p != nullptr && call.top_k == nullptr && call.rows <= SM_SPLIT_ROWS && g.steps >= SM_SPLIT_STEPS;
     SampleCall now = call;
     for (int64_t r = 0; r < call.rows; r += rows) {
         now.rows = call.rows - r < rows ? call.rows - r : rows;
