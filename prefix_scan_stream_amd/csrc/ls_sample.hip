@@ -34,8 +34,9 @@
 //   1 row, bfloat16, top-k 50, top-p, min-p: 12.2 us, the latency of the chain of steps: 2 us the launch, 2 the
 //   first read, 1 the counter, 4.5 one wave's search for the candidates' quarters, 2 their reading, 3 order
 //   and sums.  64 rows, top-k 100, top-p, min-p: 15.9 us.
-//   256 rows, bfloat16, top-p alone: 68 us, a row to a CU: 11 us the first read (6 TB/s over all), 25 the bins
+//   256 rows, bfloat16, top-p alone: 66 us, a row to a CU: 11 us the first read (6 TB/s over all), 25 the bins
 //   (16.5 vector instructions a logit), 14 the bin's elements, the rest the steps between.
+//   64 rows of flat logits (normal, a deviation of 0.5), top-p: 77 us, with two more readings for a bin of 13000.
 //   512 rows, no cuts: bfloat16 51 us, bound by vector instructions (22 a logit, 50 us at the measured rate);
 //   float32 58-62 us, with 268 MB to read beside them (4.5 TB/s).
 #include <type_traits>
@@ -839,7 +840,7 @@ struct Bin {
 
 struct Pick {
     Bin bin;
-    uint32_t above_count, reached;
+    uint32_t above_count, reached, about;
     double above, goal;
 };
 
@@ -1022,12 +1023,16 @@ __device__ __forceinline__ uint32_t index_at(const Row<TYPE>& row, uint64_t plac
     return uint32_t(place) & ((1u << row.index_bits) - 1u);
 }
 
+// x[k].  The values pass through an empty asm, or the compiler would index x itself, in memory.
 __device__ __forceinline__ float choose(const float (&x)[SM_VEC], uint32_t k)
 {
     float v = x[0];
 #pragma unroll
-    for (uint32_t i = 1; i < SM_VEC; ++i)
-        v = k == i ? x[i] : v;
+    for (uint32_t i = 1; i < SM_VEC; ++i) {
+        float y = x[i];
+        asm("" : "+v"(y));
+        v = k == i ? y : v;
+    }
     return v;
 }
 
@@ -1121,23 +1126,30 @@ __device__ __forceinline__ uint32_t collect(const Row<TYPE>& row, SharedCuts& sh
 // one the cut lies in is kept.  A range is a power of two of places and starts at a multiple
 // of it, so it is whole values, or indexes of one value.  At most eight bits of 64 go at a
 // time, and one place is one element, so eight rounds and the one that collects suffice.
-// Returns the place; `weight`: the weight up to and including it; `listed`:
-// whether the list holds the whole bin.
+// `n`: about how many elements the bin holds.  Returns the place; `weight`: the weight up to and
+// including it; `whole`: whether the list holds the whole bin.  What the bin holds before the list's range is
+// left in sh.part_mass for each sixteenth of the row.
 template <int TYPE>
 __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts& sh, const Bin& bin, bool by_count,
                                                uint32_t want, double goal, uint32_t above_count, double above,
-                                               double& weight, bool& listed)
+                                               uint32_t n, double& weight, bool& whole)
 {
-    const uint32_t tid = threadIdx.x;
-    uint64_t lo = 0, hi = place_of(row, bin.key_hi, bin.key_lo, (1u << row.index_bits) - 1u);
-    uint32_t n = 0;
-    bool in_list = false, first = true;
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(int(tid >> 6));
+    const uint64_t all = place_of(row, bin.key_hi, bin.key_lo, (1u << row.index_bits) - 1u);
+    uint64_t lo = 0, hi = all;
+    bool in_list = false;
+    uint64_t* const masses = &sh.list[wave * SM_RANGES];  // of the ranges in a sixteenth, while there is no list
+    static_assert(SM_LIST >= SM_WAVES * SM_RANGES, "room in the list");
+    whole = false;
+    if (tid < SM_WAVES)
+        sh.part_mass[tid] = 0;
     for (int round = 0; round < 10; ++round) {
         if (!in_list && n <= SM_LIST) {
+            whole = lo == 0 && hi == all;
             n = collect(row, sh, bin, lo, hi);
             in_list = n <= SM_LIST;
-            listed = first && in_list;
-            first = false;
+            whole = whole && in_list;
         }
         if (in_list && n <= SM_FEW)
             break;
@@ -1149,22 +1161,26 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
             sh.range_mass[tid] = 0;
             sh.range_count[tid] = 0;
         }
+        if (!in_list)
+            for (uint32_t i = lane; i < SM_RANGES; i += 64)
+                masses[i] = 0;
         __syncthreads();
-        const auto add = [&](uint64_t v, float x) {
+        const auto add = [&](uint64_t v, float x, uint64_t* mass) {
             const uint32_t b = uint32_t((v - lo) >> shift);
             atomicAdd(&sh.range_count[b], 1u);
-            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.range_mass[b]),
+            atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
                       static_cast<unsigned long long>(row.fixed(row.below(x), bin.bin)));
         };
         if (in_list) {
             for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
                 const uint64_t v = sh.list[i];
                 if (v >= lo && v <= hi)
-                    add(v, value_of(key_at(row, bin.key_hi, v)));
+                    add(v, value_of(key_at(row, bin.key_hi, v)), sh.range_mass);
             }
         } else {
-            const float x_lo = value_of(bin.key_lo), x_hi = value_of(bin.key_hi);
-            row.template for_steps<1>(int(tid >> 6), row.steps, SM_WAVES, [&](const float(&x)[SM_VEC], uint32_t idx) {
+            const float x_lo = value_of(key_at(row, bin.key_hi, hi)), x_hi = value_of(key_at(row, bin.key_hi, lo));
+            const int share = (row.steps + SM_WAVES - 1) / SM_WAVES, begin = wave * share;
+            row.template for_steps<1>(begin, begin + share < row.steps ? begin + share : row.steps, 1, [&](const float(&x)[SM_VEC], uint32_t idx) {
                 uint32_t in = 0;
 #pragma unroll
                 for (uint32_t k = 0; k < SM_VEC; ++k)
@@ -1176,14 +1192,30 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
                     const float y = choose(x, k);
                     const uint64_t v = place_of(row, bin.key_hi, key_of(y), idx + k);
                     if (v >= lo && v <= hi)
-                        add(v, y);
+                        add(v, y, masses);
                 }
             });
+            __syncthreads();
+            if (tid < SM_RANGES) {
+                uint64_t m = 0;
+#pragma unroll
+                for (int w = 0; w < SM_WAVES; ++w)
+                    m += sh.list[w * SM_RANGES + tid];
+                sh.range_mass[tid] = m;
+            }
         }
         __syncthreads();
         const uint32_t b = pick<SM_RANGES / 64>(
             sh.range_count, [&](uint32_t i) { return row.unfixed(sh.range_mass[i], bin.bin); }, by_count, want, goal,
             above_count, above, n);
+        if (!in_list) {
+            uint64_t before = 0;
+            for (uint32_t i = lane; i < b; i += 64)
+                before += masses[i];
+            if (before != 0)
+                atomicAdd(reinterpret_cast<unsigned long long*>(&sh.part_mass[wave]),
+                          static_cast<unsigned long long>(before));
+        }
         lo += uint64_t(b) << shift;
         const uint64_t last = lo + ((uint64_t(1) << shift) - 1);
         hi = hi < last ? hi : last;
@@ -1248,6 +1280,8 @@ __device__ __forceinline__ void choose_bin(const Row<TYPE>& row, SharedCuts& sh,
     sh.pick.above = above;
     sh.pick.goal = goal;
     sh.pick.reached = above_count + n >= want ? 1u : 0u;
+    // its elements' number, to a sixteenth of an octave
+    sh.pick.about = uint32_t(sh.bin_mass[b] / __builtin_ldexp(sh.bin_weight[b], row.frac));
 }
 __device__ __forceinline__ Bin uniform_bin(const SharedCuts& sh)
 {
@@ -1305,7 +1339,7 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
     const int share = (row.steps + SM_WAVES - 1) / SM_WAVES;
     const bool by_k = int64_t(k) < row.vocab, by_p = p < 1.0;
     Cut cut{0u, ~0u};  // keeps all
-    bool in_parts = false;
+    bool in_parts = false, whole = false;
     Bin bin{0, 0, 0};
     uint64_t place = 0;
     if (by_k || by_p) {
@@ -1316,8 +1350,6 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
             sh.bin_count[tid] = 0;
             sh.bin_weight[tid] = exp2_exact(-double(tid) / SM_PER_OCTAVE - double(row.frac));
         }
-        if (tid < SM_WAVES)
-            sh.part_mass[tid] = 0;
         __syncthreads();
         if (!FILLED) {
             const int first = wave * share, end = first + share < row.steps ? first + share : row.steps;
@@ -1354,11 +1386,12 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
             }
             bin = uniform_bin(sh);
             place = cut_in_bin(row, sh, bin, which == 0, k, uniform(sh.pick.goal), uniform(sh.pick.above_count),
-                               uniform(sh.pick.above), kept, in_parts);
+                               uniform(sh.pick.above), uniform(sh.pick.about), kept, whole);
+            in_parts = true;
             cut = Cut{key_at(row, bin.key_hi, place), index_at(row, place)};
             if (which == 1 && last_cut.key != 0 && cut.keeps(last_cut.key, last_cut.index)) {
                 // no later than top-k's own cut, which rounding may have put first
-                in_parts = in_parts && last_bin.bin == bin.bin;
+                in_parts = whole && last_bin.bin == bin.bin;
                 place = last_place;
                 cut = last_cut;
             }
