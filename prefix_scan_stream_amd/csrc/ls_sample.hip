@@ -1291,13 +1291,14 @@ __device__ __forceinline__ Bin uniform_bin(const SharedCuts& sh)
 // The histogram of one wave's share of a row.  A weight is the weight 2^(-b/8) of its bin
 // times 2^(z/8), |z| <= 1/2, and the bin counts the second factor in units of 2^-frac: a
 // polynomial of degree 6 (relative error 2^-48.9) into whose last step the rounding to an
-// integer is folded, with no exponent to insert.  Below 2^-63.8 everything counts as the last bin's
-// weight, less than 2^-46 of the sum for a row of 2^17: the difference is clamped there, which
-// saves a minimum of the bin's number (1.3 % of a nucleus call).
+// integer is folded, with no exponent to insert.  Below 2^-63.9 weights count as 0,
+// for less than 2^-46 of the sum of a row of 2^17: added to the last bin they would take turns at one
+// address (peaked rows: 200 of 42000 logits took 55 us, against 27).
 template <bool COUNTS, int TYPE>
 __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, uint32_t* count, int first, int end)
 {
     const double one = __builtin_ldexp(1.0, row.frac);
+    uint32_t beyond = 0;
     const double last = uniform(-double(SM_BINS - 1) / SM_PER_OCTAVE / row.c);  // the last bin's middle
     const double c8 = uniform(row.c * SM_PER_OCTAVE), c0 = uniform(one + 0x1p52);
     const double c1 = uniform(one * 0x1.62e42fefa3aefp-4), c2 = uniform(one * 0x1.ebfbdff82c5e7p-9);
@@ -1306,7 +1307,7 @@ __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, 
     row.template for_steps<TYPE == LOGITS_F32 ? 1 : 2>(first, end, 1, [&](const float(&x)[SM_VEC], uint32_t) {
 #pragma unroll
         for (int j = 0; j < SM_VEC; ++j) {
-            const double d = __builtin_fmax(double(x[j]) - row.top64, last);
+            const double d = double(x[j]) - row.top64;
             const double t = __builtin_fma(d, -c8, TO_INT);
             const double z = __builtin_fma(d, c8, t - TO_INT);
             double w = __builtin_fma(c6, z, c5);
@@ -1316,12 +1317,18 @@ __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, 
             w = __builtin_fma(w, z, c1);
             w = __builtin_fma(w, z, c0);
             const uint32_t b = uint32_t(__builtin_bit_cast(uint64_t, t));
-            atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
-                      static_cast<unsigned long long>(__builtin_bit_cast(uint64_t, w) & ((uint64_t(1) << 52) - 1)));
-            if (COUNTS && x[j] > -__builtin_inff())
-                atomicAdd(&count[b], 1u);
+            if (COUNTS)
+                beyond += uint32_t(__builtin_popcountll(__ballot(d <= last && x[j] > -__builtin_inff())));
+            if (d > last) {
+                atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
+                          static_cast<unsigned long long>(__builtin_bit_cast(uint64_t, w) & ((uint64_t(1) << 52) - 1)));
+                if (COUNTS)
+                    atomicAdd(&count[b], 1u);
+            }
         }
     });
+    if (COUNTS && beyond != 0 && lane_id() == 0)
+        atomicAdd(&count[SM_BINS - 1], beyond);
 }
 
 // The cuts of a row that are not settled by a few candidates: a histogram of weights (and

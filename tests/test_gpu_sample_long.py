@@ -92,3 +92,22 @@ def test_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert (to_host(tokens) == want[0]).all() and (to_host(lps) == want[1]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [3, 40])
+def test_peaked_rows(rows, dtype):
+    """Most logits so far below the largest that they weigh nothing in a sum, though top-k may
+    still have to count them and keep some."""
+    vocab = 70000
+    x = rows_of(rows, vocab, DTYPES[dtype], rows, lift=False)
+    x[:, 100:110] = torch.tensor([80.0] * 9 + [79.5], device=DEV).to(x.dtype)
+    x[::2, 50000] = 90.0
+    x[1::3, ::5] = -float("inf")
+    u, t = uniforms(rows, 9), np.full(rows, 0.6)
+    for p in (0.3, 0.999999):
+        check(x, u, t, p=np.full(rows, p))
+        for k in (5, 1000, 60000):
+            check(x, u, t, k=np.full(rows, k), p=np.full(rows, p))
+    check(x, u, t, k=np.full(rows, 30000), m=np.full(rows, 1e-30))
+    check(x, u, np.full(rows, 30.0), k=np.full(rows, 30000), p=np.full(rows, 0.99))
