@@ -111,3 +111,19 @@ def test_peaked_rows(rows, dtype):
             check(x, u, t, k=np.full(rows, k), p=np.full(rows, p))
     check(x, u, t, k=np.full(rows, 30000), m=np.full(rows, 1e-30))
     check(x, u, np.full(rows, 30.0), k=np.full(rows, 30000), p=np.full(rows, 0.99))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [4097, 16384, 32000, 65536, 65537, 131072])
+def test_top_k_about_the_number_of_parts(vocab, dtype):
+    """Around the k up to which a row's candidates come from its segments or their quarters; some rows
+    with most logits masked, or with the largest ones side by side."""
+    segs = -(-vocab // 512)
+    ks = sorted({1, segs // 2, segs // 2 + 1, segs * 3 // 4, segs * 3 // 4 + 1, segs, segs * 3 - 1, segs * 3,
+                 segs * 3 + 1, 239, 240, 241, 300} - {0})
+    x = rows_of(len(ks), vocab, DTYPES[dtype], vocab + 1, lift=False)
+    x[1::4, vocab // 50:] = -float("inf")
+    x[2::4, 1000:1400] += 9.0
+    u, t = uniforms(len(ks), 1), np.full(len(ks), 0.9)
+    check(x, u, t, k=ks)
+    check(x, u, t, k=ks, p=np.full(len(ks), 0.7), m=np.full(len(ks), 0.01))
