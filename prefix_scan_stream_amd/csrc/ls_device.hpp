@@ -190,40 +190,10 @@ __device__ __forceinline__ typename Op::T row16_shift_up(typename Op::T incl)
     return dpp_move<DPP_ROW_SHR1, 0xf>(Op::identity(), incl);
 }
 
-// 64-bit sums across the wave: the same six steps, each moving both halves.
-template <int CTRL, int ROW_MASK, class T>
-__device__ __forceinline__ T dpp_move64(T v)
-{
-    static_assert(sizeof(T) == 8, "64-bit values");
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = dpp_move<CTRL, ROW_MASK>(0u, uint32_t(b));
-    const uint32_t hi = dpp_move<CTRL, ROW_MASK>(0u, uint32_t(b >> 32));
-    return __builtin_bit_cast(T, (uint64_t(hi) << 32) | lo);
-}
-template <class T>
-__device__ __forceinline__ T wave_inclusive_sum64(T v)
-{
-    v += dpp_move64<DPP_ROW_SHR1, 0xf>(v);
-    v += dpp_move64<DPP_ROW_SHR2, 0xf>(v);
-    v += dpp_move64<DPP_ROW_SHR4, 0xf>(v);
-    v += dpp_move64<DPP_ROW_SHR8, 0xf>(v);
-    v += dpp_move64<DPP_ROW_BCAST15, 0xa>(v);
-    v += dpp_move64<DPP_ROW_BCAST31, 0xc>(v);
-    return v;
-}
-
 template <class T>
 __device__ __forceinline__ T read_lane(T v, int lane)
 {
     return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-}
-
-template <class T>
-__device__ __forceinline__ T read_lane64(T v, int lane)
-{
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = read_lane(uint32_t(b), lane), hi = read_lane(uint32_t(b >> 32), lane);
-    return __builtin_bit_cast(T, (uint64_t(hi) << 32) | lo);
 }
 
 __device__ __forceinline__ int lane_id() { return __lane_id(); }

@@ -11,7 +11,7 @@
 // block reads all counts, a few percent of the outputs' bytes at the sizes of a step.
 // Bound by the bytes of the outputs when there are many (prompts, an emptied cache), by
 // the latency of one scan (two dependent loads and three barriers) when there are few.
-#include "ls_device.hpp"
+#include "ls_wave64.hpp"
 #include "ls_internal.hpp"
 
 namespace ls {

@@ -41,7 +41,7 @@
 //   float32 58-62 us, with 268 MB to read beside them (4.5 TB/s).
 #include <type_traits>
 
-#include "ls_device.hpp"
+#include "ls_wave64.hpp"
 #include "ls_internal.hpp"
 
 namespace ls {
