@@ -72,6 +72,8 @@ constexpr int SM_COUNTER = 32;              // 32-bit words from one row's count
 // 64 rows 51.7 both, 128 rows 72 against 55; 64000 logits 1 row 31.5 against 32.8, 32 rows 34.4
 // against 33.8; 32000 logits 1 row 27.8 against 25.7.
 constexpr int SM_SPLIT_ROWS = 32;
+constexpr int DPP_QUAD_SWAP1 = 0xb1, DPP_QUAD_SWAP2 = 0x4e;  // each lane of four its neighbour's value, the other pair's
+constexpr int SM_FINE_SEGS = 32;  // segments of a row up to which its largest values are kept by sixteenths too
 constexpr int SM_SPLIT_STEPS = 128;
 
 constexpr double LOG2E = 0x1.71547652b82fep+0, LN2 = 0x1.62e42fefa39efp-1;
@@ -524,7 +526,9 @@ __device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t parts)
 // `per_wave` segments of seg_steps steps.
 struct SampleGrid {
     uint32_t* counters;  // one per row, 0 between calls
-    float* tops;         // rows x segs: each segment's largest value, or (with cuts) x 4: that of each quarter
+    // rows x segs: each segment's largest value, or (with cuts) x 4: that of each quarter, and behind these where
+    // a row has no more than SM_FINE_SEGS x 16: that of each four lanes
+    float* tops;
     double* sums;        // rows x segs: without cuts, and its weights relative to that
     float* split_tops;   // rows: the largest value where sample_bins_kernel makes the cut, else NaN
     uint64_t* masses;    // rows x SM_WAVES x SM_BINS: the bins of each sixteenth of a row
@@ -1463,32 +1467,43 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
         write_token(call, r, row, token, total);
 }
 
-// Whether the k-th largest value is looked for among the quarters of segments: with k near the number of
-// segments, and no more than 512 quarters.  1 row, bfloat16, top-k 50, with segments only against so: 16384 logits
-// 21.2 to 12.5 us, 32000 25.5 to 12.5; top-k 100 of 64000 33.6 to 15.6.  Always quarters up
-// to 64000 logits cost 0.7 us for small k.
-__device__ __forceinline__ bool by_quarters(const SampleGrid& g, uint32_t k)
+// In how many parts a segment's values are looked at for the k-th largest: 1, its quarters (4) or its
+// sixteenths (16), the fewest that number more than k, as long as they are at most 512: more parts give fewer
+// candidates, or allow more of k, and cost up to 0.7 us.  1 row, bfloat16, top-k 50, with segments only against so:
+// 4000 logits 17.9 us to 12.7, 8192 18.7 to 12.6, 16384 21.2 to 13.2, 32000 25.5 to 12.2; top-k 100 of 64000 33.6 to 15.8.
+// Keeping the sixteenths costs short rows with top-k 0.5 to 1 us where they are not asked for.
+__device__ __forceinline__ uint32_t parts_of(const SampleGrid& g, uint32_t k)
 {
-    return g.segs <= 128 && uint64_t(k) * 2 > uint64_t(g.segs);
+    const uint64_t segs = uint64_t(g.segs), twice = uint64_t(k) * 2;
+    if (g.segs <= SM_FINE_SEGS && twice > segs * 4)
+        return 16;
+    return g.segs <= 128 && twice > segs ? 4 : 1;
 }
 
 // One wave: where the candidates of a row begin.  few: at most the k-th largest logit, which is the
-// k-th largest of the largest values of the segments, or of their quarters while these are no
-// more than 512, to 16 bits of its key; else a little below the
+// k-th largest of the largest values of the segments or of parts of them, to 16 bits of its key; else a little below the
 // smallest logit that min-p may keep.  The segments' quarters with candidates go into
 // sh.quarters (a quarter is the most that is read for one candidate).
 template <int TYPE>
-__device__ __forceinline__ void find_segments(const SampleGrid& g, const Row<TYPE>& row, SharedCuts& sh,
+__device__ __forceinline__ void find_segments(const SampleGrid& g, int64_t rows, int64_t r, const Row<TYPE>& row, SharedCuts& sh,
                                               const QuarterTops& tops, bool few, uint32_t k, double least)
 {
     float low;
     if (few) {
         static_assert(SM_PER_LANE == 8, "two segments' quarters, or eight segments");
-        const bool quarters = by_quarters(g, k);
+        const uint32_t parts = parts_of(g, k);
         uint32_t key[SM_PER_LANE], at = 0;
 #pragma unroll
         for (int j = 0; j < SM_PER_LANE; ++j)
-            key[j] = key_of(clean(quarters ? tops.quarter[j / 4][j % 4] : tops.v[j], row.inf)) >> 16;
+            key[j] = key_of(clean(parts == 4 ? tops.quarter[j / 4][j % 4] : tops.v[j], row.inf)) >> 16;
+        if (__builtin_expect(parts == 16, 0)) {
+            const float* const fine = g.tops + (rows * 4 + r * 16) * g.segs;
+#pragma unroll
+            for (int j = 0; j < SM_PER_LANE; ++j) {
+                const int i = j * 64 + lane_id();
+                key[j] = key_of(clean(i < g.segs * 16 ? get(&fine[i]) : -__builtin_inff(), row.inf)) >> 16;
+            }
+        }
         const auto count = [&](auto lanes, uint32_t v) {
             uint32_t n = 0;
 #pragma unroll
@@ -1504,7 +1519,7 @@ __device__ __forceinline__ void find_segments(const SampleGrid& g, const Row<TYP
                 at = nc >= k ? c : nb >= k ? b : na >= k ? a : at;
             }
         };
-        if (quarters ? tops.per_lane == 1 : tops.per_lane <= 4)
+        if (uint32_t(g.segs) * parts <= 64u * 4)
             narrow(std::integral_constant<int, 4>{});
         else
             narrow(std::integral_constant<int, SM_PER_LANE>{});
@@ -1701,6 +1716,27 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
                 put(&g.tops[(r * g.segs + seg) * 4 + (lane >> 4)], m);
         }
     }
+    // (out of the way of long rows: the same again for each four lanes, of loads that are in the L1 now)
+    if (__builtin_expect(g.segs <= SM_FINE_SEGS && call.top_k != nullptr, 0)) {
+#pragma unroll 1
+        for (int i = 0; i < g.per_wave; ++i) {
+            const int seg = (part * g.per_wave + i) * SM_WAVES + wave;
+            if (seg >= g.segs)
+                break;
+            Raw<TYPE> raw;
+            raw.load_step(row.p, seg, row.vocab);
+            float four = NEG;
+#pragma unroll
+            for (int k = 0; k < SM_VEC; ++k) {
+                const float x = raw.at(k);
+                four = x > four ? x : four;
+            }
+            four = MaxF32::apply(four, dpp_move<DPP_QUAD_SWAP1, 0xf>(NEG, four));
+            four = MaxF32::apply(four, dpp_move<DPP_QUAD_SWAP2, 0xf>(NEG, four));
+            if ((lane & 3) == 3)
+                put(&g.tops[call.rows * g.segs * 4 + (r * g.segs + seg) * 16 + (lane >> 2)], four);
+        }
+    }
     stores_done();
     __syncthreads();
     if (tid == 0)
@@ -1714,9 +1750,10 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
         k = uint32_t(call.top_k[r]);
     const double p = share_of(call, r), least = least_of(call, r);
     // few enough that the k-th largest of n parts' values leaves few candidates: of logits in any order
-    // about -n ln(1 - k / n), which SM_SMALL has to hold (with k <= 3/4 n and 240 at most 440)
-    const uint32_t n = uint32_t(by_quarters(g, k) ? g.segs * 4 : g.segs);
-    const bool few = k <= 240 && k * 4 <= n * 3;
+    // about -n ln(1 - k / n), which SM_SMALL has to hold (with k <= 3/4 n and 240 at most 440); in a
+    // short row the bins take no longer from k = 128 on (200 of 16384: 21.2 us, with candidates 23.7)
+    const uint32_t parts = parts_of(g, k), n = uint32_t(g.segs) * parts;
+    const bool few = k <= (parts == 16 ? 128u : 240u) && k * 4 <= n * 3;
     const bool candidates = few || (p >= 1.0 && least > 0.0);
     // one wave (the others would only take its turns), then all
     if (wave == 0) {
@@ -1730,7 +1767,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
         if (g.split && lane == 0)
             g.split_tops[r] = later ? top : __builtin_nanf("");
         if (!done && candidates)
-            find_segments(g, row, sh, tops, few, k, least);
+            find_segments(g, call.rows, r, row, sh, tops, few, k, least);
     }
     __syncthreads();
     if (uniform(sh.s.arrived) == 0u)
@@ -1798,7 +1835,7 @@ static int64_t row_segs(int64_t vocab)
 }
 
 // header | a counter for each row of a launch | 16 bytes for each segment: the segments' sums and
-// behind them their largest values, or their quarters' largest values | the largest value and the
+// behind them their largest values, or their quarters' largest values | 64 bytes more for each segment where a row has few | the largest value and the
 // bins of the rows that sample_bins_kernel may take.  The counters' place is the same for every call, so that nothing else is ever written
 // there and they stay 0 between calls of any sizes.
 static size_t row_cells(int64_t rows, int64_t vocab)
@@ -1806,13 +1843,17 @@ static size_t row_cells(int64_t rows, int64_t vocab)
     return size_t(rows < SM_ROWS ? rows : SM_ROWS) * size_t(row_segs(vocab));
 }
 
+static size_t fine_bytes(int64_t rows, int64_t vocab)
+{
+    return row_segs(vocab) <= SM_FINE_SEGS ? round256(row_cells(rows, vocab) * 64) : 0;
+}
 constexpr size_t SM_MASSES = size_t(SM_WAVES) * SM_BINS * 8;  // bytes of a row
 static size_t split_rows(int64_t rows) { return size_t(rows < SM_SPLIT_ROWS ? rows : SM_SPLIT_ROWS); }
 
 size_t sample_workspace_bytes(int64_t rows, int64_t vocab)
 {
     const size_t cells = row_cells(rows, vocab);
-    return 256 + SM_ROWS * SM_COUNTER * 4 + round256(cells * 16) + SM_SPLIT_ROWS * 4 + split_rows(rows) * SM_MASSES;
+    return 256 + SM_ROWS * SM_COUNTER * 4 + round256(cells * 16) + fine_bytes(rows, vocab) + SM_SPLIT_ROWS * 4 + split_rows(rows) * SM_MASSES;
 }
 
 template <int TYPE>
@@ -1861,6 +1902,7 @@ hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t
     g.sums = reinterpret_cast<double*>(at);
     g.tops = reinterpret_cast<float*>(cuts ? at : at + size_t(rows) * size_t(g.segs) * 8);
     at += round256(row_cells(call.rows, call.vocab) * 16);
+    at += fine_bytes(call.rows, call.vocab);
     g.split_tops = reinterpret_cast<float*>(at);
     g.masses = reinterpret_cast<uint64_t*>(at + SM_SPLIT_ROWS * 4);
     g.split = call.top_p != nullptr && call.top_k == nullptr && call.rows <= SM_SPLIT_ROWS && g.steps >= SM_SPLIT_STEPS;

@@ -127,3 +127,20 @@ def test_top_k_about_the_number_of_parts(vocab, dtype):
     u, t = uniforms(len(ks), 1), np.full(len(ks), 0.9)
     check(x, u, t, k=ks)
     check(x, u, t, k=ks, p=np.full(len(ks), 0.7), m=np.full(len(ks), 0.01))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [31, 500, 1025, 3001, 8192, 16384, 16385])
+def test_top_k_of_short_rows(vocab, dtype):
+    """The same around a short row's parts, which are finer; the parts past its end are empty."""
+    segs = -(-vocab // 512)
+    ks = sorted({k for n in (segs, segs * 4, segs * 16) for k in (n // 2, n // 2 + 1, n * 3 // 4, n * 3 // 4 + 1, n)} |
+                {240, 241, vocab} - {0})
+    ks = [k for k in ks if k > 0]
+    x = rows_of(len(ks), vocab, DTYPES[dtype], vocab + 2, lift=False, pad=3)
+    x[1::4, vocab // 3:] = -float("inf")
+    x[2::4, :200] += 9.0
+    x[3::4, vocab - 1] = float("nan")
+    u, t = uniforms(len(ks), 1), np.full(len(ks), 0.9)
+    check(x, u, t, k=ks)
+    check(x, u, t, k=ks, p=np.full(len(ks), 0.7), m=np.full(len(ks), 0.01))
