@@ -31,9 +31,9 @@
 //   same way.  Otherwise the cut is found by value without sorting the row (cut_row).
 //
 // Measured, in a graph, 131072 logits to a row:
-//   1 row, bfloat16, top-k 50, top-p, min-p: 12.2 us, the latency of the chain of steps: 2 us the launch, 2 the
+//   1 row, bfloat16, top-k 50, top-p, min-p: 12.4 us, the latency of the chain of steps: 2 us the launch, 2 the
 //   first read, 1 the counter, 4.5 one wave's search for the candidates' quarters, 2 their reading, 3 order
-//   and sums.  64 rows, top-k 100, top-p, min-p: 15.9 us.
+//   and sums.  64 rows, top-k 100, top-p, min-p: 15.7 us.
 //   256 rows, bfloat16, top-p alone: 66 us, a row to a CU: 11 us the first read (6 TB/s over all), 25 the bins
 //   (16.5 vector instructions a logit), 14 the bin's elements, the rest the steps between.
 //   64 rows of flat logits (normal, a deviation of 0.5), top-p: 77 us, with two more readings for a bin of 13000.
