@@ -36,7 +36,7 @@
 //   and sums.  64 rows, top-k 100, top-p, min-p: 15.7 us.
 //   256 rows, bfloat16, top-p alone: 66 us, a row to a CU: 11 us the first read (6 TB/s over all), 25 the bins
 //   (16.5 vector instructions a logit), 14 the bin's elements, the rest the steps between.
-//   64 rows of flat logits (normal, a deviation of 0.5), top-p: 77 us, with two more readings for a bin of 13000.
+//   64 rows of flat logits (normal, a deviation of 0.5), top-p: 83 us, with two more readings for a bin of 13000.
 //   512 rows, no cuts: bfloat16 51 us, bound by vector instructions (22 a logit, 50 us at the measured rate);
 //   float32 58-62 us, with 268 MB to read beside them (4.5 TB/s).
 #include <type_traits>
@@ -1169,11 +1169,19 @@ __device__ __forceinline__ uint64_t cut_in_bin(const Row<TYPE>& row, SharedCuts&
             for (uint32_t i = lane; i < SM_RANGES; i += 64)
                 masses[i] = 0;
         __syncthreads();
+        // the lanes that agree with the first one make one addition: values that repeat, as a mask's lowest
+        // one, would take turns (208 rows of 115258 logits, 82000 of a row masked so, top-k 75685: 491 us, so 318; 64 flat rows
+        // of 131072 78 and 83)
         const auto add = [&](uint64_t v, float x, uint64_t* mass) {
-            const uint32_t b = uint32_t((v - lo) >> shift);
-            atomicAdd(&sh.range_count[b], 1u);
-            atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
-                      static_cast<unsigned long long>(row.fixed(row.below(x), bin.bin)));
+            const uint32_t b = uint32_t((v - lo) >> shift), b0 = __builtin_amdgcn_readfirstlane(b);
+            const bool same = b == b0 && x == uniform(x);
+            const uint64_t all_same = __ballot(same);
+            const uint32_t times = same ? uint32_t(__builtin_popcountll(all_same)) : 1u;
+            if (!same || uint32_t(__builtin_ctzll(all_same)) == lane) {
+                atomicAdd(&sh.range_count[b], times);
+                atomicAdd(reinterpret_cast<unsigned long long*>(&mass[b]),
+                          static_cast<unsigned long long>(row.fixed(row.below(x), bin.bin) * times));
+            }
         };
         if (in_list) {
             for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
