@@ -8,8 +8,11 @@ and importing or calling them fails loudly when libscan.so is missing.
 
 PyTorch supplies device memory and streams only.  Workspaces are cached per
 (device, stream), zero-filled by the library once when they are made, and grown
-on demand; a workspace that a larger one replaces is kept, not freed, because a
-HIP graph captured earlier may still use it (release_workspaces() frees them).
+on demand.  A call that is being captured into a HIP graph uses a workspace of
+that graph's own: the stream's cached one, if eager calls have made one, which then
+is the graph's and is kept (release_workspaces() frees it); else one from the graph's
+memory pool, whose zero fill is part of the graph.  So graphs may be replayed in any
+order, between eager calls and on several streams.
 
 Checked mode (set_checked(True), or LIBSCAN_CHECKED=1 in the environment) reads
 the workspace's error word after every call that uses one -- which waits for the
@@ -142,6 +145,9 @@ def load_library():
         lib.slot_map.restype = I
         lib.pages_release.argtypes = [P, P, I64, P, I64, I64, P, I64, P, I64, P, P]
         lib.pages_release.restype = I
+        # of the HIP runtime that libscan.so is linked with
+        lib.hipStreamGetCaptureInfo.argtypes = [P, ctypes.POINTER(I), ctypes.POINTER(ctypes.c_ulonglong)]
+        lib.hipStreamGetCaptureInfo.restype = I
         _lib = lib
         return lib
 
@@ -186,7 +192,8 @@ def ls_compact_workspace_bytes(n: int, dtype: str) -> int:
 _ws_cache: dict = {}    # (device index, stream handle) -> the uint8 workspace in use
 _ws_uses: dict = {}     # calls on each cached status workspace since its last initialisation
 STATUS_REINIT_CALLS = 1 << 25
-_ws_retired: list = []  # workspaces replaced by larger ones, kept for graphs that captured them
+_ws_graph: dict = {}    # the same key -> (capture, workspace) of the last graph captured there
+_ws_retired: list = []  # workspaces replaced by larger ones or given to a graph
 
 
 def set_checked(on: bool = True) -> None:
@@ -217,19 +224,56 @@ def ls_workspace_check(ws: torch.Tensor, stream=None) -> int:
     return flags.value
 
 
+def _capture_of(handle: int) -> int | None:
+    """The number of the capture that a stream is in; None while it is in none."""
+    if handle == 0:  # the null stream cannot be captured
+        return None
+    status, number = ctypes.c_int(0), ctypes.c_ulonglong(0)
+    if load_library().hipStreamGetCaptureInfo(handle, ctypes.byref(status), ctypes.byref(number)) != 0:
+        raise LibscanError(LS_ERR_HIP, "hipStreamGetCaptureInfo")
+    return number.value if status.value else None
+
+
+def _new_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int) -> torch.Tensor:
+    with torch.cuda.stream(stream):  # while it is being captured: from the graph's pool
+        new = torch.empty((max(nbytes, 1 << 16) + 255) & ~255, dtype=torch.uint8, device=device)
+    ls_workspace_init(new, stream)
+    return new
+
+
+def _graph_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int, key: tuple,
+                     capture: int) -> torch.Tensor:
+    """The workspace of the graph that is being captured on `stream`, for no other graph
+    and no eager call: these could run between or beside its replays."""
+    last, buf = _ws_graph.get(key, (None, None))
+    if last != capture or buf.numel() < nbytes:
+        buf = _ws_cache.get(key)
+        if buf is not None and buf.numel() >= nbytes:
+            # filled by an eager call, and not used by one again
+            _ws_retired.append(_ws_cache.pop(key))
+            _ws_uses.pop(key, None)
+        else:
+            # the fill is a node of this graph, so only this graph may count on it
+            buf = _new_workspace(device, stream, nbytes)
+        _ws_graph[key] = (capture, buf)
+    return buf
+
+
 def workspace_for(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
                   kind: str = "status") -> torch.Tensor:
     """The cached, initialised uint8 workspace of (device, stream, kind), of at least
     nbytes.  Kinds keep apart what the C ABI requires to be apart: "status" for the
     single-pass scans, segmented scans and compactions (tile status words that must
-    never be overwritten with other data), "sort" for the radix sort and "phases"
-    for the three-phase scan_ex schemes (plain scratch)."""
+    never be overwritten with other data), "sort" for the radix sort, "phases"
+    for the three-phase scan_ex schemes (plain scratch) and "sample" for
+    sample_tokens.  While the stream is being captured, the workspace is that graph's own."""
     key = (device.index, stream.cuda_stream, kind)
+    capture = _capture_of(stream.cuda_stream)
+    if capture is not None:
+        return _graph_workspace(device, stream, nbytes, key, capture)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
-        size = (max(nbytes, 1 << 16) + 255) & ~255
-        new = torch.empty(size, dtype=torch.uint8, device=device)
-        ls_workspace_init(new, stream)
+        new = _new_workspace(device, stream, nbytes)
         if buf is not None:
             _ws_retired.append(buf)
         _ws_cache[key] = new
@@ -258,6 +302,7 @@ def release_workspaces() -> None:
     """Drop every cached and retired workspace (no graph that used one may be
     replayed afterwards)."""
     _ws_cache.clear()
+    _ws_graph.clear()
     _ws_retired.clear()
     _ws_uses.clear()
 
@@ -732,10 +777,10 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature: tor
 
 
 def _sample_workspace(index: int, rows: int, vocab: int) -> torch.Tensor:
-    """The current stream's cached workspace for sample_tokens."""
-    need = ls_sample_workspace_bytes(rows, vocab)
-    buf = _ws_cache.get((index, _raw_stream(index), "sample"))
-    if buf is None or buf.numel() < need:
+    """The current stream's workspace for sample_tokens (workspace_for's, found sooner)."""
+    need, handle = ls_sample_workspace_bytes(rows, vocab), _raw_stream(index)
+    buf = _ws_cache.get((index, handle, "sample"))
+    if buf is None or buf.numel() < need or (handle != 0 and torch.cuda.is_current_stream_capturing()):
         device = torch.device("cuda", index)
         buf = workspace_for(device, torch.cuda.current_stream(device), need, "sample")
     return buf

@@ -1,0 +1,89 @@
+"""The binding's workspaces, on the CPU: which buffer a call gets and which fills are
+enqueued for it, with host memory in place of the device's and streams and captures made up."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import prefix_scan_stream_amd as ps
+
+CPU = torch.device("cpu")
+
+
+@pytest.fixture
+def fills(monkeypatch):
+    """Captures by stream handle, and the (buffer's address, capture) of each fill."""
+    state = SimpleNamespace(capture={}, log=[])
+
+    def init(ws, stream):
+        ws.zero_()
+        state.log.append((ws.data_ptr(), state.capture.get(stream.cuda_stream)))
+
+    def new(device, stream, nbytes):
+        ws = torch.empty((max(nbytes, 1 << 16) + 255) & ~255, dtype=torch.uint8)
+        init(ws, stream)
+        return ws
+
+    monkeypatch.setattr(ps, "ls_workspace_init", init)
+    monkeypatch.setattr(ps, "_new_workspace", new, raising=False)
+    monkeypatch.setattr(ps, "_capture_of", lambda handle: state.capture.get(handle), raising=False)
+    for name in ("_ws_cache", "_ws_graph", "_ws_uses"):
+        monkeypatch.setattr(ps, name, {}, raising=False)
+    monkeypatch.setattr(ps, "_ws_retired", [])
+    return state
+
+
+def stream(handle):
+    return SimpleNamespace(cuda_stream=handle)
+
+
+def alive(ws):
+    return any(ws is held for held in [*ps._ws_cache.values(), *ps._ws_retired])
+
+
+KINDS = ["status", "sort", "phases", "sample"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_graph_counts_on_its_own_fill_only(fills, kind):
+    """Two captures on a stream without a workspace, the second no larger: each has a buffer
+    and a fill of its own, and an eager call there counts on neither."""
+    s = stream(7)
+    fills.capture[7] = 1
+    a = ps.workspace_for(CPU, s, 100_000, kind)
+    assert ps.workspace_for(CPU, s, 90_000, kind) is a
+    assert fills.log == [(a.data_ptr(), 1)]
+    fills.capture[7] = 2
+    b = ps.workspace_for(CPU, s, 90_000, kind)
+    assert b is not a and fills.log[1:] == [(b.data_ptr(), 2)]
+    bigger = ps.workspace_for(CPU, s, 300_000, kind)
+    assert bigger.numel() >= 300_000 and fills.log[2:] == [(bigger.data_ptr(), 2)]
+    del fills.capture[7]
+    c = ps.workspace_for(CPU, s, 90_000, kind)
+    assert c is not a and c is not b and c is not bigger and fills.log[3:] == [(c.data_ptr(), None)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_graph_takes_the_workspace_of_a_stream_that_was_warmed_up(fills, kind):
+    """No fill in the first graph; the buffer is kept for it and nobody else has it again."""
+    s = stream(9)
+    warm = ps.workspace_for(CPU, s, 100_000, kind)
+    fills.capture[9] = 5
+    assert ps.workspace_for(CPU, s, 100_000, kind) is warm and len(fills.log) == 1
+    assert ps.workspace_for(CPU, s, 50_000, kind) is warm and alive(warm)
+    del fills.capture[9]
+    eager = ps.workspace_for(CPU, s, 50_000, kind)
+    assert eager is not warm and fills.log[1:] == [(eager.data_ptr(), None)]
+    assert ps.workspace_for(CPU, s, 50_000, kind) is eager
+    fills.capture[9] = 6
+    assert ps.workspace_for(CPU, s, 50_000, kind) is eager and alive(warm) and alive(eager)
+
+
+def test_two_streams_of_one_capture(fills):
+    """Branches of a graph may run side by side."""
+    fills.capture.update({3: 1, 4: 1})
+    assert ps.workspace_for(CPU, stream(3), 1000) is not ps.workspace_for(CPU, stream(4), 1000)
+
+
+def test_the_null_stream_is_never_captured():
+    assert ps._capture_of(0) is None
