@@ -30,7 +30,9 @@
  *     `out` enables 128-bit loads and stores; other alignments are accepted and
  *     run a slower path.
  *   - Concurrent calls must use distinct workspaces; calls that share a
- *     workspace on different streams race.
+ *     workspace on different streams race.  So do calls that share one on the
+ *     same stream, if several host threads enqueue them at the same time: some
+ *     calls are several kernels, which must not stand between another call's.
  *
  * Workspaces
  *   The scans, segmented scans, compactions and the radix sort take a caller's

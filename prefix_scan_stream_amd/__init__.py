@@ -189,6 +189,9 @@ def ls_compact_workspace_bytes(n: int, dtype: str) -> int:
 
 # ------------------------------------------------------------ workspaces
 
+# Held from the lookup of a workspace to the end of the call that enqueues on it: the kernels of
+# one call stand together on the stream, also where several host threads use that.
+_ws_lock = threading.RLock()
 _ws_cache: dict = {}    # (device index, stream handle) -> the uint8 workspace in use
 _ws_uses: dict = {}     # calls on each cached status workspace since its last initialisation
 STATUS_REINIT_CALLS = 1 << 25
@@ -267,26 +270,27 @@ def workspace_for(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
     never be overwritten with other data), "sort" for the radix sort, "phases"
     for the three-phase scan_ex schemes (plain scratch) and "sample" for
     sample_tokens.  While the stream is being captured, the workspace is that graph's own."""
-    key = (device.index, stream.cuda_stream, kind)
-    capture = _capture_of(stream.cuda_stream)
-    if capture is not None:
-        return _graph_workspace(device, stream, nbytes, key, capture)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        new = _new_workspace(device, stream, nbytes)
-        if buf is not None:
-            _ws_retired.append(buf)
-        _ws_cache[key] = new
-        _ws_uses[key] = 0
-        buf = new
-    elif kind == "status":
-        # status words compare epochs modulo 2^26: zero the workspace again well
-        # before that many calls (one fill kernel per 2^25 calls)
-        _ws_uses[key] = _ws_uses.get(key, 0) + 1
-        if _ws_uses[key] >= STATUS_REINIT_CALLS:
-            ls_workspace_init(buf, stream)
+    with _ws_lock:
+        key = (device.index, stream.cuda_stream, kind)
+        capture = _capture_of(stream.cuda_stream)
+        if capture is not None:
+            return _graph_workspace(device, stream, nbytes, key, capture)
+        buf = _ws_cache.get(key)
+        if buf is None or buf.numel() < nbytes:
+            new = _new_workspace(device, stream, nbytes)
+            if buf is not None:
+                _ws_retired.append(buf)
+            _ws_cache[key] = new
             _ws_uses[key] = 0
-    return buf
+            buf = new
+        elif kind == "status":
+            # status words compare epochs modulo 2^26: zero the workspace again well
+            # before that many calls (one fill kernel per 2^25 calls)
+            _ws_uses[key] = _ws_uses.get(key, 0) + 1
+            if _ws_uses[key] >= STATUS_REINIT_CALLS:
+                ls_workspace_init(buf, stream)
+                _ws_uses[key] = 0
+        return buf
 
 
 def workspace_error_flags(device=None, stream=None) -> int:
@@ -356,11 +360,12 @@ def _scan(name: str, x: torch.Tensor, op: str, out, total):
     n = x.numel()
     stream, sh = _stream_handle(x.device)
     need = ls_scan_workspace_bytes(n, dt, op)
-    ws = workspace_for(x.device, stream, need)
-    st = getattr(lib, name)(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], _ptr(total),
-                            _ptr(ws), ws.numel(), sh)
-    _check(st, name)
-    _after_call(ws, stream, name)
+    with _ws_lock:
+        ws = workspace_for(x.device, stream, need)
+        st = getattr(lib, name)(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], _ptr(total),
+                                _ptr(ws), ws.numel(), sh)
+        _check(st, name)
+        _after_call(ws, stream, name)
     return out
 
 
@@ -393,22 +398,23 @@ def segmented_scan(x: torch.Tensor, op: str = "sum", exclusive: bool = False,
     if total is not None and (total.dtype != x.dtype or total.numel() < 1):
         raise ValueError("libscan: total must hold one element of the input dtype")
     stream, sh = _stream_handle(x.device)
-    ws = workspace_for(x.device, stream, ls_segmented_workspace_bytes(n, dt, op))
-    excl = 1 if exclusive else 0
-    if heads is not None:
-        heads = _flags_tensor(heads, n)
-        st = lib.segmented_scan(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], excl, _ptr(heads),
-                                _ptr(total), _ptr(ws), ws.numel(), sh)
-        _check(st, "segmented_scan")
-        _after_call(ws, stream, "segmented_scan")
-    else:
-        if offsets.dtype != torch.int64 or not offsets.is_contiguous() or offsets.numel() < 1:
-            raise ValueError("libscan: offsets must be a contiguous int64 tensor of nseg + 1 entries")
-        st = lib.segmented_scan_offsets(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], excl,
-                                        _ptr(offsets), offsets.numel() - 1, _ptr(total), _ptr(ws),
-                                        ws.numel(), sh)
-        _check(st, "segmented_scan_offsets")
-        _after_call(ws, stream, "segmented_scan_offsets")
+    with _ws_lock:
+        ws = workspace_for(x.device, stream, ls_segmented_workspace_bytes(n, dt, op))
+        excl = 1 if exclusive else 0
+        if heads is not None:
+            heads = _flags_tensor(heads, n)
+            st = lib.segmented_scan(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], excl, _ptr(heads),
+                                    _ptr(total), _ptr(ws), ws.numel(), sh)
+            _check(st, "segmented_scan")
+            _after_call(ws, stream, "segmented_scan")
+        else:
+            if offsets.dtype != torch.int64 or not offsets.is_contiguous() or offsets.numel() < 1:
+                raise ValueError("libscan: offsets must be a contiguous int64 tensor of nseg + 1 entries")
+            st = lib.segmented_scan_offsets(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], excl,
+                                            _ptr(offsets), offsets.numel() - 1, _ptr(total), _ptr(ws),
+                                            ws.numel(), sh)
+            _check(st, "segmented_scan_offsets")
+            _after_call(ws, stream, "segmented_scan_offsets")
     return out
 
 
@@ -469,12 +475,13 @@ def scan_ex(x: torch.Tensor, op: str = "sum", inclusive: bool = True,
     stream, sh = _stream_handle(x.device)
     need = ls_scan_ex_workspace_bytes(n, dt, op, scheme)
     phases = scheme in ("reduce_then_scan", "scan_then_propagate")
-    ws = workspace_for(x.device, stream, need, "phases" if phases else "status")
-    st = lib.scan_ex(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], 0 if inclusive else 1,
-                     SCHEME_CODES[scheme], _ptr(total), _ptr(ws), ws.numel(), sh)
-    _check(st, "scan_ex")
-    if not phases:  # the three-phase schemes never wait, and keep no error word
-        _after_call(ws, stream, "scan_ex")
+    with _ws_lock:
+        ws = workspace_for(x.device, stream, need, "phases" if phases else "status")
+        st = lib.scan_ex(_ptr(x), _ptr(out), n, DTYPE_CODES[dt], OP_CODES[op], 0 if inclusive else 1,
+                         SCHEME_CODES[scheme], _ptr(total), _ptr(ws), ws.numel(), sh)
+        _check(st, "scan_ex")
+        if not phases:  # the three-phase schemes never wait, and keep no error word
+            _after_call(ws, stream, "scan_ex")
     return out
 
 
@@ -499,11 +506,12 @@ def compact_if(x: torch.Tensor, cmp: str, threshold, out: torch.Tensor | None = 
     n = x.numel()
     stream, sh = _stream_handle(x.device)
     need = ls_compact_workspace_bytes(n, dt)
-    ws = workspace_for(x.device, stream, need)
-    st = lib.compact_if(_ptr(x), _ptr(out), _ptr(count), n, DTYPE_CODES[dt], CMP_CODES[cmp],
-                        thr_bits, _ptr(ws), ws.numel(), sh)
-    _check(st, "compact_if")
-    _after_call(ws, stream, "compact_if")
+    with _ws_lock:
+        ws = workspace_for(x.device, stream, need)
+        st = lib.compact_if(_ptr(x), _ptr(out), _ptr(count), n, DTYPE_CODES[dt], CMP_CODES[cmp],
+                            thr_bits, _ptr(ws), ws.numel(), sh)
+        _check(st, "compact_if")
+        _after_call(ws, stream, "compact_if")
     return out, count
 
 
@@ -542,10 +550,11 @@ def compact_flags(x: torch.Tensor, flags: torch.Tensor, out: torch.Tensor | None
         out = torch.empty_like(x)
     count = _count_tensor(count, x.device)
     stream, sh = _stream_handle(x.device)
-    ws = workspace_for(x.device, stream, ls_compact_workspace_bytes(n, "uint32"))
-    st = lib.compact_flags(_ptr(x), _ptr(flags), _ptr(out), _ptr(count), n, _ptr(ws), ws.numel(), sh)
-    _check(st, "compact_flags")
-    _after_call(ws, stream, "compact_flags")
+    with _ws_lock:
+        ws = workspace_for(x.device, stream, ls_compact_workspace_bytes(n, "uint32"))
+        st = lib.compact_flags(_ptr(x), _ptr(flags), _ptr(out), _ptr(count), n, _ptr(ws), ws.numel(), sh)
+        _check(st, "compact_flags")
+        _after_call(ws, stream, "compact_flags")
     return out, count
 
 
@@ -563,11 +572,12 @@ def select_indices_if(x: torch.Tensor, cmp: str, threshold, out: torch.Tensor | 
         out = torch.empty(n, dtype=torch.int32, device=x.device)
     count = _count_tensor(count, x.device)
     stream, sh = _stream_handle(x.device)
-    ws = workspace_for(x.device, stream, ls_compact_workspace_bytes(n, dt))
-    st = lib.select_indices_if(_ptr(x), _ptr(out), _ptr(count), n, DTYPE_CODES[dt], CMP_CODES[cmp],
-                               _threshold_bits(dt, threshold), _ptr(ws), ws.numel(), sh)
-    _check(st, "select_indices_if")
-    _after_call(ws, stream, "select_indices_if")
+    with _ws_lock:
+        ws = workspace_for(x.device, stream, ls_compact_workspace_bytes(n, dt))
+        st = lib.select_indices_if(_ptr(x), _ptr(out), _ptr(count), n, DTYPE_CODES[dt], CMP_CODES[cmp],
+                                   _threshold_bits(dt, threshold), _ptr(ws), ws.numel(), sh)
+        _check(st, "select_indices_if")
+        _after_call(ws, stream, "select_indices_if")
     return out, count
 
 
@@ -582,10 +592,11 @@ def select_indices_flags(flags: torch.Tensor, out: torch.Tensor | None = None,
         out = torch.empty(n, dtype=torch.int32, device=flags.device)
     count = _count_tensor(count, flags.device)
     stream, sh = _stream_handle(flags.device)
-    ws = workspace_for(flags.device, stream, ls_compact_workspace_bytes(n, "uint32"))
-    st = lib.select_indices_flags(_ptr(flags), _ptr(out), _ptr(count), n, _ptr(ws), ws.numel(), sh)
-    _check(st, "select_indices_flags")
-    _after_call(ws, stream, "select_indices_flags")
+    with _ws_lock:
+        ws = workspace_for(flags.device, stream, ls_compact_workspace_bytes(n, "uint32"))
+        st = lib.select_indices_flags(_ptr(flags), _ptr(out), _ptr(count), n, _ptr(ws), ws.numel(), sh)
+        _check(st, "select_indices_flags")
+        _after_call(ws, stream, "select_indices_flags")
     return out, count
 
 
@@ -652,11 +663,12 @@ def radix_sort(keys: torch.Tensor, values: torch.Tensor | None = None,
         out_values = torch.empty_like(values)
     stream, sh = _stream_handle(keys.device)
     need = ls_radix_sort_workspace_bytes(n, dt, values is not None)
-    ws = workspace_for(keys.device, stream, need, "sort")
-    st = lib.radix_sort(_ptr(keys), _ptr(out_keys), _ptr(values), _ptr(out_values), n, DTYPE_CODES[dt],
-                        _ptr(ws), ws.numel(), sh)
-    _check(st, "radix_sort")
-    _after_call(ws, stream, "radix_sort")
+    with _ws_lock:
+        ws = workspace_for(keys.device, stream, need, "sort")
+        st = lib.radix_sort(_ptr(keys), _ptr(out_keys), _ptr(values), _ptr(out_values), n, DTYPE_CODES[dt],
+                            _ptr(ws), ws.numel(), sh)
+        _check(st, "radix_sort")
+        _after_call(ws, stream, "radix_sort")
     return out_keys, (out_values if values is not None else None)
 
 
@@ -765,12 +777,13 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature: tor
     for t, name, dtype in ((top_k, "top_k", _I32), (top_p, "top_p", _F32), (min_p, "min_p", _F32)):
         if t is not None and not (t.dtype is dtype and t.get_device() == index and t.shape == one and t.is_contiguous()):
             _vector(t, name, dtype, rows, index)
-    ws = _sample_workspace(index, rows, vocab)
-    st = lib.sample_tokens(
-        logits.data_ptr(), rows, vocab, stride, code, uniforms.data_ptr(), temperature.data_ptr(),
-        None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
-        None if min_p is None else min_p.data_ptr(), out.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(index))
+    with _ws_lock:
+        ws = _sample_workspace(index, rows, vocab)
+        st = lib.sample_tokens(
+            logits.data_ptr(), rows, vocab, stride, code, uniforms.data_ptr(), temperature.data_ptr(),
+            None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+            None if min_p is None else min_p.data_ptr(), out.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel(),
+            _raw_stream(index))
     if st != LS_OK:
         raise LibscanError(st, "sample_tokens")
     return out, logprobs

@@ -1,5 +1,7 @@
 """The binding's workspaces, on the CPU: which buffer a call gets and which fills are
 enqueued for it, with host memory in place of the device's and streams and captures made up."""
+import threading
+import time
 from types import SimpleNamespace
 
 import pytest
@@ -87,3 +89,69 @@ def test_two_streams_of_one_capture(fills):
 
 def test_the_null_stream_is_never_captured():
     assert ps._capture_of(0) is None
+
+
+# ------------------------------------------------------------ host threads
+
+class Library:
+    """Stands for the library: a call on the workspace has to come from the thread that last
+    looked one up, and no other call may be under way."""
+
+    def __init__(self):
+        self.owner, self.inside, self.broken, self.calls = None, 0, [], 0
+
+    def lookup(self, *args):
+        self.owner = threading.get_ident()
+        time.sleep(0.002)
+        return torch.empty(1 << 16, dtype=torch.uint8)
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return lambda *args: ps.LS_OK
+
+        def call(*args):
+            self.inside += 1
+            if self.owner != threading.get_ident() or self.inside != 1:
+                self.broken.append(name)
+            time.sleep(0.002)
+            self.inside -= 1
+            self.calls += 1
+            return ps.LS_OK
+        return call
+
+
+def _entry_points():
+    x, f = torch.zeros(32, dtype=torch.int32), torch.zeros(32, dtype=torch.uint8)
+    logits, one = torch.zeros(2, 16), torch.ones(2)
+    return {
+        "scan_inclusive": lambda: ps.scan_inclusive(x), "scan_exclusive": lambda: ps.scan_exclusive(x),
+        "scan_ex": lambda: ps.scan_ex(x, scheme="reduce_then_scan"),
+        "segmented_scan": lambda: ps.segmented_scan(x, heads=f),
+        "segmented_scan_offsets": lambda: ps.segmented_scan(x, offsets=torch.tensor([0, 32])),
+        "compact_if": lambda: ps.compact_if(x, "lt", 1), "compact_flags": lambda: ps.compact_flags(x, f),
+        "select_indices_if": lambda: ps.select_indices_if(x, "lt", 1),
+        "select_indices_flags": lambda: ps.select_indices_flags(f), "radix_sort": lambda: ps.radix_sort(x),
+        "sample_tokens": lambda: ps.sample_tokens(logits, one, one, top_p=one),
+    }
+
+
+@pytest.mark.parametrize("name", list(_entry_points()))
+def test_a_call_keeps_its_workspace_while_it_enqueues(name, monkeypatch):
+    """Two host threads on one stream: from the lookup of the workspace to the end of the
+    library's call neither comes between the other's."""
+    lib, call = Library(), _entry_points()[name]
+    monkeypatch.setattr(ps, "_lib", lib)
+    monkeypatch.setattr(ps, "load_library", lambda: lib)
+    monkeypatch.setattr(ps, "_require_gpu", lambda *t: None)
+    monkeypatch.setattr(ps, "_stream_handle", lambda device: (stream(0), 0))
+    monkeypatch.setattr(ps, "_current_device", lambda: -1)
+    monkeypatch.setattr(ps, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(ps, "workspace_for", lib.lookup)
+    monkeypatch.setattr(ps, "_sample_workspace", lib.lookup)
+    monkeypatch.setattr(ps, "_checked", False)
+    threads = [threading.Thread(target=lambda: [call() for _ in range(5)]) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert lib.calls == 10 and not lib.broken
