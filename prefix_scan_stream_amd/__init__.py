@@ -196,7 +196,8 @@ _ws_cache: dict = {}    # (device index, stream handle) -> the uint8 workspace i
 _ws_uses: dict = {}     # calls on each cached status workspace since its last initialisation
 STATUS_REINIT_CALLS = 1 << 25
 _ws_graph: dict = {}    # the same key -> (capture, workspace) of the last graph captured there
-_ws_retired: list = []  # workspaces replaced by larger ones or given to a graph
+_ws_retired: list = []  # workspaces given to a graph
+WORKSPACE_DOUBLING_BYTES = 64 << 20
 
 
 def set_checked(on: bool = True) -> None:
@@ -277,12 +278,13 @@ def workspace_for(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
             return _graph_workspace(device, stream, nbytes, key, capture)
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
-            new = _new_workspace(device, stream, nbytes)
             if buf is not None:
-                _ws_retired.append(buf)
-            _ws_cache[key] = new
+                # at least twice the old one while small, so that needs that grow call by call (a row more
+                # each time) make few of them.  The old one has no graph to serve (_graph_workspace) and goes
+                # back to the stream's memory
+                nbytes = max(nbytes, min(2 * buf.numel(), WORKSPACE_DOUBLING_BYTES))
+            buf = _ws_cache[key] = _new_workspace(device, stream, nbytes)
             _ws_uses[key] = 0
-            buf = new
         elif kind == "status":
             # status words compare epochs modulo 2^26: zero the workspace again well
             # before that many calls (one fill kernel per 2^25 calls)
@@ -303,7 +305,7 @@ def workspace_error_flags(device=None, stream=None) -> int:
 
 
 def release_workspaces() -> None:
-    """Drop every cached and retired workspace (no graph that used one may be
+    """Drop every cached workspace and those given to graphs (no graph that used one may be
     replayed afterwards)."""
     _ws_cache.clear()
     _ws_graph.clear()

@@ -1,7 +1,9 @@
 """The binding's workspaces, on the CPU: which buffer a call gets and which fills are
 enqueued for it, with host memory in place of the device's and streams and captures made up."""
+import gc
 import threading
 import time
+import weakref
 from types import SimpleNamespace
 
 import pytest
@@ -155,3 +157,27 @@ def test_a_call_keeps_its_workspace_while_it_enqueues(name, monkeypatch):
     for t in threads:
         t.join()
     assert lib.calls == 10 and not lib.broken
+
+
+# ------------------------------------------------------------ growth
+
+def test_growing_batches_make_few_workspaces_and_keep_one(fills, monkeypatch):
+    """A batch that grows by a row a step: the buffers are made a few times, none that was
+    replaced is kept, and the last is at most about twice the need."""
+    made, new = [], ps._new_workspace
+    monkeypatch.setattr(ps, "_new_workspace", lambda *a: made.append(weakref.ref(w := new(*a))) or w, raising=False)
+    for rows in range(1, 513):
+        need = ps.ls_sample_workspace_bytes(rows, 131072)
+        ws = ps.workspace_for(CPU, stream(0), need, "sample")
+        assert ws.numel() >= need
+    assert len(made) < 16 and ws.numel() <= 2 * need + 256
+    gc.collect()
+    assert [ref() is not None for ref in made] == [False] * (len(made) - 1) + [True]
+    assert not ps._ws_retired
+
+
+def test_large_workspaces_grow_to_their_need(fills):
+    """No doubling where that would take a large part of the memory."""
+    limit = ps.WORKSPACE_DOUBLING_BYTES
+    ps.workspace_for(CPU, stream(0), limit, "sort")
+    assert ps.workspace_for(CPU, stream(0), limit + 5, "sort").numel() < limit + 512
