@@ -863,6 +863,7 @@ struct SharedCuts {
     double part_sum[SM_WAVES];
     uint64_t part_mass[SM_WAVES];
     uint32_t n_list, n_small, n_quarters, keep;
+    uint32_t goes_on;  // whether the row's last block has more to do (a word of its own: s.arrived is still being read)
     float top, low;
     double kept;
     Pick pick;
@@ -1770,7 +1771,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
         const bool done = settle(call, g, r, row, tops, top);
         sh.n_small = 0, sh.s.found = ~0u, sh.s.last = 0;
         const bool later = !done && g.split && p < 1.0;
-        sh.s.arrived = done || later ? 0u : 1u;
+        sh.goes_on = done || later ? 0u : 1u;
         sh.top = top;
         if (g.split && lane == 0)
             g.split_tops[r] = later ? top : __builtin_nanf("");
@@ -1778,7 +1779,7 @@ __global__ __launch_bounds__(SM_BLOCK) void sample_cut_kernel(SampleCall call, S
             find_segments(g, call.rows, r, row, sh, tops, few, k, least);
     }
     __syncthreads();
-    if (uniform(sh.s.arrived) == 0u)
+    if (uniform(sh.goes_on) == 0u)
         return;
     row.set_top(uniform(sh.top));
     row.set_temperature(call.temperature[r]);
