@@ -433,8 +433,8 @@ ls_status ls_sample_workspace_bytes(int64_t rows, int64_t vocab, size_t *bytes);
  *                r * row_stride.  Any alignment to the element.
  *   rows, vocab  0 <= rows, vocab < 2^31; row_stride >= vocab when rows > 1, or 0
  *                (every row the same).
- *   uniforms     rows float32 in [0, 1).  1 and above take the last kept token,
- *                negative ones and NaN count as 0.
+ *   uniforms     rows float32 in [0, 1).  1 and above take the last kept token whose
+ *                weight is not 0, negative ones and NaN count as 0.
  *   temperature  rows float32.  T <= 0 or NaN: the lowest index of M, with
  *                log-probability 0; the cuts and the random number do not matter.
  *   top_k, top_p, min_p  rows int32 / float32 / float32 each, or NULL: no such cut.

@@ -372,8 +372,12 @@ struct Row {
 };
 
 // ---------------------------------------------------------------- running sums
-// The place of u in a sum: u <= 0 and NaN count as 0.
-__device__ __forceinline__ double goal_of(double u, double total) { return u > 0.0 ? u * total : 0.0; }
+// The place of u in a sum: u <= 0 and NaN count as 0.  From 1 on it is past every running sum, whose rounding may
+// be more than the last tokens weigh: the last positive weight is taken.
+__device__ __forceinline__ double goal_of(double u, double total)
+{
+    return u > 0.0 ? (u < 1.0 ? u * total : double(__builtin_inff())) : 0.0;
+}
 
 // Sums of N values per lane: `incl` with the lanes before, `total` of all.
 template <int N>
@@ -830,10 +834,18 @@ __global__ __launch_bounds__(SM_ALL_BLOCK, 4) void sample_all_kernel(SampleCall 
     const double goal = goal_of(double(call.uniforms[r]), total);
     bool over;
     const int at = wave_first_over(v, goal, incl, before, over);
-    const int seg = at < 0 ? 0 : at / SM_PER_LANE * tops.per_lane + at % SM_PER_LANE;
-    const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
-    const uint32_t token =
-        wave_find_token<TYPE == LOGITS_F32 ? 2 : 4>(row, s0, s1, before, goal, [&](float x, uint32_t) { return row.weight(x); });
+    int seg = at < 0 ? 0 : at / SM_PER_LANE * tops.per_lane + at % SM_PER_LANE;
+    // u >= 1: from the last segment back, since a segment's sum may be 0 where a weight is not (it is relative to
+    // another logit), and the other way round
+    const bool last = goal == double(__builtin_inff());
+    if (last)
+        seg = g.segs - 1;
+    uint32_t token;
+    do {
+        const int s0 = seg * g.seg_steps, s1 = s0 + g.seg_steps < g.steps ? s0 + g.seg_steps : g.steps;
+        token = wave_find_token<TYPE == LOGITS_F32 ? 2 : 4>(row, s0, s1, before, goal,
+                                                            [&](float x, uint32_t) { return row.weight(x); });
+    } while (last && token == ~0u && --seg >= 0);
     write_token(call, r, row, token, total);
 }
 
@@ -1426,7 +1438,8 @@ __device__ __forceinline__ void cut_row(const SampleCall& call, int64_t r, const
     };
     double total;
     const double u = double(call.uniforms[r]);
-    if (in_parts && least == 0.0 && u > 0.0) {
+    // (u <= 0 and u >= 1 ask for the first and last weight of all, which the bins may have left out)
+    if (in_parts && least == 0.0 && u > 0.0 && u < 1.0) {
         for (uint32_t i = tid; i < sh.n_list; i += SM_BLOCK) {
             const uint64_t v = sh.list[i];
             if (v <= place)
