@@ -427,8 +427,11 @@ ls_status ls_sample_workspace_bytes(int64_t rows, int64_t vocab, size_t *bytes);
  *          their sum, and always the first (p <= 0 or NaN: only the first);
  *   min_p  keeps of those each token with w_i >= min(1, min_p) (<= 0 or NaN: all).
  * The token is the first index whose running sum of kept weights, in index order,
- * exceeds u times their sum Z.  Weights and sums are in 64 bits (single weights to a
- * relative 2^-50, sums over a row to 2^-44; below exp(-745) a weight is 0).
+ * exceeds u times their sum Z.  Weights and sums are in 64 bits: a weight 2^-e is
+ * right to a relative 2^-50 + e 2^-52 (below exp(-745) it is 0), a sum over a row to a
+ * relative 2^-44 if vocab <= 2^17 or there are no cuts; a cut by value (top_p, or a
+ * large top_k) of a longer row adds up to 2^-(61 - ceil(log2 vocab)), as bins of
+ * weight hold 64 bits: 2^-43 for 2^18 tokens, 2^-37 for 2^24, 2^-30 for 2^31.
  *   logits       rows x vocab elements of type t; row r starts at element
  *                r * row_stride.  Any alignment to the element.
  *   rows, vocab  0 <= rows, vocab < 2^31; row_stride >= vocab when rows > 1, or 0

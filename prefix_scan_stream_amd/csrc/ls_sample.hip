@@ -16,7 +16,8 @@
 // 64 bits: a double multiply-add issues at the rate of a single one here (5.5 cycles a
 // wave and SIMD against 5.3, measured), and 2^f is a polynomial: of degree 10 where single
 // weights count (exp2_poly, 2^-50.6), of degree 9 in the sums of a whole row (exp2_sum4,
-// 2^-44.6), of degree 6 in the bins (fill_bins, 2^-48.9).
+// 2^-44.6), of degree 6 in the bins (fill_bins, 2^-48.9).  The bins' integers round more than that:
+// to 2^-44.06 of a weight in rows of up to 2^17, and a bit more for each doubling (make_row).
 //
 // One launch.  A row is cut into segments, and its segments are shared out to blocks, so
 // that few rows still use the whole GPU.  Every block leaves what its segments hold in
@@ -548,6 +549,9 @@ __device__ __forceinline__ Row<TYPE> make_row(const SampleCall& call, const Samp
     row.vocab = call.vocab;
     row.steps = g.steps;
     row.index_bits = call.vocab > 1 ? 32 - __builtin_clz(uint32_t(call.vocab - 1)) : 0;
+    // A bin is a sum of up to vocab integers of at most 2^(frac + 1/16), a range of one (cut_in_bin) too.  Rounded to the
+    // unit, a weight is off by 2^-(frac + 0.94) of itself in a bin and 2^-(frac + 0.06) in a range, always the same way
+    // where logits are equal; 2^-44 up to 2^17 logits, 2^-(61 - index_bits) beyond.
     row.frac = 61 - row.index_bits < 44 ? 61 - row.index_bits : 44;
     row.inf = false;
     return row;
@@ -1316,9 +1320,9 @@ __device__ __forceinline__ Bin uniform_bin(const SharedCuts& sh)
 // The histogram of one wave's share of a row.  A weight is the weight 2^(-b/8) of its bin
 // times 2^(z/8), |z| <= 1/2, and the bin counts the second factor in units of 2^-frac: a
 // polynomial of degree 6 (relative error 2^-48.9) into whose last step the rounding to an
-// integer is folded, with no exponent to insert.  Below 2^-63.9 weights count as 0,
-// for less than 2^-46 of the sum of a row of 2^17: added to the last bin they would take turns at one
-// address (peaked rows: 200 of 42000 logits took 55 us, against 27).
+// integer is folded, with no exponent to insert.  Below 2^-63.9 weights count as 0, for at most
+// vocab 2^-63.9 of the sum (2^-46.9 in a row of 2^17, a quarter of the integers' rounding in any row): added to
+// the last bin they would take turns at one address (peaked rows: 200 of 42000 logits took 55 us, against 27).
 template <bool COUNTS, int TYPE>
 __device__ __forceinline__ void fill_bins(const Row<TYPE>& row, uint64_t* mass, uint32_t* count, int first, int end)
 {

@@ -87,3 +87,34 @@ def test_u_of_one_where_a_wave_starts_with_light_tokens(dtype):
     x[:, -2048:] = -75.0
     tokens, _ = ps.sample_tokens(x, vec([1.0] * 256), vec([0.1] * 256))
     assert to_host(tokens).tolist() == [vocab - 2049] * 256
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_equal_logits_of_a_very_long_row(dtype):
+    """One logit of 0 and 2^24 equal ones of -a, whose weights all round the same way in the bins.  Kept by
+    top-p are those in front of p Z, and the token is the first past u times their weight, both by division;
+    p and u are such that no boundary is nearer than 16 times what the sums may be off (2^-37)."""
+    vocab = (1 << 24) + 5
+    n = vocab - 1
+    rng = np.random.default_rng(24)
+    rows = []
+    while len(rows) < 4:
+        a, p, u = np.float32(rng.uniform(0.5, 12)), np.float32(rng.uniform(0.1, 0.99)), np.float32(rng.uniform(0.01, 0.99))
+        if dtype == "bf16":
+            a = np.float32(torch.tensor(a).bfloat16().float())
+        w = np.exp(-np.longdouble(a))
+        z = 1 + n * w
+        far = lambda at, total: abs(at - np.rint(at)) * w / total > 16 * np.longdouble(2)**-37
+        cut = (np.longdouble(p) * z - 1) / w  # the equal ones in front of it are kept
+        kept = int(np.ceil(cut))
+        goal = (np.longdouble(u) * (1 + kept * w) - 1) / w
+        if 1 < cut < n - 1 and 1 < goal and far(cut, z) and far(goal, 1 + kept * w):
+            rows.append((a, p, u, 1 + int(np.floor(goal)), float(-np.longdouble(a) - np.log(1 + kept * w))))
+    x = torch.empty(4, vocab, dtype=DTYPES[dtype], device=DEV)
+    for r, row in enumerate(rows):
+        x[r] = -float(row[0])
+    x[:, 0] = 0.0
+    tokens, lps = ps.sample_tokens(x, vec([row[2] for row in rows]), vec(np.ones(4)), top_p=vec([row[1] for row in rows]))
+    assert to_host(tokens).tolist() == [row[3] for row in rows]
+    for got, row in zip(to_host(lps), rows):
+        assert abs(float(got) - row[4]) <= 2.0**-24 * abs(row[4]) + 2.0**-36
