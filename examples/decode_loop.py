@@ -6,8 +6,9 @@ Each step, for a batch of requests of different lengths:
     pages_append   gives each request the pages its new tokens need (a prompt at first,
                    then one token a step);
     slot_map       says where these tokens go in the cache;
-    the model      writes their keys into the cache and makes logits (here: an embedding,
-                   one matrix, and the mean of the request's cached keys);
+    the model      writes their keys into the cache and makes logits (here: an embedding for a
+                   key, and one matrix on the sum of the request's cached keys, read back
+                   through the block table and divided by the root of their number);
     sample_tokens  picks a token a request;
     pages_release  puts the pages of finished requests back on the free list.
 Everything stays on the GPU; the loop reads nothing back until its end.  A request that is
@@ -23,8 +24,10 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import prefix_scan_stream_amd as ps
 
 
-def serve(requests=64, steps=40, page_size=16, vocab=4096, width=64, pages=None, longest=120, seed=0):
-    """Runs the loop; returns (tokens of the last step, lengths, tables, free pages, free count, generated)."""
+def serve(requests=64, steps=40, page_size=16, vocab=4096, width=64, pages=None, longest=120, seed=0, on_step=None):
+    """Runs the loop; returns (tokens of the last step, lengths, tables, free pages, free count, generated).
+    on_step, where given, gets each step's (request of each new key, key, sums of the requests' cached keys,
+    finished requests)."""
     dev = torch.device("cuda:0")
     g = torch.Generator(device=dev)
     g.manual_seed(seed)
@@ -33,13 +36,15 @@ def serve(requests=64, steps=40, page_size=16, vocab=4096, width=64, pages=None,
     # whole numbers, so that their sums do not depend on the order of the additions
     embed = torch.randint(-2, 3, (vocab, width), device=dev, generator=g).float()
     head = torch.randn(width, vocab, device=dev, generator=g) * 0.4
-    keys = torch.zeros(pages * page_size, width, device=dev)
+    # a slot more than the pages have: the keys of entries that are no token go there
+    keys = torch.zeros(pages * page_size + 1, width, device=dev)
+    spare = pages * page_size
+    at = torch.arange(columns * page_size, device=dev)
     tables = torch.full((requests, columns), -1, dtype=torch.int32, device=dev)
     free = torch.arange(pages, dtype=torch.int32, device=dev)
-    count, next_count = torch.full((1,), pages, device=dev), torch.empty(1, dtype=torch.int64, device=dev)
+    count = torch.full((1,), pages, device=dev)
     lens = torch.zeros(requests, dtype=torch.int32, device=dev)
     prompt = torch.randint(1, longest + 1, (requests,), dtype=torch.int32, device=dev, generator=g)
-    sums = torch.zeros(requests, width, device=dev)
     tokens = torch.randint(0, vocab, (requests,), device=dev, generator=g)
     generated = torch.zeros(requests, dtype=torch.int64, device=dev)
     temperature = torch.rand(requests, device=dev, generator=g) * 0.8 + 0.4
@@ -56,9 +61,10 @@ def serve(requests=64, steps=40, page_size=16, vocab=4096, width=64, pages=None,
         live = slots >= 0
         rows = owner.clamp_min(0).long()
         x = embed[(tokens[rows] + positions) % vocab] * live[:, None]
-        keys.index_copy_(0, torch.where(live, slots, torch.zeros_like(slots)), x)
-        sums.index_add_(0, rows, x)
+        keys.index_copy_(0, torch.where(live, slots, torch.full_like(slots, spare)), x)
         lens = lens + new
+        cached = tables[:, at // page_size].long() * page_size + at % page_size
+        sums = keys[torch.where(at < lens[:, None], cached, torch.full_like(cached, spare))].sum(1)
         logits = (sums / lens.clamp_min(1)[:, None].float().sqrt()) @ head
         uniforms = torch.rand(requests, device=dev, generator=g)
         picked, _ = ps.sample_tokens(logits, uniforms, temperature, top_k=top_k, top_p=top_p)
@@ -66,11 +72,11 @@ def serve(requests=64, steps=40, page_size=16, vocab=4096, width=64, pages=None,
         generated += granted
         # a token in eight ends its request; its row starts over with another prompt
         done = granted & (tokens % 8 == 0)
-        next_count = ps.pages_release(lens, done, tables, free, count, page_size)
-        count = next_count
+        count = ps.pages_release(lens, done, tables, free, count, page_size)
         tables.masked_fill_(done[:, None], -1)
         lens = lens.masked_fill(done, 0)
-        sums.masked_fill_(done[:, None], 0.0)
+        if on_step is not None:
+            on_step(owner, x, sums, done)
     return tokens, lens, tables, free, count, generated
 
 
