@@ -228,14 +228,17 @@ def ls_workspace_check(ws: torch.Tensor, stream=None) -> int:
     return flags.value
 
 
+_capture_status, _capture_number = ctypes.c_int(0), ctypes.c_ulonglong(0)
+_capture_refs = ctypes.byref(_capture_status), ctypes.byref(_capture_number)
+
+
 def _capture_of(handle: int) -> int | None:
-    """The number of the capture that a stream is in; None while it is in none."""
+    """The number of the capture that a stream is in; None while it is in none.  Under _ws_lock."""
     if handle == 0:  # the null stream cannot be captured
         return None
-    status, number = ctypes.c_int(0), ctypes.c_ulonglong(0)
-    if load_library().hipStreamGetCaptureInfo(handle, ctypes.byref(status), ctypes.byref(number)) != 0:
+    if (_lib or load_library()).hipStreamGetCaptureInfo(handle, *_capture_refs) != 0:
         raise LibscanError(LS_ERR_HIP, "hipStreamGetCaptureInfo")
-    return number.value if status.value else None
+    return _capture_number.value if _capture_status.value else None
 
 
 def _new_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int) -> torch.Tensor:
@@ -272,10 +275,12 @@ def workspace_for(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
     for the three-phase scan_ex schemes (plain scratch) and "sample" for
     sample_tokens.  While the stream is being captured, the workspace is that graph's own."""
     with _ws_lock:
-        key = (device.index, stream.cuda_stream, kind)
-        capture = _capture_of(stream.cuda_stream)
-        if capture is not None:
-            return _graph_workspace(device, stream, nbytes, key, capture)
+        handle = stream.cuda_stream
+        key = (device.index, handle, kind)
+        if handle != 0:
+            capture = _capture_of(handle)
+            if capture is not None:
+                return _graph_workspace(device, stream, nbytes, key, capture)
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
             if buf is not None:
@@ -795,7 +800,7 @@ def _sample_workspace(index: int, rows: int, vocab: int) -> torch.Tensor:
     """The current stream's workspace for sample_tokens (workspace_for's, found sooner)."""
     need, handle = ls_sample_workspace_bytes(rows, vocab), _raw_stream(index)
     buf = _ws_cache.get((index, handle, "sample"))
-    if buf is None or buf.numel() < need or (handle != 0 and torch.cuda.is_current_stream_capturing()):
+    if buf is None or buf.numel() < need or (handle != 0 and _capture_of(handle) is not None):
         device = torch.device("cuda", index)
         buf = workspace_for(device, torch.cuda.current_stream(device), need, "sample")
     return buf
