@@ -9,17 +9,21 @@
 // chunk's outputs, consecutive ones per turn.  Nothing is handed from block to
 // block, so there is no workspace, no wait and no second launch; the price is that each
 // block reads all counts, a few percent of the outputs' bytes at the sizes of a step.
-// Bound by the bytes of the outputs when there are many (prompts, an emptied cache), by
-// the latency of one scan (two dependent loads and three barriers) when there are few.
+// That is made for batches: up to 4096 requests 4-5 us for a step of a token each, then about
+// 2.5 us more for each 4096 in the grid's every block (16384: 13 us; 65536: 37-57; 2^20: 0.54-0.84 ms).
+// With few outputs bound by the latency of one scan (3.6-4.5 us against 2 of an empty kernel; a number of
+// requests that is no multiple of eight loads its last ones one by one, 1 us).  With many (prompts, an
+// emptied cache) 2-3.5 TB/s: each lane waits for an output's store before it loads the next.
 #include "ls_wave64.hpp"
 #include "ls_internal.hpp"
 
 namespace ls {
 
-// Measured for the outputs of 4096 prompts (2.9 M pages) / 2.9 M slots / 4.1 M released
+// Measured for the outputs of 4096 prompts (2.7 M pages) / 2.6 M slots / 4.1 M released
 // pages: 512 blocks of 512 threads 11.1 / 12.2 / 13.5 us; 256 blocks 12.4 / 14.8 / 18.8 (too
 // few waves), 768 blocks 13.2 / 14.0 / 12.4 and 1024 13.7 / 13.2 / 15.9 (the LDS holds three
-// blocks a CU, so the last ones start late); 256 blocks of 1024 threads 10.0 / 13.1 / 13.1.
+// blocks a CU, so the last ones start late); 256 blocks of 1024 threads 10.0 / 13.1 / 13.1.  No
+// grid is the best for all three; this one is kept for all, as the slots of every step have their best here.
 constexpr int PG_BLOCK = 512;
 constexpr int PG_WAVES = PG_BLOCK / 64;
 constexpr int PG_CHUNK = 4096;                  // requests per scan

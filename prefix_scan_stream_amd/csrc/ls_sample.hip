@@ -33,13 +33,13 @@
 //
 // Measured, in a graph, 131072 logits to a row:
 //   1 row, bfloat16, top-k 50, top-p, min-p: 12.4 us, the latency of the chain of steps: 2 us the launch, 2 the
-//   first read, 1 the counter, 4.5 one wave's search for the candidates' quarters, 2 their reading, 3 order
-//   and sums.  64 rows, top-k 100, top-p, min-p: 15.7 us.
+//   first read, 1 the counter, 4.5 the row's parameters (loaded one after the other) and one wave's search for the
+//   candidates' quarters, 2 their reading, 3 order and sums.  64 rows, top-k 100, top-p, min-p: 15.6 us.
 //   256 rows, bfloat16, top-p alone: 66 us, a row to a CU: 11 us the first read (6 TB/s over all), 25 the bins
 //   (16.5 vector instructions a logit), 14 the bin's elements, the rest the steps between.
 //   64 rows of flat logits (normal, a deviation of 0.5), top-p: 83 us, with two more readings for a bin of 13000.
-//   512 rows, no cuts: bfloat16 51 us, bound by vector instructions (22 a logit, 50 us at the measured rate);
-//   float32 58-62 us, with 268 MB to read beside them (4.5 TB/s).
+//   512 rows, no cuts: bfloat16 and float16 51 us, bound by vector instructions (21 a logit by the counters, 47 us at
+//   the measured rate); float32 57-62 us, 20 a logit with 268 MB to read beside them (4.3-4.7 TB/s).
 #include <type_traits>
 
 #include "ls_wave64.hpp"
@@ -705,8 +705,8 @@ __device__ __forceinline__ double careful_sum(const Row<TYPE>& row, int s0, int 
 // reaches from 2^-1000 to 2^1000, so a wave's weights can be taken relative to the largest
 // value of its first loads, whatever comes later: logits are held within 2^+-1000 of it, and a
 // sum that leaves 2^-800 .. 2^800 (as one with NaN in it may) is made again with the
-// segment's own largest value.  Bound by the logits' bytes in float32 and by the
-// multiply-adds (18 instructions a logit) in 16 bits.
+// segment's own largest value.  Bound by the logits' bytes in float32 and by the vector
+// instructions (21 a logit, 18 of them for the weight) in 16 bits.
 template <int TYPE>
 __global__ __launch_bounds__(SM_ALL_BLOCK, 4) void sample_all_kernel(SampleCall call, SampleGrid g)
 {
