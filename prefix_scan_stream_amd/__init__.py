@@ -196,7 +196,7 @@ _ws_cache: dict = {}    # (device index, stream handle) -> the uint8 workspace i
 _ws_uses: dict = {}     # calls on each cached status workspace since its last initialisation
 STATUS_REINIT_CALLS = 1 << 25
 _ws_graph: dict = {}    # the same key -> (capture, workspace) of the last graph captured there
-_ws_retired: list = []  # workspaces given to a graph
+_ws_retired: list = []  # (the same key, workspace given to a graph)
 WORKSPACE_DOUBLING_BYTES = 64 << 20
 
 
@@ -257,7 +257,7 @@ def _graph_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: in
         buf = _ws_cache.get(key)
         if buf is not None and buf.numel() >= nbytes:
             # filled by an eager call, and not used by one again
-            _ws_retired.append(_ws_cache.pop(key))
+            _ws_retired.append((key, _ws_cache.pop(key)))
             _ws_uses.pop(key, None)
         else:
             # the fill is a node of this graph, so only this graph may count on it
@@ -302,11 +302,19 @@ def workspace_for(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
 
 def workspace_error_flags(device=None, stream=None) -> int:
     """Error bits of the cached workspace of (device, stream) (defaults: cuda:0's
-    current stream); 0 when there is none yet.  Waits for the stream."""
+    current stream) and of those that graphs captured there have taken, the last such
+    graph's in any case (once it has been replayed); 0 when there is none yet.  Waits for
+    the stream; wait for the graphs' replays before."""
     device = torch.device(device if device is not None else "cuda:0")
     s = stream if stream is not None else torch.cuda.current_stream(device)
-    buf = _ws_cache.get((device.index, s.cuda_stream, "status"))
-    return 0 if buf is None else ls_workspace_check(buf, s)
+    key = (device.index, s.cuda_stream, "status")
+    with _ws_lock:
+        held = [_ws_cache.get(key), _ws_graph.get(key, (None, None))[1]]
+        held += [ws for taken, ws in _ws_retired if taken == key and ws is not held[1]]
+        flags = 0
+        for ws in held:
+            flags |= 0 if ws is None else ls_workspace_check(ws, s)
+    return flags
 
 
 def release_workspaces() -> None:

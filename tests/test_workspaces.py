@@ -42,7 +42,7 @@ def stream(handle):
 
 
 def alive(ws):
-    return any(ws is held for held in [*ps._ws_cache.values(), *ps._ws_retired])
+    return any(ws is held for held in [*ps._ws_cache.values(), *(kept for _, kept in ps._ws_retired)])
 
 
 KINDS = ["status", "sort", "phases", "sample"]
@@ -81,6 +81,27 @@ def test_a_graph_takes_the_workspace_of_a_stream_that_was_warmed_up(fills, kind)
     assert ps.workspace_for(CPU, s, 50_000, kind) is eager
     fills.capture[9] = 6
     assert ps.workspace_for(CPU, s, 50_000, kind) is eager and alive(warm) and alive(eager)
+
+
+def test_error_bits_of_a_graphs_workspace_are_reported(fills, monkeypatch):
+    """A call in a graph that gave up a wait shows on the stream it was captured on, whether the
+    graph took the stream's workspace or has one of its own."""
+    monkeypatch.setattr(ps, "ls_workspace_check", lambda ws, s: int(ws[8]))
+    s, device = stream(11), SimpleNamespace(index=None)
+    monkeypatch.setattr(torch, "device", lambda d: d)
+    assert ps.workspace_error_flags(device, s) == 0
+    ps.workspace_for(CPU, s, 1000)
+    buffers = []
+    for capture in (1, 2, 3):
+        fills.capture[11] = capture
+        buffers.append(ps.workspace_for(CPU, s, 1000))
+    del fills.capture[11]
+    buffers.append(ps.workspace_for(CPU, s, 1000))
+    assert ps.workspace_error_flags(device, s) == 0
+    for bit, ws in ((1, buffers[0]), (2, buffers[2]), (4, buffers[3])):  # taken, the last graph's own, eager
+        ws[8] = bit
+    assert ps.workspace_error_flags(device, s) == 7
+    assert ps.workspace_error_flags(device, stream(12)) == 0
 
 
 def test_two_streams_of_one_capture(fills):
