@@ -198,6 +198,7 @@ STATUS_REINIT_CALLS = 1 << 25
 _ws_graph: dict = {}    # the same key -> (capture, workspace) of the last graph captured there
 _ws_retired: list = []  # (the same key, workspace given to a graph)
 WORKSPACE_DOUBLING_BYTES = 64 << 20
+WORKSPACES_TAKEN_BYTES = 256 << 20  # most that graphs take of streams' workspaces, as these are kept for good
 
 
 def set_checked(on: bool = True) -> None:
@@ -241,27 +242,31 @@ def _capture_of(handle: int) -> int | None:
     return _capture_number.value if _capture_status.value else None
 
 
-def _new_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int) -> torch.Tensor:
+def _new_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
+                   fill: int | None = None) -> torch.Tensor:
+    """A workspace whose first `fill` bytes (None: all) are zero."""
     with torch.cuda.stream(stream):  # while it is being captured: from the graph's pool
         new = torch.empty((max(nbytes, 1 << 16) + 255) & ~255, dtype=torch.uint8, device=device)
-    ls_workspace_init(new, stream)
+    ls_workspace_init(new[:fill], stream)
     return new
 
 
-def _graph_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int, key: tuple,
-                     capture: int) -> torch.Tensor:
+def _graph_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int, kind: str,
+                     key: tuple, capture: int) -> torch.Tensor:
     """The workspace of the graph that is being captured on `stream`, for no other graph
     and no eager call: these could run between or beside its replays."""
     last, buf = _ws_graph.get(key, (None, None))
     if last != capture or buf.numel() < nbytes:
         buf = _ws_cache.get(key)
-        if buf is not None and buf.numel() >= nbytes:
+        if buf is not None and buf.numel() >= nbytes and \
+                buf.numel() + sum(ws.numel() for _, ws in _ws_retired) <= WORKSPACES_TAKEN_BYTES:
             # filled by an eager call, and not used by one again
             _ws_retired.append((key, _ws_cache.pop(key)))
             _ws_uses.pop(key, None)
         else:
-            # the fill is a node of this graph, so only this graph may count on it
-            buf = _new_workspace(device, stream, nbytes)
+            # the fill is a node of this graph, so only this graph may count on it; plain scratch needs
+            # none but its header's error word
+            buf = _new_workspace(device, stream, nbytes, None if kind in ("status", "sample") else 256)
         _ws_graph[key] = (capture, buf)
     return buf
 
@@ -280,7 +285,7 @@ def workspace_for(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
         if handle != 0:
             capture = _capture_of(handle)
             if capture is not None:
-                return _graph_workspace(device, stream, nbytes, key, capture)
+                return _graph_workspace(device, stream, nbytes, kind, key, capture)
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
             if buf is not None:

@@ -4,6 +4,7 @@ import gc
 import threading
 import time
 import weakref
+from contextlib import nullcontext
 from types import SimpleNamespace
 
 import pytest
@@ -17,15 +18,15 @@ CPU = torch.device("cpu")
 @pytest.fixture
 def fills(monkeypatch):
     """Captures by stream handle, and the (buffer's address, capture) of each fill."""
-    state = SimpleNamespace(capture={}, log=[])
+    state = SimpleNamespace(capture={}, log=[], made=getattr(ps, "_new_workspace", None))
 
     def init(ws, stream):
         ws.zero_()
         state.log.append((ws.data_ptr(), state.capture.get(stream.cuda_stream)))
 
-    def new(device, stream, nbytes):
+    def new(device, stream, nbytes, fill=None):
         ws = torch.empty((max(nbytes, 1 << 16) + 255) & ~255, dtype=torch.uint8)
-        init(ws, stream)
+        init(ws[:fill], stream)
         return ws
 
     monkeypatch.setattr(ps, "ls_workspace_init", init)
@@ -81,6 +82,32 @@ def test_a_graph_takes_the_workspace_of_a_stream_that_was_warmed_up(fills, kind)
     assert ps.workspace_for(CPU, s, 50_000, kind) is eager
     fills.capture[9] = 6
     assert ps.workspace_for(CPU, s, 50_000, kind) is eager and alive(warm) and alive(eager)
+
+
+def test_graphs_take_no_more_than_so_much(fills, monkeypatch):
+    """A program that warms up and captures again and again: what is kept for its graphs ends at the
+    limit, and graphs past it have their own fill."""
+    monkeypatch.setattr(ps, "WORKSPACES_TAKEN_BYTES", 5 << 16)
+    s, taken = stream(13), 0
+    for capture in range(1, 20):
+        warm = ps.workspace_for(CPU, s, 1 << 16)
+        fills.capture[13] = capture
+        ws = ps.workspace_for(CPU, s, 1 << 16)
+        assert ws is warm or fills.log[-1] == (ws.data_ptr(), capture)
+        taken += ws is warm
+        del fills.capture[13]
+    assert taken == 5 == len(ps._ws_retired)
+
+
+@pytest.mark.parametrize("kind,filled", [("status", 70_144), ("sample", 70_144), ("sort", 256), ("phases", 256)])
+def test_fill_of_a_graphs_own_workspace(fills, monkeypatch, kind, filled):
+    """Plain scratch is not filled at every replay, its header apart."""
+    log = []
+    monkeypatch.setattr(ps, "ls_workspace_init", lambda ws, s: log.append(ws.numel()))
+    monkeypatch.setattr(ps, "_new_workspace", fills.made)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: nullcontext())
+    fills.capture[14] = 1
+    assert ps.workspace_for(CPU, stream(14), 70_000, kind).numel() == 70_144 and log == [filled]
 
 
 def test_error_bits_of_a_graphs_workspace_are_reported(fills, monkeypatch):
