@@ -43,7 +43,8 @@
  *   - Status workspaces, of the single-pass scans (scan_inclusive,
  *     scan_exclusive, scan_ex with a single-pass scheme), segmented scans and
  *     compactions: zero-filled once before first use, by ls_workspace_init (or
- *     any zero fill of the whole buffer).  Every call leaves the workspace ready
+ *     any zero fill of the whole buffer; one that is only captured into a graph
+ *     counts for that graph's calls alone).  Every call leaves the workspace ready
  *     for the next, so calls enqueue no clearing work of their own.  Between
  *     calls its contents must not change, and it must serve no other purpose: a
  *     status workspace used by a radix sort or a three-phase scan_ex, or written
