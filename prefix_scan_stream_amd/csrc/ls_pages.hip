@@ -21,8 +21,8 @@ namespace ls {
 
 // Measured for the outputs of 4096 prompts (2.7 M pages) / 2.6 M slots / 4.1 M released
 // pages: 512 blocks of 512 threads 11.1 / 12.2 / 13.5 us; 256 blocks 12.4 / 14.8 / 18.8 (too
-// few waves), 768 blocks 13.2 / 14.0 / 12.4 and 1024 13.7 / 13.2 / 15.9 (the LDS holds three
-// blocks a CU, so the last ones start late); 256 blocks of 1024 threads 10.0 / 13.1 / 13.1.  No
+// few waves), 768 blocks 13.2 / 14.0 / 12.4 and 1024 13.7 / 13.2 / 15.9 (the registers, 88 / 90 / 74, leave a CU
+// two blocks, of the last operator three, so later ones start late); 256 blocks of 1024 threads 10.0 / 13.1 / 13.1.  No
 // grid is the best for all three; this one is kept for all, as the slots of every step have their best here.
 constexpr int PG_BLOCK = 512;
 constexpr int PG_WAVES = PG_BLOCK / 64;
