@@ -173,7 +173,8 @@ def prepare(case, seed):
 
 def _maps(s):
     """The maps h -> a h + b of all tokens, and 1 - a."""
-    x, g = s["x"].float(), s["gate"].float()
+    # copies, also of float32: what follows adds to them in place
+    x, g = s["x"].to(torch.float32, copy=True), s["gate"].to(torch.float32, copy=True)
     if s["gating"] == "sigmoid":
         a, rest = 1 / (1 + torch.exp(-g)), 1 / (1 + torch.exp(g))
         return a, rest * x, rest
@@ -216,7 +217,7 @@ def _plain_train(s):
     b[:, 0] += a[:, 0] * first
     h = _compose(a, b, 1)
     before = torch.cat([first[:, None], h[:, :-1]], 1)
-    dout = s["dout"].float()
+    dout = s["dout"].to(torch.float32, copy=True)
     if s["dstate_out"] is not None:
         dout[:, -1] += s["dstate_out"]
     # from the last token to the first, with the decay of the token behind
