@@ -507,6 +507,133 @@ ls_status pages_release(const int32_t *lens, const uint8_t *finished, int64_t re
                         int64_t columns, int64_t table_stride, int32_t *free_pages, int64_t free_capacity,
                         const int64_t *free_count, int64_t page_size, int64_t *count_out, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * A layer's scans: a gated linear recurrence over the tokens of each sequence, and
+ * tokens to the rows of their experts and back, each with its gradients.  The common
+ * rules hold: asynchronous on `stream`, arguments checked on the host before anything is
+ * enqueued, kernels only (so calls can be captured in a graph), no library call.
+ * Elements are float32, float16 or bfloat16 (ls_logits); states, sums and products are
+ * in float32, and each output is rounded once.  Results are the same bits on every run.
+ * ------------------------------------------------------------------------- */
+
+/* What a gate value g means: the decay a, and what token x puts in.
+ *   LS_GATE_DECAY    a = g,                 h = a h + x
+ *   LS_GATE_LOG      a = exp(g),            h = a h + x
+ *   LS_GATE_SIGMOID  a = 1 / (1 + exp(-g)), h = a h + (1 - a) x */
+typedef enum ls_gating { LS_GATE_DECAY = 0, LS_GATE_LOG = 1, LS_GATE_SIGMOID = 2 } ls_gating;
+
+/* Most channels of a row in the calls below. */
+#define LS_MAX_CHANNELS (1LL << 23)
+/* A recurrence keeps its value in front of every 64th row, for its gradients. */
+#define LS_RECURRENCE_PERIOD 64
+
+/* Rows of the array of carries: ceil(rows / LS_RECURRENCE_PERIOD), of each sequence, or once
+ * where the rows are packed (packed != 0).  Errors: LS_ERR_INVALID_ARG for sizes outside
+ * gated_recurrence's, or carry_rows == NULL. */
+ls_status ls_recurrence_carry_rows(int64_t sequences, int64_t rows, int packed, int64_t *carry_rows);
+
+/* Workspace size for gated_recurrence and gated_recurrence_backward of these sizes; 0 where
+ * they need none.  Errors: LS_ERR_INVALID_ARG for sizes outside gated_recurrence's, an
+ * unknown type or bytes == NULL. */
+ls_status ls_recurrence_workspace_bytes(int64_t sequences, int64_t rows, int64_t channels, int packed, ls_logits t,
+                                        size_t *bytes);
+
+/* h_t = a_t h_{t-1} + b_t for the tokens t of each sequence, channel by channel, with a and b
+ * from the gate and x as ls_gating says, and h_0 the sequence's state.
+ *   x, gate, out   elements of type t.  Channel c of token r of sequence s is element
+ *                  s * sequence_stride + r * row_stride + c.  Inputs may overlap each other and
+ *                  themselves (stride 0: the same row for all); the output's rows lie apart,
+ *                  sequence after sequence or token after token.
+ *   offsets        NULL: each of `sequences` sequences has `rows` tokens.  Else sequences + 1
+ *                  int64 on the device: sequence s is the rows offsets[s] .. offsets[s + 1] - 1
+ *                  of one matrix of `rows` rows (sequence strides are not used), offsets[0] == 0,
+ *                  none below the one before it, the last at most `rows`; sequences may be
+ *                  empty.  Rows behind the last sequence are not written.  Offsets that break these
+ *                  rules give unspecified results but no access outside the buffers.
+ *   state          sequences x channels float32, row s at element s * state_stride, or NULL: zeros.
+ *   state_out      the same with state_out_stride: h after each sequence's last token, not
+ *                  rounded; the state itself for a sequence without tokens.  It may be `state`
+ *                  (same pointer and stride), and else overlaps nothing.
+ *   carries        NULL, or ls_recurrence_carry_rows x channels float32, for
+ *                  gated_recurrence_backward.
+ *   sequences, rows, channels   0 <= sequences, rows < 2^31; 0 <= channels <= LS_MAX_CHANNELS.
+ *   ws             >= ls_recurrence_workspace_bytes bytes, 16-byte aligned, zero-filled once by
+ *                  ls_workspace_init before its first use; each call leaves it ready for the next.
+ *                  It serves the two recurrence calls only.  May be NULL where the size is 0.
+ * Decays of magnitude up to 1 are meant; larger ones work while the products of the decays of
+ * any run of tokens stay within float32.  A sequence's infinities and NaN stay its own.
+ * Errors: LS_ERR_INVALID_ARG (sizes, strides, NULL, alignment to the element, overlap, enums),
+ * LS_ERR_WORKSPACE. */
+ls_status gated_recurrence(const void *x, int64_t x_sequence_stride, int64_t x_row_stride, const void *gate,
+                           int64_t gate_sequence_stride, int64_t gate_row_stride, void *out,
+                           int64_t out_sequence_stride, int64_t out_row_stride, const float *state,
+                           int64_t state_stride, float *state_out, int64_t state_out_stride, float *carries,
+                           const int64_t *offsets, int64_t sequences, int64_t rows, int64_t channels, ls_logits t,
+                           ls_gating gating, void *ws, size_t ws_bytes, void *stream);
+
+/* The gradients of gated_recurrence: from dout, that of out, and dstate_out, that of state_out
+ * (NULL: zeros), those of x, gate and state.  x, gate, state, offsets, sizes, type and gating
+ * are the forward call's, carries what it wrote.  dx and dgate have the type t, dstate is
+ * float32; rows behind the last sequence are not written.  No output overlaps any other
+ * buffer.  h is made again from x and gate in float32. */
+ls_status gated_recurrence_backward(const void *dout, int64_t dout_sequence_stride, int64_t dout_row_stride,
+                                    const void *x, int64_t x_sequence_stride, int64_t x_row_stride, const void *gate,
+                                    int64_t gate_sequence_stride, int64_t gate_row_stride, const float *carries,
+                                    const float *state, int64_t state_stride, const float *dstate_out,
+                                    int64_t dstate_out_stride, void *dx, int64_t dx_sequence_stride,
+                                    int64_t dx_row_stride, void *dgate, int64_t dgate_sequence_stride,
+                                    int64_t dgate_row_stride, float *dstate, int64_t dstate_stride,
+                                    const int64_t *offsets, int64_t sequences, int64_t rows, int64_t channels,
+                                    ls_logits t, ls_gating gating, void *ws, size_t ws_bytes, void *stream);
+
+#define LS_MAX_EXPERTS 1024
+
+/* Workspace size for experts_sort.  Errors: LS_ERR_INVALID_ARG for sizes outside
+ * experts_sort's or bytes == NULL. */
+ls_status ls_experts_workspace_bytes(int64_t pairs, int64_t num_experts, size_t *bytes);
+
+/* A stable sort of (token, expert) pairs by expert.
+ *   experts      pairs int32 or int64 (id_bits 32 or 64): the expert of each pair, pair
+ *                token * top + choice.  A number outside [0, num_experts) sends its pair nowhere.
+ *   offsets      num_experts + 1 int64: expert e has the rows offsets[e] .. offsets[e + 1] - 1.
+ *   order        pairs int32: the pair of each row, -1 behind the last row.
+ *   places       pairs int32: the row of each pair, or -1.
+ *   pairs, num_experts   0 <= pairs < 2^31; 1 <= num_experts <= LS_MAX_EXPERTS.
+ *   ws           >= ls_experts_workspace_bytes bytes, 16-byte aligned; plain scratch.
+ * Errors: LS_ERR_INVALID_ARG (sizes, NULL, alignment, outputs that overlap anything),
+ * LS_ERR_WORKSPACE. */
+ls_status experts_sort(const void *experts, int id_bits, int64_t pairs, int64_t num_experts, int64_t *offsets,
+                       int32_t *order, int32_t *places, void *ws, size_t ws_bytes, void *stream);
+
+/* Tokens to the rows of their pairs: rows[places[token * top + j]] = x[token].
+ *   x            tokens x channels elements of type t, row r at element r * x_stride.
+ *   places       tokens * top int32, as experts_sort gives them: different rows for different
+ *                pairs.  A place outside [0, num_rows) takes part in nothing.
+ *   rows         num_rows x channels, at rows_stride; rows that no place names are not written.
+ *   sizes        0 <= tokens, top, num_rows, tokens * top < 2^31; channels <= LS_MAX_CHANNELS.
+ * Its gradient is experts_combine without weights.  Errors: LS_ERR_INVALID_ARG. */
+ls_status experts_gather(const void *x, int64_t x_stride, const int32_t *places, void *rows, int64_t rows_stride,
+                         int64_t tokens, int64_t top, int64_t num_rows, int64_t channels, ls_logits t, void *stream);
+
+/* The rows of each token's pairs, weighted and added up in the order of its pairs:
+ * out[token] = sum over j of weights[token * top + j] * rows[places[token * top + j]]; zeros for
+ * a token without a row.
+ *   weights      tokens * top elements of type weight_type, or NULL: ones.  The weight of a
+ *                pair without a row is not read.
+ * Other arguments as for experts_gather.  Without weights, its gradient is experts_gather. */
+ls_status experts_combine(const void *rows, int64_t rows_stride, const int32_t *places, const void *weights,
+                          ls_logits weight_type, void *out, int64_t out_stride, int64_t tokens, int64_t top,
+                          int64_t num_rows, int64_t channels, ls_logits t, void *stream);
+
+/* The gradients of experts_combine with weights: drows[place] = weight * dout[token], and
+ * dweights[pair] = the product of dout[token] and rows[place] summed over the channels, 0 for a pair
+ * without a row.  drows has the type t, its rows that no place names are not written; dweights
+ * has the type weight_type. */
+ls_status experts_combine_backward(const void *dout, int64_t dout_stride, const void *rows, int64_t rows_stride,
+                                   const int32_t *places, const void *weights, ls_logits weight_type, void *drows,
+                                   int64_t drows_stride, void *dweights, int64_t tokens, int64_t top, int64_t num_rows,
+                                   int64_t channels, ls_logits t, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,7 +38,9 @@ __all__ = [
     "segmented_scan", "ls_segmented_workspace_bytes", "scan_noalloc", "SCAN_NOALLOC_MAX_N",
     "ls_workspace_init", "ls_workspace_check", "set_checked", "workspace_error_flags",
     "release_workspaces", "sample_tokens", "ls_sample_workspace_bytes", "pages_append", "slot_map",
-    "pages_release",
+    "pages_release", "gated_recurrence", "gated_recurrence_backward", "recurrence_carries",
+    "ls_recurrence_workspace_bytes", "experts_sort", "experts_gather", "experts_combine",
+    "experts_combine_backward", "ls_experts_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -51,6 +53,7 @@ CMP_CODES = {"lt": 0, "le": 1, "gt": 2, "ge": 3, "eq": 4, "ne": 5}
 SCHEME_CODES = {"single_pass": 0, "reduce_then_scan": 1, "scan_then_propagate": 2,
                 "deterministic": 3}
 LOGITS_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+GATING_CODES = {"decay": 0, "log": 1, "sigmoid": 2}
 BLOCK_SCAN_CODES = {"wave_dpp": 0, "hillis_steele": 1, "hillis_steele_double": 2, "blelloch": 3}
 _TORCH_DTYPES = {torch.int32: "int32", torch.float32: "float32"}
 if hasattr(torch, "uint32"):
@@ -145,6 +148,26 @@ def load_library():
         lib.slot_map.restype = I
         lib.pages_release.argtypes = [P, P, I64, P, I64, I64, P, I64, P, I64, P, P]
         lib.pages_release.restype = I
+        lib.ls_recurrence_carry_rows.argtypes = [I64, I64, I, ctypes.POINTER(I64)]
+        lib.ls_recurrence_carry_rows.restype = I
+        lib.ls_recurrence_workspace_bytes.argtypes = [I64, I64, I64, I, I, ctypes.POINTER(SZ)]
+        lib.ls_recurrence_workspace_bytes.restype = I
+        lib.gated_recurrence.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, I64, P, I64, P, P, I64, I64, I64, I, I,
+                                         P, SZ, P]
+        lib.gated_recurrence.restype = I
+        lib.gated_recurrence_backward.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, P, I64, P, I64, P, I64, I64, P,
+                                                  I64, I64, P, I64, P, I64, I64, I64, I, I, P, SZ, P]
+        lib.gated_recurrence_backward.restype = I
+        lib.ls_experts_workspace_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+        lib.ls_experts_workspace_bytes.restype = I
+        lib.experts_sort.argtypes = [P, I, I64, I64, P, P, P, P, SZ, P]
+        lib.experts_sort.restype = I
+        lib.experts_gather.argtypes = [P, I64, P, P, I64, I64, I64, I64, I64, I, P]
+        lib.experts_gather.restype = I
+        lib.experts_combine.argtypes = [P, I64, P, P, I, P, I64, I64, I64, I64, I64, I, P]
+        lib.experts_combine.restype = I
+        lib.experts_combine_backward.argtypes = [P, I64, P, I64, P, P, I, P, I64, P, I64, I64, I64, I64, I, P]
+        lib.experts_combine_backward.restype = I
         # of the HIP runtime that libscan.so is linked with
         lib.hipStreamGetCaptureInfo.argtypes = [P, ctypes.POINTER(I), ctypes.POINTER(ctypes.c_ulonglong)]
         lib.hipStreamGetCaptureInfo.restype = I
@@ -266,7 +289,7 @@ def _graph_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: in
         else:
             # the fill is a node of this graph, so only this graph may count on it; plain scratch needs
             # none but its header's error word
-            buf = _new_workspace(device, stream, nbytes, None if kind in ("status", "sample") else 256)
+            buf = _new_workspace(device, stream, nbytes, None if kind in ("status", "sample", "recurrence") else 256)
         _ws_graph[key] = (capture, buf)
     return buf
 
@@ -277,8 +300,9 @@ def workspace_for(device: torch.device, stream: torch.cuda.Stream, nbytes: int,
     nbytes.  Kinds keep apart what the C ABI requires to be apart: "status" for the
     single-pass scans, segmented scans and compactions (tile status words that must
     never be overwritten with other data), "sort" for the radix sort, "phases"
-    for the three-phase scan_ex schemes (plain scratch) and "sample" for
-    sample_tokens.  While the stream is being captured, the workspace is that graph's own."""
+    for the three-phase scan_ex schemes (plain scratch), "sample" for
+    sample_tokens, "recurrence" for the gated recurrence and its gradients, and "experts" for
+    experts_sort (plain scratch).  While the stream is being captured, the workspace is that graph's own."""
     with _ws_lock:
         handle = stream.cuda_stream
         key = (device.index, handle, kind)
@@ -312,13 +336,14 @@ def workspace_error_flags(device=None, stream=None) -> int:
     the stream; wait for the graphs' replays before."""
     device = torch.device(device if device is not None else "cuda:0")
     s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (device.index, s.cuda_stream, "status")
+    flags = 0
     with _ws_lock:
-        held = [_ws_cache.get(key), _ws_graph.get(key, (None, None))[1]]
-        held += [ws for taken, ws in _ws_retired if taken == key and ws is not held[1]]
-        flags = 0
-        for ws in held:
-            flags |= 0 if ws is None else ls_workspace_check(ws, s)
+        for kind in ("status", "recurrence"):
+            key = (device.index, s.cuda_stream, kind)
+            held = [_ws_cache.get(key), _ws_graph.get(key, (None, None))[1]]
+            held += [ws for taken, ws in _ws_retired if taken == key and ws is not held[1]]
+            for ws in held:
+                flags |= 0 if ws is None else ls_workspace_check(ws, s)
     return flags
 
 
@@ -944,3 +969,362 @@ def pages_release(lens: torch.Tensor, finished: torch.Tensor, tables: torch.Tens
     if st != LS_OK:
         raise LibscanError(st, "pages_release")
     return count_out
+
+
+# ------------------------------------------------------------ a layer's scans
+
+def _element_code(t) -> int:
+    code = LOGITS_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"libscan: unsupported dtype {t.dtype} (float32, float16, bfloat16)")
+    return code
+
+
+def _like_rows(t, name: str, x) -> tuple:
+    """(address, sequence stride, row stride) of a tensor of x's shape, type and device whose
+    channels are contiguous; the sequence stride of packed rows is 0."""
+    if t.shape != x.shape or t.dtype is not x.dtype or t.get_device() != x.get_device():
+        _require_gpu(t)
+        raise ValueError(f"libscan: {name} must be of x's shape, dtype and device: {tuple(x.shape)}, {x.dtype}, {x.device}")
+    stride = t.stride()
+    if stride[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0:
+        raise ValueError(f"libscan: the channels of {name} must be contiguous")
+    return t.data_ptr(), 0 if len(stride) == 2 else stride[0], stride[-2]
+
+
+def _state_rows(t, name: str, sequences: int, channels: int, index: int) -> tuple:
+    """(address, row stride) of a state, one row for each sequence; of None (NULL, channels)."""
+    if t is None:
+        return None, channels
+    if t.dtype is not _F32 or t.shape != (sequences, channels) or t.get_device() != index:
+        _require_gpu(t)
+        raise ValueError(f"libscan: {name} must be float32 of {sequences} x {channels} on cuda:{index}")
+    stride, step = t.stride()
+    if step != 1 and channels > 1 and sequences > 0:
+        raise ValueError(f"libscan: the rows of {name} must be contiguous")
+    return t.data_ptr(), stride
+
+
+def _sequences_of(x, offsets) -> tuple:
+    """(sequences, rows, channels, address of the offsets): x is sequences x rows x channels;
+    or, with offsets, packed rows x channels; or, without, one token a sequence."""
+    _require_gpu(x, offsets)
+    if offsets is None:
+        if x.dim() == 3:
+            return (*x.shape, None)
+        if x.dim() != 2:
+            raise ValueError("libscan: x must be sequences x tokens x channels, or rows x channels")
+        return x.shape[0], 1, x.shape[1], None
+    if x.dim() != 2:
+        raise ValueError("libscan: packed x must be rows x channels")
+    if offsets.dtype is not _I64 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() < 1 \
+            or offsets.get_device() != x.get_device():
+        raise ValueError("libscan: offsets must be a contiguous int64 vector of sequences + 1 entries on x's device")
+    return offsets.numel() - 1, x.shape[0], x.shape[1], offsets.data_ptr()
+
+
+def _tokens_apart(rows: tuple, x, offsets) -> tuple:
+    """Of one token a sequence, the row stride is the sequences'."""
+    return (rows[0], rows[2], 0) if offsets is None and x.dim() == 2 else rows
+
+
+def _gating(gating: str) -> int:
+    code = GATING_CODES.get(gating)
+    if code is None:
+        raise ValueError(f"libscan: gating must be one of {sorted(GATING_CODES)}, not {gating!r}")
+    return code
+
+
+def ls_recurrence_workspace_bytes(sequences: int, rows: int, channels: int, packed: bool, dtype: torch.dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().ls_recurrence_workspace_bytes(sequences, rows, channels, 1 if packed else 0, LOGITS_CODES[dtype],
+                                                        ctypes.byref(out)), "ls_recurrence_workspace_bytes")
+    return out.value
+
+
+def recurrence_carries(x: torch.Tensor, offsets: torch.Tensor | None = None) -> torch.Tensor:
+    """An array for gated_recurrence's carries, which its gradients need."""
+    sequences, rows, channels, packed = _sequences_of(x, offsets)
+    n = ctypes.c_int64(0)
+    _check(load_library().ls_recurrence_carry_rows(sequences, rows, 0 if packed is None else 1, ctypes.byref(n)),
+           "ls_recurrence_carry_rows")
+    return torch.empty(n.value, channels, dtype=torch.float32, device=x.device)
+
+
+def _carries(t, x, offsets, sequences: int, rows: int, channels: int, index: int):
+    if t is None:
+        return None
+    n = ctypes.c_int64(0)
+    _check(load_library().ls_recurrence_carry_rows(sequences, rows, 0 if offsets is None else 1, ctypes.byref(n)),
+           "ls_recurrence_carry_rows")
+    if t.dtype is not _F32 or t.shape != (n.value, channels) or not t.is_contiguous() or t.get_device() != index:
+        _require_gpu(t)
+        raise ValueError("libscan: carries must be recurrence_carries(x, offsets)")
+    return t.data_ptr()
+
+
+def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, state: torch.Tensor | None = None, gating: str = "sigmoid",
+                     offsets: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     state_out: torch.Tensor | None = None, carries: torch.Tensor | None = None):
+    """h_t = a_t h_{t-1} + b_t over the tokens of each sequence, channel by channel, from the
+    sequence's state (None: zeros).  gating: "decay" (a = gate, b = x), "log" (a = exp(gate),
+    b = x) or "sigmoid" (a = sigmoid(gate), b = (1 - a) x).
+
+    x and gate (float32, float16 or bfloat16; channels contiguous, at any strides) are
+    sequences x tokens x channels; sequences x channels for one token each; or, with
+    `offsets` (int64, one more than sequences, from 0), rows x channels with sequence s in the rows
+    offsets[s] .. offsets[s + 1] - 1, possibly none.  Rows behind the last sequence are left
+    as they are in `out`.  States are float32, sequences x channels, and so are sums; state_out may be
+    state.  carries, from recurrence_carries, receives what the gradients need.
+
+    Returns (out, state_out), written into the tensors given: h, and h after each
+    sequence's last token."""
+    lib = _lib or load_library()
+    sequences, rows, channels, packed = _sequences_of(x, offsets)
+    code, kind, index = _element_code(x), _gating(gating), x.get_device()
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return gated_recurrence(x, gate, state, gating, offsets, out, state_out, carries)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if state_out is None:
+        state_out = torch.empty(sequences, channels, dtype=_F32, device=x.device)
+    args = (*_tokens_apart(_like_rows(x, "x", x), x, offsets), *_tokens_apart(_like_rows(gate, "gate", x), x, offsets),
+            *_tokens_apart(_like_rows(out, "out", x), x, offsets), *_state_rows(state, "state", sequences, channels, index),
+            *_state_rows(state_out, "state_out", sequences, channels, index),
+            _carries(carries, x, offsets, sequences, rows, channels, index), packed, sequences, rows, channels, code, kind)
+    _recurrence_call(lib.gated_recurrence, "gated_recurrence", args, packed, sequences, rows, channels, code, index)
+    return out, state_out
+
+
+_size_out = ctypes.c_size_t(0)
+_size_ref = ctypes.byref(_size_out)
+
+
+def _recurrence_call(fn, name: str, args: tuple, packed, sequences: int, rows: int, channels: int, code: int,
+                     index: int) -> None:
+    handle = _raw_stream(index)
+    if packed is None and rows <= 1:  # no carries between blocks: no workspace
+        st = fn(*args, None, 0, handle)
+    else:
+        with _ws_lock:
+            _check(_lib.ls_recurrence_workspace_bytes(sequences, rows, channels, 0 if packed is None else 1, code, _size_ref),
+                   "ls_recurrence_workspace_bytes")
+            need = _size_out.value
+            if need == 0:
+                st = fn(*args, None, 0, handle)
+            else:
+                stream = torch.cuda.current_stream(index)
+                ws = workspace_for(torch.device("cuda", index), stream, need, "recurrence")
+                st = fn(*args, ws.data_ptr(), ws.numel(), handle)
+                if st == LS_OK:
+                    _after_call(ws, stream, name)
+    if st != LS_OK:
+        raise LibscanError(st, name)
+
+
+def gated_recurrence_backward(dout: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, carries: torch.Tensor,
+                              state: torch.Tensor | None = None, dstate_out: torch.Tensor | None = None,
+                              gating: str = "sigmoid", offsets: torch.Tensor | None = None,
+                              dx: torch.Tensor | None = None, dgate: torch.Tensor | None = None,
+                              dstate: torch.Tensor | None = None):
+    """The gradients of gated_recurrence: from those of out and of state_out (None: zeros)
+    those of x, gate and state.  x, gate, state, gating and offsets are the forward call's (the
+    state as it was before it), carries what it wrote.  dx and dgate have x's shape and
+    type, at any strides; of packed rows those behind the last sequence are left as they are.
+
+    Returns (dx, dgate, dstate), written into the tensors given."""
+    lib = _lib or load_library()
+    sequences, rows, channels, packed = _sequences_of(x, offsets)
+    code, kind, index = _element_code(x), _gating(gating), x.get_device()
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return gated_recurrence_backward(dout, x, gate, carries, state, dstate_out, gating, offsets, dx, dgate, dstate)
+    if carries is None:
+        raise ValueError("libscan: the gradients need the carries of the forward call")
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dgate is None:
+        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dstate is None:
+        dstate = torch.empty(sequences, channels, dtype=_F32, device=x.device)
+    args = (*_tokens_apart(_like_rows(dout, "dout", x), x, offsets), *_tokens_apart(_like_rows(x, "x", x), x, offsets),
+            *_tokens_apart(_like_rows(gate, "gate", x), x, offsets),
+            _carries(carries, x, offsets, sequences, rows, channels, index),
+            *_state_rows(state, "state", sequences, channels, index),
+            *_state_rows(dstate_out, "dstate_out", sequences, channels, index),
+            *_tokens_apart(_like_rows(dx, "dx", x), x, offsets), *_tokens_apart(_like_rows(dgate, "dgate", x), x, offsets),
+            *_state_rows(dstate, "dstate", sequences, channels, index), packed, sequences, rows, channels, code, kind)
+    _recurrence_call(lib.gated_recurrence_backward, "gated_recurrence_backward", args, packed, sequences, rows, channels,
+                     code, index)
+    return dx, dgate, dstate
+
+
+def ls_experts_workspace_bytes(pairs: int, num_experts: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().ls_experts_workspace_bytes(pairs, num_experts, ctypes.byref(out)), "ls_experts_workspace_bytes")
+    return out.value
+
+
+def experts_sort(experts: torch.Tensor, num_experts: int, offsets: torch.Tensor | None = None,
+                 order: torch.Tensor | None = None, places: torch.Tensor | None = None):
+    """A stable sort of the pairs of tokens and experts by expert.  experts (int32 or int64,
+    contiguous, tokens x choices) holds each pair's expert; a number outside [0, num_experts)
+    sends its pair nowhere.
+
+    Returns (offsets, order, places), written into the tensors given: expert e has the
+    rows offsets[e] .. offsets[e + 1] - 1 (int64, num_experts + 1); order (int32, one a
+    pair) is the pair of each row, -1 behind the last; places (int32, of experts' shape) the
+    row of each pair, or -1."""
+    lib = _lib or load_library()
+    index, pairs = experts.get_device(), experts.numel()
+    _require_gpu(experts)
+    bits = 64 if experts.dtype is _I64 else 32
+    if experts.dtype is not _I64 and experts.dtype is not _I32:
+        raise TypeError(f"libscan: experts must be int32 or int64, not {experts.dtype}")
+    if not experts.is_contiguous():
+        raise ValueError("libscan: experts must be contiguous")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return experts_sort(experts, num_experts, offsets, order, places)
+    if offsets is None:
+        offsets = torch.empty(max(num_experts, 0) + 1, dtype=_I64, device=experts.device)
+    if order is None:
+        order = torch.empty(pairs, dtype=_I32, device=experts.device)
+    if places is None:
+        places = torch.empty(experts.shape, dtype=_I32, device=experts.device)
+    if not (offsets.dtype is _I64 and order.dtype is _I32 and places.dtype is _I32
+            and index == offsets.get_device() == order.get_device() == places.get_device()
+            and offsets.shape == (num_experts + 1,) and order.shape == (pairs,) and places.shape == experts.shape
+            and offsets.is_contiguous() and order.is_contiguous() and places.is_contiguous()):
+        _vector(offsets, "offsets", _I64, num_experts + 1, index)
+        _vector(order, "order", _I32, pairs, index)
+        _places(places, experts.shape, index)
+    with _ws_lock:
+        need, handle = ls_experts_workspace_bytes(pairs, num_experts), _raw_stream(index)
+        ws = _ws_cache.get((index, handle, "experts"))
+        if ws is None or ws.numel() < need or (handle != 0 and _capture_of(handle) is not None):
+            device = torch.device("cuda", index)
+            ws = workspace_for(device, torch.cuda.current_stream(device), need, "experts")
+        st = lib.experts_sort(experts.data_ptr(), bits, pairs, num_experts, offsets.data_ptr(), order.data_ptr(),
+                              places.data_ptr(), ws.data_ptr(), ws.numel(), handle)
+    if st != LS_OK:
+        raise LibscanError(st, "experts_sort")
+    return offsets, order, places
+
+
+def _places(places, shape, index: int) -> None:
+    _require_gpu(places)
+    if places.dtype is not _I32 or places.dim() < 1 or not places.is_contiguous() or places.get_device() != index \
+            or (shape is not None and places.shape != shape):
+        raise ValueError("libscan: places must be contiguous int32, tokens x choices, on the rows' device")
+
+
+def _pairs_of(places, index: int) -> tuple:
+    """(tokens, choices) of places: a matrix, or a vector for one choice a token."""
+    if not (places.is_cuda and places.dtype is _I32 and places.dim() == 2 and places.is_contiguous()
+            and places.get_device() == index):
+        _places(places, None, index)
+        if places.dim() > 2:
+            raise ValueError("libscan: places must be tokens x choices")
+    return places.shape if places.dim() == 2 else (places.shape[0], 1)
+
+
+def _weights_of(t, name: str, places, index: int) -> tuple:
+    if t is None:
+        return None, 0
+    if t.shape != places.shape or not t.is_contiguous() or t.get_device() != index:
+        _require_gpu(t)
+        raise ValueError(f"libscan: {name} must be contiguous, of places' shape and on its device")
+    return t.data_ptr(), _element_code(t)
+
+
+def _same(t, name: str, dtype, index: int, rows: int | None, channels: int, overlapping: bool) -> tuple:
+    """(rows, row stride) of a matrix of this type, device and number of channels (and rows)."""
+    n, columns, stride = _matrix(t, name, overlapping)
+    if t.dtype is not dtype or t.get_device() != index or columns != channels or (rows is not None and n != rows):
+        raise ValueError(f"libscan: {name} must be {dtype} of {'' if rows is None else rows} x {channels} on cuda:{index}")
+    return n, stride
+
+
+def experts_gather(x: torch.Tensor, places: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Tokens (rows of x) to the rows of their pairs: out[places[t, j]] = x[t].  places is
+    experts_sort's; places outside out take part in nothing, and rows of out that no place
+    names are left as they are (without `out`: one row a pair, the unnamed ones undefined).
+    Its gradient is experts_combine without weights."""
+    lib = _lib or load_library()
+    tokens, channels, stride = _matrix(x, "x", True)
+    index, code = x.get_device(), _element_code(x)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return experts_gather(x, places, out)
+    n, top = _pairs_of(places, index)
+    if n != tokens:
+        raise ValueError(f"libscan: places has {n} tokens, x {tokens}")
+    if out is None:
+        out = torch.empty(tokens * top, channels, dtype=x.dtype, device=x.device)
+    num_rows, out_stride = _same(out, "out", x.dtype, index, None, channels, False)
+    st = lib.experts_gather(x.data_ptr(), stride, places.data_ptr(), out.data_ptr(), out_stride, tokens, top, num_rows,
+                            channels, code, _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, "experts_gather")
+    return out
+
+
+def experts_combine(rows: torch.Tensor, places: torch.Tensor, weights: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The rows of each token's pairs, weighted and added up in float32:
+    out[t] = sum over j of weights[t, j] * rows[places[t, j]].  places is experts_sort's; a
+    place outside rows takes part in nothing.  weights (float32, float16 or bfloat16; None:
+    ones) has places' shape.  Without weights this is the gradient of experts_gather."""
+    lib = _lib or load_library()
+    num_rows, channels, stride = _matrix(rows, "rows", True)
+    index, code = rows.get_device(), _element_code(rows)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return experts_combine(rows, places, weights, out)
+    tokens, top = _pairs_of(places, index)
+    weights_at, weight_code = _weights_of(weights, "weights", places, index)
+    if out is None:
+        out = torch.empty(tokens, channels, dtype=rows.dtype, device=rows.device)
+    _, out_stride = _same(out, "out", rows.dtype, index, tokens, channels, False)
+    st = lib.experts_combine(rows.data_ptr(), stride, places.data_ptr(), weights_at, weight_code, out.data_ptr(), out_stride,
+                             tokens, top, num_rows, channels, code, _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, "experts_combine")
+    return out
+
+
+def experts_combine_backward(dout: torch.Tensor, rows: torch.Tensor, places: torch.Tensor, weights: torch.Tensor,
+                             drows: torch.Tensor | None = None, dweights: torch.Tensor | None = None):
+    """The gradients of experts_combine with weights: drows[places[t, j]] = weights[t, j] *
+    dout[t], and dweights[t, j] = the product of dout[t] and rows[places[t, j]] over the channels (0
+    for a place outside rows).  Rows of drows that no place names are left as they are
+    (without `drows`: undefined).  Returns (drows, dweights), of rows' and weights' types."""
+    lib = _lib or load_library()
+    tokens, channels, stride = _matrix(dout, "dout", True)
+    index, code = dout.get_device(), _element_code(dout)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return experts_combine_backward(dout, rows, places, weights, drows, dweights)
+    n, top = _pairs_of(places, index)
+    if n != tokens:
+        raise ValueError(f"libscan: places has {n} tokens, dout {tokens}")
+    if weights is None:
+        raise ValueError("libscan: without weights the gradient of experts_combine is experts_gather")
+    num_rows, rows_stride = _same(rows, "rows", dout.dtype, index, None, channels, True)
+    weights_at, weight_code = _weights_of(weights, "weights", places, index)
+    if drows is None:
+        drows = torch.empty(num_rows, channels, dtype=rows.dtype, device=rows.device)
+    _, drows_stride = _same(drows, "drows", dout.dtype, index, num_rows, channels, False)
+    if dweights is None:
+        dweights = torch.empty_like(weights)
+    dweights_at, dweight_code = _weights_of(dweights, "dweights", places, index)
+    if dweight_code != weight_code:
+        raise TypeError("libscan: dweights must have the type of weights")
+    st = lib.experts_combine_backward(dout.data_ptr(), stride, rows.data_ptr(), rows_stride, places.data_ptr(), weights_at,
+                                      weight_code, drows.data_ptr(), drows_stride, dweights_at, tokens, top, num_rows,
+                                      channels, code, _raw_stream(index))
+    if st != LS_OK:
+        raise LibscanError(st, "experts_combine_backward")
+    return drows, dweights

@@ -223,6 +223,107 @@ bool matrix_ok(int64_t rows, int64_t columns, int64_t stride, bool broadcast)
 
 bool page_size_ok(int64_t page_size) { return page_size >= 1 && page_size <= INT32_MAX; }
 
+bool element_ok(ls_logits t) { return t == LS_LOGITS_FLOAT32 || t == LS_LOGITS_FLOAT16 || t == LS_LOGITS_BFLOAT16; }
+size_t element_size(ls_logits t) { return t == LS_LOGITS_FLOAT32 ? 4 : 2; }
+bool channels_ok(int64_t n) { return n >= 0 && n <= LS_MAX_CHANNELS; }
+
+// Rows of `width` bytes in two dimensions: row (s, r) at byte s * outer + r * inner.
+struct Rows {
+    const void* p;
+    int64_t outers, outer, inners, inner, width;  // bytes
+    size_t align;
+    bool written;
+    bool none() const { return outers == 0 || inners == 0 || width == 0; }
+    int64_t span() const { return none() ? 0 : (outers - 1) * outer + (inners - 1) * inner + width; }
+    // The distance that both strides are multiples of and no row is longer than, or 0.
+    int64_t pitch() const
+    {
+        const int64_t o = outers > 1 ? outer : 0, i = inners > 1 ? inner : 0;
+        const int64_t unit = o == 0 ? i : i == 0 ? o : (o < i ? o : i);
+        return unit > 0 && o % unit == 0 && i % unit == 0 && unit >= width ? unit : 0;
+    }
+};
+
+// Strides in range, and where written, no row on another.
+bool rows_ok(const Rows& r)
+{
+    if (r.outer < 0 || r.inner < 0)
+        return false;
+    if (r.none())
+        return true;
+    if (r.p == nullptr || !aligned(r.p, r.align))
+        return false;
+    const int64_t most = INT64_MAX / 16;
+    if ((r.outers > 1 && r.outer > most / (r.outers - 1)) || (r.inners > 1 && r.inner > most / (r.inners - 1)))
+        return false;
+    if (!r.written)
+        return true;
+    const bool by_outer = (r.inners == 1 || r.inner >= r.width) &&
+                          (r.outers == 1 || r.outer >= (r.inners - 1) * r.inner + r.width);
+    const bool by_inner = (r.outers == 1 || r.outer >= r.width) &&
+                          (r.inners == 1 || r.inner >= (r.outers - 1) * r.outer + r.width);
+    return by_outer || by_inner;
+}
+
+// Whether two may share bytes: their spans meet, and they are not columns of one matrix beside each other.
+bool rows_meet(const Rows& a, const Rows& b)
+{
+    if (!overlaps(a.p, size_t(a.span()), b.p, size_t(b.span())))
+        return false;
+    int64_t pitch = a.pitch();
+    if (a.span() == a.width)  // one row fits any pitch
+        pitch = b.pitch();
+    if (pitch <= 0 || (b.span() != b.width && b.pitch() != pitch))
+        return true;
+    const int64_t apart = int64_t(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+    const int64_t d = (apart % pitch + pitch) % pitch;
+    return d < a.width || d + b.width > pitch;
+}
+
+template <int N>
+bool all_rows_ok(const Rows (&r)[N])
+{
+    for (int i = 0; i < N; ++i) {
+        if (!rows_ok(r[i]))
+            return false;
+        for (int j = 0; j < i; ++j)
+            if ((r[i].written || r[j].written) && rows_meet(r[i], r[j]))
+                return false;
+    }
+    return true;
+}
+
+Rows flat(const void* p, size_t bytes, size_t align, bool written)
+{
+    return {p, 1, 0, bytes > 0 ? 1 : 0, 0, int64_t(bytes), align, written};
+}
+Rows matrix(const void* p, int64_t rows, int64_t stride, int64_t columns, size_t size, bool written)
+{
+    return {p, 1, 0, rows, stride, columns * int64_t(size), size, written};
+}
+
+// Strides that can be turned into bytes.
+template <int N>
+bool strides_ok(const int64_t (&s)[N])
+{
+    for (int64_t v : s)
+        if (v < 0 || v > INT64_MAX / 64)
+            return false;
+    return true;
+}
+
+bool recurrence_sizes_ok(int64_t sequences, int64_t rows, int64_t channels)
+{
+    return count_ok(sequences) && count_ok(rows) && channels_ok(channels);
+}
+bool gating_ok(ls_gating g) { return g >= LS_GATE_DECAY && g <= LS_GATE_SIGMOID; }
+
+bool experts_sizes_ok(int64_t tokens, int64_t top, int64_t num_rows, int64_t channels)
+{
+    return count_ok(tokens) && count_ok(top) && count_ok(num_rows) && channels_ok(channels) &&
+           (top == 0 || tokens <= INT32_MAX / top);
+}
+
 }  // namespace
 
 extern "C" {
@@ -553,6 +654,236 @@ ls_status pages_release(const int32_t* lens, const uint8_t* finished, int64_t re
     return from_hip(ls::launch_pages_release(lens, finished, requests, tables, columns, table_stride, free_pages,
                                              free_capacity, free_count, page_size, count_out,
                                              reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status ls_recurrence_carry_rows(int64_t sequences, int64_t rows, int packed, int64_t* carry_rows)
+{
+    if (carry_rows == nullptr || !recurrence_sizes_ok(sequences, rows, 0))
+        return LS_ERR_INVALID_ARG;
+    *carry_rows = ls::recur_carry_rows(sequences, rows, packed != 0);
+    return LS_OK;
+}
+
+ls_status ls_recurrence_workspace_bytes(int64_t sequences, int64_t rows, int64_t channels, int packed, ls_logits t,
+                                        size_t* bytes)
+{
+    if (bytes == nullptr || !recurrence_sizes_ok(sequences, rows, channels) || !element_ok(t))
+        return LS_ERR_INVALID_ARG;
+    *bytes = ls::recur_workspace_bytes(sequences, rows, channels, packed != 0, int(t));
+    return LS_OK;
+}
+
+ls_status gated_recurrence(const void* x, int64_t x_sequence_stride, int64_t x_row_stride, const void* gate,
+                           int64_t gate_sequence_stride, int64_t gate_row_stride, void* out,
+                           int64_t out_sequence_stride, int64_t out_row_stride, const float* state,
+                           int64_t state_stride, float* state_out, int64_t state_out_stride, float* carries,
+                           const int64_t* offsets, int64_t sequences, int64_t rows, int64_t channels, ls_logits t,
+                           ls_gating gating, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!recurrence_sizes_ok(sequences, rows, channels) || !element_ok(t) || !gating_ok(gating))
+        return LS_ERR_INVALID_ARG;
+    const int64_t strides[] = {x_sequence_stride, x_row_stride, gate_sequence_stride, gate_row_stride, out_sequence_stride,
+                               out_row_stride, state_stride, state_out_stride};
+    if (!strides_ok(strides))
+        return LS_ERR_INVALID_ARG;
+    const bool packed = offsets != nullptr;
+    const int64_t z = int64_t(element_size(t)), width = channels * z, chains = packed ? 1 : sequences;
+    const bool same = state == state_out && state_stride == state_out_stride;
+    const size_t need = ls::recur_workspace_bytes(sequences, rows, channels, packed, int(t));
+    const Rows all[] = {
+        {x, chains, x_sequence_stride * z, rows, x_row_stride * z, width, size_t(z), false},
+        {gate, chains, gate_sequence_stride * z, rows, gate_row_stride * z, width, size_t(z), false},
+        {out, chains, out_sequence_stride * z, rows, out_row_stride * z, width, size_t(z), true},
+        matrix(state, state != nullptr && !same ? sequences : 0, state_stride * 4, channels, 4, false),
+        matrix(state_out, sequences, state_out_stride * 4, channels, 4, true),
+        flat(carries, carries != nullptr ? size_t(ls::recur_carry_rows(sequences, rows, packed)) * size_t(channels) * 4 : 0, 4, true),
+        flat(offsets, packed ? size_t(sequences + 1) * 8 : 0, 8, false),
+        flat(ws, ws != nullptr && ws_bytes >= need ? need : 0, 16, true),
+    };
+    if (!all_rows_ok(all))
+        return LS_ERR_INVALID_ARG;
+    if (need > 0) {
+        const ls_status st = check_ws(ws, ws_bytes, need);
+        if (st != LS_OK)
+            return st;
+    }
+    const ls::RecurForward call = {x, gate, out, x_sequence_stride, x_row_stride, gate_sequence_stride, gate_row_stride,
+                                   out_sequence_stride, out_row_stride, state, state_out, state_stride, state_out_stride,
+                                   carries, offsets, sequences, rows, channels, int(gating)};
+    return from_hip(ls::launch_recurrence(call, int(t), ws, reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status gated_recurrence_backward(const void* dout, int64_t dout_sequence_stride, int64_t dout_row_stride,
+                                    const void* x, int64_t x_sequence_stride, int64_t x_row_stride, const void* gate,
+                                    int64_t gate_sequence_stride, int64_t gate_row_stride, const float* carries,
+                                    const float* state, int64_t state_stride, const float* dstate_out,
+                                    int64_t dstate_out_stride, void* dx, int64_t dx_sequence_stride,
+                                    int64_t dx_row_stride, void* dgate, int64_t dgate_sequence_stride,
+                                    int64_t dgate_row_stride, float* dstate, int64_t dstate_stride,
+                                    const int64_t* offsets, int64_t sequences, int64_t rows, int64_t channels,
+                                    ls_logits t, ls_gating gating, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!recurrence_sizes_ok(sequences, rows, channels) || !element_ok(t) || !gating_ok(gating))
+        return LS_ERR_INVALID_ARG;
+    const int64_t strides[] = {dout_sequence_stride, dout_row_stride, x_sequence_stride, x_row_stride, gate_sequence_stride,
+                               gate_row_stride, state_stride, dstate_out_stride, dx_sequence_stride, dx_row_stride,
+                               dgate_sequence_stride, dgate_row_stride, dstate_stride};
+    if (!strides_ok(strides))
+        return LS_ERR_INVALID_ARG;
+    const bool packed = offsets != nullptr;
+    const int64_t z = int64_t(element_size(t)), width = channels * z, chains = packed ? 1 : sequences;
+    const size_t need = ls::recur_workspace_bytes(sequences, rows, channels, packed, int(t));
+    const Rows all[] = {
+        {dout, chains, dout_sequence_stride * z, rows, dout_row_stride * z, width, size_t(z), false},
+        {x, chains, x_sequence_stride * z, rows, x_row_stride * z, width, size_t(z), false},
+        {gate, chains, gate_sequence_stride * z, rows, gate_row_stride * z, width, size_t(z), false},
+        flat(carries, size_t(ls::recur_carry_rows(sequences, rows, packed)) * size_t(channels) * 4, 4, false),
+        matrix(state, state != nullptr ? sequences : 0, state_stride * 4, channels, 4, false),
+        matrix(dstate_out, dstate_out != nullptr ? sequences : 0, dstate_out_stride * 4, channels, 4, false),
+        {dx, chains, dx_sequence_stride * z, rows, dx_row_stride * z, width, size_t(z), true},
+        {dgate, chains, dgate_sequence_stride * z, rows, dgate_row_stride * z, width, size_t(z), true},
+        matrix(dstate, sequences, dstate_stride * 4, channels, 4, true),
+        flat(offsets, packed ? size_t(sequences + 1) * 8 : 0, 8, false),
+        flat(ws, ws != nullptr && ws_bytes >= need ? need : 0, 16, true),
+    };
+    if (!all_rows_ok(all))
+        return LS_ERR_INVALID_ARG;
+    if (need > 0) {
+        const ls_status st = check_ws(ws, ws_bytes, need);
+        if (st != LS_OK)
+            return st;
+    }
+    const ls::RecurBackward call = {dout, x, gate, dx, dgate, dout_sequence_stride, dout_row_stride, x_sequence_stride,
+                                    x_row_stride, gate_sequence_stride, gate_row_stride, dx_sequence_stride, dx_row_stride,
+                                    dgate_sequence_stride, dgate_row_stride, state, dstate_out, dstate, state_stride,
+                                    dstate_out_stride, dstate_stride, carries, offsets, sequences, rows, channels, int(gating)};
+    return from_hip(ls::launch_recurrence_backward(call, int(t), ws, reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status ls_experts_workspace_bytes(int64_t pairs, int64_t num_experts, size_t* bytes)
+{
+    if (bytes == nullptr || !count_ok(pairs) || num_experts < 1 || num_experts > LS_MAX_EXPERTS)
+        return LS_ERR_INVALID_ARG;
+    *bytes = ls::experts_workspace_bytes(pairs, num_experts);
+    return LS_OK;
+}
+
+ls_status experts_sort(const void* experts, int id_bits, int64_t pairs, int64_t num_experts, int64_t* offsets,
+                       int32_t* order, int32_t* places, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!count_ok(pairs) || num_experts < 1 || num_experts > LS_MAX_EXPERTS || (id_bits != 32 && id_bits != 64))
+        return LS_ERR_INVALID_ARG;
+    const size_t need = ls::experts_workspace_bytes(pairs, num_experts), id = size_t(id_bits / 8), n = size_t(pairs) * 4;
+    const Buffer buffers[] = {
+        {experts, size_t(pairs) * id, id, false},
+        {offsets, size_t(num_experts + 1) * 8, 8, true},
+        {order, n, 4, true},
+        {places, n, 4, true},
+        {ws, ws != nullptr && ws_bytes >= need ? need : 0, 16, true},
+    };
+    if (!buffers_ok(buffers))
+        return LS_ERR_INVALID_ARG;
+    const ls_status st = check_ws(ws, ws_bytes, need);
+    if (st != LS_OK)
+        return st;
+    return from_hip(ls::launch_experts_sort(experts, id_bits, pairs, num_experts, offsets, order, places, ws,
+                                            reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status experts_gather(const void* x, int64_t x_stride, const int32_t* places, void* rows, int64_t rows_stride,
+                         int64_t tokens, int64_t top, int64_t num_rows, int64_t channels, ls_logits t, void* stream)
+{
+    const int64_t strides[] = {x_stride, rows_stride};
+    if (!experts_sizes_ok(tokens, top, num_rows, channels) || !element_ok(t) || !strides_ok(strides))
+        return LS_ERR_INVALID_ARG;
+    const size_t z = element_size(t);
+    const Rows all[] = {
+        matrix(x, tokens, x_stride * int64_t(z), channels, z, false),
+        flat(places, size_t(tokens * top) * 4, 4, false),
+        matrix(rows, num_rows, rows_stride * int64_t(z), channels, z, true),
+    };
+    if (!all_rows_ok(all))
+        return LS_ERR_INVALID_ARG;
+    ls::ExpertsRows call = {};
+    call.x = x;
+    call.x_row = x_stride;
+    call.rows_out = rows;
+    call.rows_out_row = rows_stride;
+    call.places = places;
+    call.tokens = tokens;
+    call.rows_count = num_rows;
+    call.channels = channels;
+    call.top = int(top);
+    return from_hip(ls::launch_experts_rows(call, ls::EXPERTS_GATHER, int(t), reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status experts_combine(const void* rows, int64_t rows_stride, const int32_t* places, const void* weights,
+                          ls_logits weight_type, void* out, int64_t out_stride, int64_t tokens, int64_t top,
+                          int64_t num_rows, int64_t channels, ls_logits t, void* stream)
+{
+    const int64_t strides[] = {rows_stride, out_stride};
+    if (!experts_sizes_ok(tokens, top, num_rows, channels) || !element_ok(t) || !element_ok(weight_type) || !strides_ok(strides))
+        return LS_ERR_INVALID_ARG;
+    const size_t z = element_size(t), pairs = size_t(tokens * top), wz = element_size(weight_type);
+    const Rows all[] = {
+        matrix(rows, num_rows, rows_stride * int64_t(z), channels, z, false),
+        flat(places, pairs * 4, 4, false),
+        flat(weights, weights != nullptr ? pairs * wz : 0, wz, false),
+        matrix(out, tokens, out_stride * int64_t(z), channels, z, true),
+    };
+    if (!all_rows_ok(all))
+        return LS_ERR_INVALID_ARG;
+    ls::ExpertsRows call = {};
+    call.rows = rows;
+    call.rows_row = rows_stride;
+    call.out = out;
+    call.out_row = out_stride;
+    call.places = places;
+    call.weights = weights;
+    call.weight_type = int(weight_type);
+    call.tokens = tokens;
+    call.rows_count = num_rows;
+    call.channels = channels;
+    call.top = int(top);
+    return from_hip(ls::launch_experts_rows(call, ls::EXPERTS_COMBINE, int(t), reinterpret_cast<hipStream_t>(stream)));
+}
+
+ls_status experts_combine_backward(const void* dout, int64_t dout_stride, const void* rows, int64_t rows_stride,
+                                   const int32_t* places, const void* weights, ls_logits weight_type, void* drows,
+                                   int64_t drows_stride, void* dweights, int64_t tokens, int64_t top, int64_t num_rows,
+                                   int64_t channels, ls_logits t, void* stream)
+{
+    const int64_t strides[] = {dout_stride, rows_stride, drows_stride};
+    if (!experts_sizes_ok(tokens, top, num_rows, channels) || !element_ok(t) || !element_ok(weight_type) || !strides_ok(strides))
+        return LS_ERR_INVALID_ARG;
+    const size_t z = element_size(t), pairs = size_t(tokens * top), wz = element_size(weight_type);
+    const Rows all[] = {
+        matrix(dout, tokens, dout_stride * int64_t(z), channels, z, false),
+        matrix(rows, num_rows, rows_stride * int64_t(z), channels, z, false),
+        flat(places, pairs * 4, 4, false),
+        flat(weights, pairs * wz, wz, false),
+        matrix(drows, num_rows, drows_stride * int64_t(z), channels, z, true),
+        flat(dweights, pairs * wz, wz, true),
+    };
+    if (!all_rows_ok(all))
+        return LS_ERR_INVALID_ARG;
+    ls::ExpertsRows call = {};
+    call.x = dout;
+    call.x_row = dout_stride;
+    call.rows = rows;
+    call.rows_row = rows_stride;
+    call.rows_out = drows;
+    call.rows_out_row = drows_stride;
+    call.places = places;
+    call.weights = weights;
+    call.weight_type = int(weight_type);
+    call.dweights = dweights;
+    call.tokens = tokens;
+    call.rows_count = num_rows;
+    call.channels = channels;
+    call.top = int(top);
+    return from_hip(
+        ls::launch_experts_rows(call, ls::EXPERTS_COMBINE_BACKWARD, int(t), reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,386 @@
+// ls_experts.hip -- tokens to the rows of their experts and back (gfx950).
+//
+// A token t goes to `top` experts; pair p = t * top + j.  The sort is a stable counting sort of
+// the pairs by expert: a histogram per tile of pairs, prefix sums over (expert, tile), and a
+// rank among the pairs of the same expert in the tile, found 64 pairs at a time by comparing
+// expert numbers bit by bit across the wave (one ballot a bit).  The moves of rows read each
+// token's places once and go over its channels 16 bytes a lane: the gather reads a token's row
+// once and writes it to all its places, the combination reads all its places and writes one
+// row, its gradient reads both and writes both.  A place that is not a row (a pair over its
+// expert's capacity) takes part in nothing.
+#include "ls_elements.hpp"
+#include "ls_internal.hpp"
+
+namespace ls {
+
+// ---------------------------------------------------------------- sort
+
+constexpr int EX_BLOCK = 512;
+constexpr int EX_WAVES = EX_BLOCK / 64;
+constexpr int EX_STEPS = 8;                              // pairs per lane and turn
+constexpr int EX_TURN = EX_BLOCK * EX_STEPS;             // pairs per block and turn
+constexpr int EX_TILES = 128;                            // most tiles
+
+struct ExpertsTiles {
+    int64_t n, per_tile;  // pairs; pairs per tile, a multiple of EX_TURN
+    int tiles;
+};
+static ExpertsTiles experts_tiles(int64_t n)
+{
+    const int64_t turns = n > 0 ? (n + EX_TURN - 1) / EX_TURN : 1, per = (turns + EX_TILES - 1) / EX_TILES;
+    return {n, per * EX_TURN, int((turns + per - 1) / per)};
+}
+
+// The expert of a pair, or `experts` for one that goes nowhere.
+template <class I>
+__device__ __forceinline__ uint32_t expert_of(const I* ids, int64_t p, int64_t n, int experts)
+{
+    if (p >= n)
+        return uint32_t(experts);
+    const int64_t e = ids[p];
+    return e >= 0 && e < experts ? uint32_t(e) : uint32_t(experts);
+}
+
+template <class I>
+__global__ __launch_bounds__(EX_BLOCK) void experts_count_kernel(const I* ids, ExpertsTiles t, int experts, uint32_t* counts)
+{
+    extern __shared__ uint32_t count[];  // one per expert, and one for pairs without
+    for (int e = threadIdx.x; e <= experts; e += EX_BLOCK)
+        count[e] = 0;
+    __syncthreads();
+    const int64_t from = blockIdx.x * t.per_tile, to = from + t.per_tile < t.n ? from + t.per_tile : t.n;
+    for (int64_t p = from + threadIdx.x; p < to; p += EX_BLOCK)
+        atomicAdd(&count[expert_of(ids, p, t.n, experts)], 1u);
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += EX_BLOCK)
+        counts[int64_t(blockIdx.x) * experts + e] = count[e];
+}
+
+// With one tile the counts are made here (counts == NULL).
+template <class I>
+__global__ __launch_bounds__(EX_BLOCK) void experts_place_kernel(const I* ids, ExpertsTiles t, int experts, int bits,
+                                                                 const uint32_t* counts, int64_t* offsets, int32_t* order,
+                                                                 int32_t* places)
+{
+    extern __shared__ uint32_t shared[];
+    uint32_t* base = shared;                       // [experts + 1]: the next row of each expert
+    uint32_t* seen = shared + experts + 1;         // [waves][experts + 1]
+    __shared__ uint32_t wave_total[EX_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t from = blockIdx.x * t.per_tile, to = from + t.per_tile < t.n ? from + t.per_tile : t.n;
+    if (counts == nullptr) {
+        for (int e = tid; e <= experts; e += EX_BLOCK)
+            seen[e] = 0;
+        __syncthreads();
+        for (int64_t p = from + tid; p < to; p += EX_BLOCK)
+            atomicAdd(&seen[expert_of(ids, p, t.n, experts)], 1u);
+        __syncthreads();
+    }
+    // prefix sums over the experts, EX_BLOCK of them at a time
+    uint32_t carry = 0;
+    for (int e0 = 0; e0 < experts; e0 += EX_BLOCK) {
+        const int e = e0 + tid;
+        uint32_t total = 0, before = 0;
+        if (e < experts) {
+            if (counts == nullptr) {
+                total = seen[e];
+            } else {
+                for (int i = 0; i < t.tiles; ++i) {
+                    const uint32_t c = counts[int64_t(i) * experts + e];
+                    total += c;
+                    before += i < int(blockIdx.x) ? c : 0;
+                }
+            }
+        }
+        const uint32_t incl = wave_inclusive_scan<SumU32>(total);
+        if (lane == 63)
+            wave_total[wave] = incl;
+        __syncthreads();
+        uint32_t first = carry;
+        for (int w = 0; w < EX_WAVES; ++w) {
+            first += w < wave ? wave_total[w] : 0;
+            carry += wave_total[w];
+        }
+        if (e < experts) {
+            base[e] = first + incl - total + before;
+            if (blockIdx.x == 0)
+                offsets[e] = first + incl - total;
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0 && tid == 0)
+        offsets[experts] = carry;
+    for (int64_t turn = from; turn < to; turn += EX_TURN) {
+        for (int e = tid; e < EX_WAVES * (experts + 1); e += EX_BLOCK)
+            seen[e] = 0;
+        __syncthreads();
+        // volatile: a lane reads what other lanes of its wave wrote a step before
+        volatile uint32_t* mine = seen + wave * (experts + 1);
+        uint32_t ex[EX_STEPS], rank[EX_STEPS];
+        const int64_t p0 = turn + wave * (64 * EX_STEPS) + lane;
+#pragma unroll
+        for (int i = 0; i < EX_STEPS; ++i)
+            ex[i] = expert_of(ids, p0 + i * 64, t.n, experts);
+#pragma unroll
+        for (int i = 0; i < EX_STEPS; ++i) {
+            uint64_t peers = ~0ull;
+            for (int b = 0; b < bits; ++b) {
+                const bool on = (ex[i] >> b) & 1;
+                const uint64_t m = __ballot(on);
+                peers &= on ? m : ~m;
+            }
+            const uint32_t old = mine[ex[i]];
+            const uint32_t lower = __builtin_popcountll(peers & ((1ull << lane) - 1));
+            rank[i] = old + lower;
+            if (lower == 0)
+                mine[ex[i]] = old + uint32_t(__builtin_popcountll(peers));
+        }
+        __syncthreads();
+        // where each wave's pairs of an expert begin
+        for (int e = tid; e < experts; e += EX_BLOCK) {
+            uint32_t next = base[e];
+            for (int w = 0; w < EX_WAVES; ++w) {
+                const uint32_t c = seen[w * (experts + 1) + e];
+                seen[w * (experts + 1) + e] = next;
+                next += c;
+            }
+            base[e] = next;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < EX_STEPS; ++i) {
+            const int64_t p = p0 + i * 64;
+            if (p < to) {
+                const bool routed = ex[i] < uint32_t(experts);
+                const uint32_t row = mine[ex[i]] + rank[i];
+                places[p] = routed ? int32_t(row) : -1;
+                if (routed)
+                    order[row] = int32_t(p);
+            }
+        }
+        __syncthreads();
+    }
+    for (int64_t i = from + tid; i < to; i += EX_BLOCK)
+        if (i >= carry)
+            order[i] = -1;
+}
+
+size_t experts_workspace_bytes(int64_t pairs, int64_t experts)
+{
+    const ExpertsTiles t = experts_tiles(pairs);
+    return 256 + (t.tiles > 1 ? size_t(t.tiles) * size_t(experts) * 4 : 0);
+}
+
+template <class I>
+static hipError_t experts_sort_of(const I* ids, int64_t pairs, int experts, int64_t* offsets, int32_t* order, int32_t* places,
+                                  void* ws, hipStream_t stream)
+{
+    const ExpertsTiles t = experts_tiles(pairs);
+    uint32_t* counts = t.tiles > 1 ? reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + 256) : nullptr;
+    int bits = 1;
+    while ((1 << bits) <= experts)  // `experts` itself is a value too
+        ++bits;
+    const size_t row = size_t(experts + 1) * 4;
+    if (counts != nullptr)
+        experts_count_kernel<I><<<dim3(t.tiles), dim3(EX_BLOCK), row, stream>>>(ids, t, experts, counts);
+    experts_place_kernel<I><<<dim3(t.tiles), dim3(EX_BLOCK), row * (1 + EX_WAVES), stream>>>(
+        ids, t, experts, bits, counts, offsets, order, places);
+    return hipGetLastError();
+}
+
+hipError_t launch_experts_sort(const void* ids, int id_bits, int64_t pairs, int64_t experts, int64_t* offsets, int32_t* order,
+                               int32_t* places, void* ws, hipStream_t stream)
+{
+    if (id_bits == 32)
+        return experts_sort_of(static_cast<const int32_t*>(ids), pairs, int(experts), offsets, order, places, ws, stream);
+    return experts_sort_of(static_cast<const int64_t*>(ids), pairs, int(experts), offsets, order, places, ws, stream);
+}
+
+// ---------------------------------------------------------------- rows
+
+// A block is `x` lanes over a row's parts of VEC channels by `y` tokens.  A launch holds less than 2^32
+// threads along x, so a block may take several tokens.
+constexpr int64_t EX_GRID = 1 << 20;
+struct RowGrid {
+    dim3 grid, block;
+};
+static RowGrid row_grid(int64_t tokens, int64_t parts, int most)
+{
+    int x = 8;
+    while (x < most && x < parts)
+        x *= 2;
+    const int y = 256 / x;
+    const int64_t blocks = (tokens + y - 1) / y;
+    return {dim3(uint32_t(blocks < EX_GRID ? blocks : EX_GRID), uint32_t((parts + x - 1) / x)), dim3(x, y)};
+}
+
+__device__ __forceinline__ float weight_at(const void* weights, int type, int64_t p)
+{
+    if (weights == nullptr)
+        return 1.0f;
+    if (type == LOGITS_F32)
+        return static_cast<const float*>(weights)[p];
+    float v[1];
+    const uint32_t w = static_cast<const uint16_t*>(weights)[p];
+    if (type == LOGITS_F16)
+        F16::unpack(w, v);
+    else
+        BF16::unpack(w, v);
+    return v[0];
+}
+
+template <class E, int VEC>
+__global__ __launch_bounds__(256) void experts_gather_kernel(ExpertsRows q)
+{
+    const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * VEC;
+    if (c >= q.channels)
+        return;
+    for (int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y; t < q.tokens; t += int64_t(gridDim.x) * blockDim.y) {
+        Elements<E, VEC> v;
+        v.load(static_cast<const char*>(q.x) + (t * q.x_row + c) * E::size);
+        for (int j = 0; j < q.top; ++j) {
+            const int64_t at = q.places[t * q.top + j];
+            if (at >= 0 && at < q.rows_count)
+                v.store(static_cast<char*>(q.rows_out) + (at * q.rows_out_row + c) * E::size);
+        }
+    }
+}
+
+constexpr int EX_FLIGHT = 8;  // rows on their way at once
+
+template <class E, int VEC>
+__global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsRows q)
+{
+    const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * VEC;
+    if (c >= q.channels)
+        return;
+    for (int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y; t < q.tokens; t += int64_t(gridDim.x) * blockDim.y) {
+        float sum[VEC] = {};
+        for (int j0 = 0; j0 < q.top; j0 += EX_FLIGHT) {
+            Elements<E, VEC> v[EX_FLIGHT];
+            float w[EX_FLIGHT];
+            bool there[EX_FLIGHT];
+    #pragma unroll
+            for (int i = 0; i < EX_FLIGHT; ++i) {
+                const int64_t p = t * q.top + j0 + i;
+                const int64_t at = j0 + i < q.top ? q.places[p] : -1;
+                there[i] = at >= 0 && at < q.rows_count;
+                if (there[i]) {
+                    w[i] = weight_at(q.weights, q.weight_type, p);
+                    v[i].load(static_cast<const char*>(q.rows) + (at * q.rows_row + c) * E::size);
+                }
+            }
+    #pragma unroll
+            for (int i = 0; i < EX_FLIGHT; ++i)
+                if (there[i]) {
+                    float f[VEC];
+                    v[i].get(f);
+    #pragma unroll
+                    for (int k = 0; k < VEC; ++k)
+                        sum[k] = __builtin_fmaf(w[i], f[k], sum[k]);
+                }
+        }
+        Elements<E, VEC> o;
+        o.set(sum);
+        o.store(static_cast<char*>(q.out) + (t * q.out_row + c) * E::size);
+    }
+}
+
+// One wave a token.
+template <class E, int VEC>
+__global__ __launch_bounds__(256) void experts_combine_backward_kernel(ExpertsRows q)
+{
+    const int lane = threadIdx.x & 63;
+    for (int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); t < q.tokens; t += int64_t(gridDim.x) * 4) {
+        for (int j0 = 0; j0 < q.top; j0 += EX_FLIGHT) {
+            float dot[EX_FLIGHT] = {}, w[EX_FLIGHT];
+            int64_t at[EX_FLIGHT];
+    #pragma unroll
+            for (int i = 0; i < EX_FLIGHT; ++i) {
+                const int64_t p = t * q.top + j0 + i;
+                at[i] = j0 + i < q.top ? q.places[p] : -1;
+                if (at[i] >= q.rows_count)
+                    at[i] = -1;
+                w[i] = at[i] >= 0 ? weight_at(q.weights, q.weight_type, p) : 0.0f;
+            }
+            for (int64_t c = lane * VEC; c < q.channels; c += 64 * VEC) {
+                Elements<E, VEC> d, v[EX_FLIGHT];
+                d.load(static_cast<const char*>(q.x) + (t * q.x_row + c) * E::size);
+    #pragma unroll
+                for (int i = 0; i < EX_FLIGHT; ++i)
+                    if (at[i] >= 0)
+                        v[i].load(static_cast<const char*>(q.rows) + (at[i] * q.rows_row + c) * E::size);
+                float df[VEC];
+                d.get(df);
+    #pragma unroll
+                for (int i = 0; i < EX_FLIGHT; ++i)
+                    if (at[i] >= 0) {
+                        float f[VEC], g[VEC];
+                        v[i].get(f);
+    #pragma unroll
+                        for (int k = 0; k < VEC; ++k) {
+                            dot[i] = __builtin_fmaf(f[k], df[k], dot[i]);
+                            g[k] = w[i] * df[k];
+                        }
+                        v[i].set(g);
+                        v[i].store(static_cast<char*>(q.rows_out) + (at[i] * q.rows_out_row + c) * E::size);
+                    }
+            }
+    #pragma unroll
+            for (int i = 0; i < EX_FLIGHT; ++i)
+                if (j0 + i < q.top) {
+                    const float sum = wave_inclusive_scan<SumF32>(dot[i]);
+                    if (lane == 63) {
+                        const int64_t p = t * q.top + j0 + i;
+                        const float r = at[i] >= 0 ? sum : 0.0f;
+                        if (q.weight_type == LOGITS_F32)
+                            static_cast<float*>(q.dweights)[p] = r;
+                        else
+                            static_cast<uint16_t*>(q.dweights)[p] =
+                                uint16_t(q.weight_type == LOGITS_F16 ? F16::pack<1>({r}) : BF16::pack<1>({r}));
+                    }
+                }
+        }
+    }
+}
+
+// 16 bytes a lane where every row is aligned to that, else an element.
+static bool wide_rows(const ExpertsRows& q, int size)
+{
+    const int64_t vec = 16 / size;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(q.x) | reinterpret_cast<uintptr_t>(q.rows) |
+                        reinterpret_cast<uintptr_t>(q.rows_out) | reinterpret_cast<uintptr_t>(q.out);
+    return q.channels % vec == 0 && p % 16 == 0 && q.x_row % vec == 0 && q.rows_row % vec == 0 && q.out_row % vec == 0 &&
+           q.rows_out_row % vec == 0;
+}
+
+template <class E, int VEC>
+static hipError_t rows_of(const ExpertsRows& q, ExpertsMove move, hipStream_t stream)
+{
+    const int64_t parts = (q.channels + VEC - 1) / VEC;
+    const RowGrid g = row_grid(q.tokens, parts, 256);
+    if (move == EXPERTS_GATHER)
+        experts_gather_kernel<E, VEC><<<g.grid, g.block, 0, stream>>>(q);
+    else if (move == EXPERTS_COMBINE)
+        experts_combine_kernel<E, VEC><<<g.grid, g.block, 0, stream>>>(q);
+    else
+        experts_combine_backward_kernel<E, VEC><<<row_grid(q.tokens, 64, 64).grid, dim3(256), 0, stream>>>(q);
+    return hipGetLastError();
+}
+
+template <class E>
+static hipError_t rows_of_type(const ExpertsRows& q, ExpertsMove move, hipStream_t stream)
+{
+    return wide_rows(q, E::size) ? rows_of<E, 16 / E::size>(q, move, stream) : rows_of<E, 1>(q, move, stream);
+}
+
+hipError_t launch_experts_rows(const ExpertsRows& q, ExpertsMove move, int type, hipStream_t stream)
+{
+    if (q.tokens == 0 || (q.channels == 0 && move != EXPERTS_COMBINE_BACKWARD) || (q.top == 0 && move != EXPERTS_COMBINE))
+        return hipSuccess;
+    if (type == LOGITS_F32)
+        return rows_of_type<F32>(q, move, stream);
+    return type == LOGITS_F16 ? rows_of_type<F16>(q, move, stream) : rows_of_type<BF16>(q, move, stream);
+}
+
+}  // namespace ls

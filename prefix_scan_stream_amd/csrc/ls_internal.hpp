@@ -94,4 +94,54 @@ struct SampleCall {
 size_t sample_workspace_bytes(int64_t rows, int64_t vocab);
 hipError_t launch_sample(const SampleCall& call, int type, void* ws, hipStream_t stream);
 
+// ---- gated linear recurrence (ls_recurrence.hip); element types are LogitType's, strides in elements
+enum Gating : int { GATE_DECAY = 0, GATE_LOG = 1, GATE_SIGMOID = 2 };
+struct RecurForward {
+    const void *x, *gate;
+    void* out;
+    int64_t x_sequence, x_row, gate_sequence, gate_row, out_sequence, out_row;
+    const float* state;  // or NULL: zeros
+    float* state_out;
+    int64_t state_row, state_out_row;
+    float* carries;      // or NULL
+    const int64_t* offsets;  // packed rows; or NULL
+    int64_t sequences, rows, channels;  // rows: of each sequence, or of all
+    int gating;
+};
+struct RecurBackward {
+    const void *dout, *x, *gate;
+    void *dx, *dgate;
+    int64_t dout_sequence, dout_row, x_sequence, x_row, gate_sequence, gate_row, dx_sequence, dx_row, dgate_sequence, dgate_row;
+    const float *state, *dstate_out;  // or NULL: zeros
+    float* dstate;
+    int64_t state_row, dstate_out_row, dstate_row;
+    const float* carries;
+    const int64_t* offsets;
+    int64_t sequences, rows, channels;
+    int gating;
+};
+size_t recur_workspace_bytes(int64_t sequences, int64_t rows, int64_t channels, bool packed, int type);
+int64_t recur_carry_rows(int64_t sequences, int64_t rows, bool packed);
+hipError_t launch_recurrence(const RecurForward& call, int type, void* ws, hipStream_t stream);
+hipError_t launch_recurrence_backward(const RecurBackward& call, int type, void* ws, hipStream_t stream);
+
+// ---- tokens to their experts' rows and back (ls_experts.hip); strides in elements
+size_t experts_workspace_bytes(int64_t pairs, int64_t experts);
+hipError_t launch_experts_sort(const void* ids, int id_bits, int64_t pairs, int64_t experts, int64_t* offsets, int32_t* order,
+                               int32_t* places, void* ws, hipStream_t stream);
+enum ExpertsMove : int { EXPERTS_GATHER = 0, EXPERTS_COMBINE = 1, EXPERTS_COMBINE_BACKWARD = 2 };
+struct ExpertsRows {
+    const void* x;        // tokens x channels: what is gathered, or the gradient of the sums
+    const void* rows;     // rows_count x channels: what is combined
+    void* rows_out;       // rows_count x channels: what gather and the gradient write
+    void* out;            // tokens x channels: the sums
+    int64_t x_row, rows_row, rows_out_row, out_row;
+    const int32_t* places;  // tokens x top
+    const void* weights;    // tokens x top, or NULL: ones
+    void* dweights;
+    int64_t tokens, rows_count, channels;
+    int top, weight_type;
+};
+hipError_t launch_experts_rows(const ExpertsRows& call, ExpertsMove move, int type, hipStream_t stream);
+
 }  // namespace ls
