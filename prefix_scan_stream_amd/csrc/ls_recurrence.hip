@@ -3,16 +3,17 @@
 //
 // A token is the affine map h -> a h + b of each channel, and maps compose:
 //     (a1, b1) then (a2, b2)  =  (a2 a1, a2 b1 + b2),
-// so the recurrence is a scan.  Channels lie beside each other in memory and are
-// independent: a lane owns CPL neighbouring channels (4 bytes of a row), a wave RC_ROWS
-// consecutive tokens of its 64 CPL channels, and a block's waves lie one behind the other
-// in time.  Per tile (waves x RC_ROWS tokens):
+// so the recurrence is a scan. Channels lie beside each
+// other in memory and are independent: a lane owns CPL neighbouring
+// channels (4 bytes of a row), a wave some consecutive tokens of its 64 CPL channels, and a
+// block's waves lie one behind the other in time.  Per tile (64 or 128 tokens):
 //   1. every wave loads its rows (each load 256 consecutive bytes), makes a and b of them in
 //      float32 and composes its map;
-//   2. the waves' maps meet in LDS; every wave applies those in front of it to the tile's
-//      carry and goes through its rows once more, from registers, writing h.
-// The block walks the tiles of its sequence (packed rows: of all sequences) and keeps the
-// carry in registers; the next tile's rows are on their way while a tile is finished.
+//   2. the waves' maps meet in LDS; every wave applies those in front of it to the value in
+//      front of the tile and goes through its rows once more, from registers, writing h.
+// So every byte is read once and written once.  The value in front of a tile comes from the
+// block's last tile, where a block walks its sequence and the next tile's rows are on their
+// way meanwhile, or through the workspace, where each tile is a block ("tiles as blocks").
 //
 // Backward, with mu_t = a_t lambda_t the gradient that h_{t-1} receives:
 //     lambda_t = dh_t + mu_{t+1},   mu_t = a_t mu_{t+1} + a_t dh_t,
@@ -27,11 +28,8 @@
 
 namespace ls {
 
-constexpr int RC_ROWS = 16;    // tokens per wave and tile
-constexpr int RC_WAVES = 8;
+constexpr int RC_TILE = 128;   // most tokens of a tile
 constexpr int RC_PERIOD = 64;  // a carry is kept of every 64th row
-constexpr int RC_TILE = RC_WAVES * RC_ROWS;
-static_assert(RC_TILE % RC_PERIOD == 0 && RC_PERIOD % RC_ROWS == 0, "tiles hold whole periods, periods whole waves");
 
 // A lane's part of a row: 4 bytes, or one 16-bit element where rows are not aligned to two.
 template <class E, int CPL>
@@ -72,25 +70,66 @@ __device__ __forceinline__ void store_state(__amdgpu_buffer_rsrc_t rs, uint32_t 
 }
 
 // A row's window in a matrix: `bytes` of it from the block's first channel, none if it is not there.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_window(const void* base, int64_t offset, bool there, uint32_t bytes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_window(const void* p, bool there, uint32_t bytes)
 {
-    return make_rsrc(static_cast<const char*>(base) + offset, there ? bytes : 0u);
+    return make_rsrc(p, there ? bytes : 0u);
+}
+
+__device__ __forceinline__ uint64_t uniform(uint64_t v)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v)), hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
+    return (uint64_t(hi) << 32) | lo;
+}
+
+// Rows one after the other, of which `left` are there.  The compiler must not see through the
+// address and the count: it would make all rows' windows at once, more than the scalar registers hold, and
+// keep them in vector registers.
+struct RowWalk {
+    uint64_t at;
+    int64_t row;  // bytes
+    uint32_t bytes;
+    int left;
+    __device__ __forceinline__ RowWalk(const char* base, int64_t first, int64_t row_bytes, uint32_t width, int rows_left)
+        : at(uniform(reinterpret_cast<uint64_t>(base) + uint64_t(first * row_bytes))), row(row_bytes), bytes(width),
+          left(__builtin_amdgcn_readfirstlane(rows_left))
+    {
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t window() const
+    {
+        return row_window(reinterpret_cast<const void*>(at), left > 0, bytes);
+    }
+    __device__ __forceinline__ void step(int64_t by)
+    {
+        at += uint64_t(by);
+        asm volatile("" : "+s"(at));
+    }
+    __device__ __forceinline__ void next()
+    {
+        step(row);
+        --left;
+        asm volatile("" : "+s"(left));
+    }
+    // towards the first row: `left` counts what lies in front, this row among it
+    __device__ __forceinline__ void previous(bool there)
+    {
+        step(-row);
+        left = __builtin_amdgcn_readfirstlane(there ? 1 : 0);
+        asm volatile("" : "+s"(left));
+    }
+};
+
+// Rows from `row` on, at most `most`.
+__device__ __forceinline__ int rows_left(int64_t rows, int64_t row, int most)
+{
+    const int64_t n = rows - row;
+    return n < 0 ? 0 : n < most ? int(n) : most;
 }
 
 // ---------------------------------------------------------------- the gate
 
-// The decay of one token and channel, as a value that gives both a and 1 - a to full
-// precision: sigmoid(-|g|) is the smaller of the two, its sign says which.
-struct Decay {
-    float u;
-    __device__ __forceinline__ float keep(int gating) const
-    {
-        return gating != GATE_SIGMOID ? u : (u > 0.0f ? 1.0f - u : -u);
-    }
-};
-
 __device__ __forceinline__ float gate_exp(float g) { return __builtin_amdgcn_exp2f(g * 1.44269504088896340736f); }
 
+// a = 1 / (1 + exp(-g)) and 1 - a, each to its own full precision: the smaller one is made first.
 __device__ __forceinline__ void sigmoid_both(float g, float& a, float& rest)
 {
     const float e = gate_exp(-__builtin_fabsf(g));
@@ -99,33 +138,41 @@ __device__ __forceinline__ void sigmoid_both(float g, float& a, float& rest)
     rest = g >= 0.0f ? small : big;
 }
 
-// a, and b = what the token puts in.
-template <class E, int CPL>
-__device__ __forceinline__ void token_maps(int gating, const uint32_t (&rx)[RC_ROWS], const uint32_t (&rg)[RC_ROWS],
-                                           float (&a)[RC_ROWS][CPL], float (&b)[RC_ROWS][CPL])
+// a and b = what the token puts in, from the gate and x.
+template <int GATING>
+__device__ __forceinline__ void token_map(float g, float x, float& a, float& b)
 {
-#pragma unroll
-    for (int j = 0; j < RC_ROWS; ++j) {
-        E::unpack(rx[j], b[j]);
-        E::unpack(rg[j], a[j]);
-    }
-    if (gating == GATE_SIGMOID) {
-#pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j)
-#pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                float rest;
-                sigmoid_both(a[j][c], a[j][c], rest);
-                b[j][c] *= rest;
-            }
-    } else if (gating == GATE_LOG) {
-#pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j)
-#pragma unroll
-            for (int c = 0; c < CPL; ++c)
-                a[j][c] = gate_exp(a[j][c]);
+    if constexpr (GATING == GATE_SIGMOID) {
+        float rest;
+        sigmoid_both(g, a, rest);
+        b = x * rest;
+    } else {
+        a = GATING == GATE_LOG ? gate_exp(g) : g;
+        b = x;
     }
 }
+
+// A decay in one register that gives a and 1 - a to full precision: of a sigmoid the smaller of the two, with a
+// sign that says which.
+template <int GATING>
+struct Decay {
+    float u;
+    __device__ __forceinline__ void make(float g)
+    {
+        if constexpr (GATING == GATE_SIGMOID) {
+            const float e = gate_exp(-__builtin_fabsf(g));
+            const float small = e * __builtin_amdgcn_rcpf(1.0f + e);
+            // not 0 for a >= 1/2, as 0 has no side (a gate beyond 87: 1 - a is below float32's range)
+            u = g >= 0.0f ? __builtin_fmaxf(small, 1e-38f) : -small;
+            u = g != g ? g : u;
+        } else {
+            u = GATING == GATE_LOG ? gate_exp(g) : g;
+        }
+    }
+    __device__ __forceinline__ void nothing() { u = GATING == GATE_SIGMOID ? 1e-38f : 1.0f; }  // a = 1
+    __device__ __forceinline__ float a() const { return GATING != GATE_SIGMOID ? u : u > 0.0f ? 1.0f - u : -u; }
+    __device__ __forceinline__ float rest() const { return GATING != GATE_SIGMOID ? 1.0f : u > 0.0f ? u : 1.0f + u; }
+};
 
 // ---------------------------------------------------------------- packed rows
 
@@ -175,64 +222,392 @@ __device__ __forceinline__ void mark_rows(const int64_t* offsets, int64_t sequen
     __syncthreads();
 }
 
-// ---------------------------------------------------------------- forward
+// ---------------------------------------------------------------- maps
 
-// A wave's composed map (or, behind a sequence's start, the value itself).
+// A composed map (or, behind a sequence's start, h alone: the value itself).
 template <int CPL>
 struct alignas(8 * CPL) WaveMap {
     float a[CPL], h[CPL];
 };
 
-template <class E, int CPL, bool PACKED>
-__global__ __launch_bounds__(RC_WAVES * 64) void recur_forward_kernel(RecurForward q)
+// ---------------------------------------------------------------- tiles as blocks of their own
+// Where sequences and channels are too few to fill the GPU with blocks that walk, each tile is a
+// block.  The tiles of a chain (a sequence, or the packed rows; and a group of channels) get their
+// places in it from a counter, in the order blocks start, and a block only ever waits for lower
+// places: for blocks that run or have run, however many of them fit and whatever else the GPU
+// does.  (A block that stays to hand values to later places would not do: 256 chains filled the GPU
+// with such blocks, and the later ones never started.)
+//
+// Places form groups of RC_GROUP.  A tile publishes its map, composes those in front of it in its group (each
+// wave fetches one),
+// and applies them to the group's front, the value in front of its first place.  The group's last
+// tile publishes the next group's front.  So a value passes a group with one store and one load,
+// while a tile reads at most RC_GROUP - 1 maps.  A tile with a sequence's start (backward: end)
+// does not depend on what is in front, and maps say so.
+//
+// A word that is 0 is empty; values are made not to be 0 (a zero becomes -0, which shows in
+// nothing but the sign of a zero).  A group counts the tiles that have read all they need, and the last
+// one sets its words and the counter back to 0; so does the last place with the chain's
+// counter.  So a call leaves the workspace as it found it: all 0.
+
+constexpr int RC_GROUP = 8;                   // a wave of a block for each
+constexpr int RC_COUNTER = 32;                // 32-bit words from counter to counter: a line each
+constexpr uint32_t RC_RESTART = 0x7fc0c0deu;  // for a factor: nothing passes (a NaN that no product makes)
+
+struct ChainLayout {
+    int64_t chains, most, groups;  // most places of a chain, and its groups
+    size_t maps, fronts, counts, bytes;  // offsets
+};
+__host__ __device__ inline ChainLayout chain_layout(int64_t chains, int64_t most, int lanes_channels)
+{
+    ChainLayout l;
+    l.chains = chains;
+    l.most = most;
+    l.groups = (most + RC_GROUP - 1) / RC_GROUP;
+    l.counts = sizeof(WsHeader) + size_t(chains) * RC_COUNTER * 4;
+    l.maps = l.counts + size_t(chains) * size_t(l.groups) * RC_COUNTER * 4;
+    l.fronts = l.maps + size_t(chains) * size_t(most) * size_t(lanes_channels) * 8;
+    l.bytes = l.fronts + size_t(chains) * size_t(l.groups) * size_t(lanes_channels) * 4;
+    return l;
+}
+
+// What a tile's waves fetch of its group, in LDS; `arrived` starts at 0.
+template <int CPL>
+struct GroupParts {
+    WaveMap<CPL> maps[RC_GROUP - 1][64];
+    float value[CPL][64];  // in front of the tile
+    int restart[RC_GROUP - 1], arrived;
+};
+
+template <int CPL>
+struct Chain {
+    WsHeader* header;
+    uint32_t* counter;  // places given out
+    uint32_t* counts;   // of each group: tiles that have read what they need
+    uint64_t* maps;     // [place][64 CPL]: factor | value << 32
+    uint32_t* fronts;   // [group][64 CPL]
+    int64_t most, places;
+
+    static constexpr int CH = 64 * CPL;
+
+    __device__ __forceinline__ Chain() {}
+    __device__ __forceinline__ Chain(void* ws, const ChainLayout& l, int64_t chain)
+        : header(static_cast<WsHeader*>(ws)), most(l.most), places(l.most)
+    {
+        char* p = static_cast<char*>(ws);
+        counter = reinterpret_cast<uint32_t*>(p + sizeof(WsHeader)) + chain * RC_COUNTER;
+        counts = reinterpret_cast<uint32_t*>(p + l.counts) + chain * l.groups * RC_COUNTER;
+        maps = reinterpret_cast<uint64_t*>(p + l.maps) + chain * l.most * CH;
+        fronts = reinterpret_cast<uint32_t*>(p + l.fronts) + chain * l.groups * CH;
+    }
+
+    // The block's place, in the order blocks start; `most`: the workspace is not as it should be.
+    __device__ __forceinline__ int64_t take_place(uint32_t& shared) const
+    {
+        if (most == 1)
+            return 0;
+        if (threadIdx.x == 0) {
+            const uint32_t t = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (int64_t(t) == most - 1)
+                __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (int64_t(t) >= most)
+                flag_error(header, WS_ERR_BAD_TICKET);
+            shared = t;
+        }
+        __syncthreads();
+        const int64_t t = uint32_t(__builtin_amdgcn_readfirstlane(shared));
+        return t < most ? t : most;
+    }
+
+    // Whether a wait is to end without what it waits for, for the whole wave: it has lasted too long, which is then on
+    // record; or it has lasted a while and another one is on record (or a chain's waits would end one after the other).
+    __device__ __forceinline__ bool gives_up(uint64_t start, int lane) const
+    {
+        const uint64_t ticks = uint64_t(wall_clock64()) - start;
+        const bool late = ticks >= WAIT_LIMIT_TICKS;
+        const bool given_up = ticks >= FALLBACK_TICKS &&
+                              __hip_atomic_load(&header->error_flags, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0;
+        if (__builtin_amdgcn_readfirstlane(int(late || given_up)) == 0)
+            return false;
+        if (late && lane == 0)
+            flag_error(header, WS_ERR_WAIT_TIMEOUT);
+        return true;
+    }
+
+    __device__ __forceinline__ void publish_map(int64_t place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool restart) const
+    {
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            const uint32_t f = restart ? RC_RESTART : to_bits(a[c]);
+            const uint64_t w = (uint64_t(to_bits(h[c])) << 32) | f;
+            status_store(maps + place * CH + lane * CPL + c, w == 0 ? 0x80000000ull : w);
+        }
+    }
+
+    // Two 32-bit words at once where a lane has two.
+    __device__ __forceinline__ void store_front(int64_t group, int lane, const uint32_t (&w)[CPL]) const
+    {
+        uint32_t* p = fronts + group * CH + lane * CPL;
+        if constexpr (CPL == 2)
+            status_store(reinterpret_cast<uint64_t*>(p), (uint64_t(w[1]) << 32) | w[0]);
+        else
+            __hip_atomic_store(p, w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ void publish_front(int64_t group, int lane, const float (&h)[CPL]) const
+    {
+        uint32_t w[CPL];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+            w[c] = to_bits(h[c]) == 0 ? 0x80000000u : to_bits(h[c]);
+        store_front(group, lane, w);
+    }
+    __device__ __forceinline__ void wait_front(int64_t group, int lane, float (&h)[CPL]) const
+    {
+        const uint32_t* p = fronts + group * CH + lane * CPL;
+        const uint64_t start = wait_start();
+        for (;;) {
+            bool there;
+            if constexpr (CPL == 2) {
+                const uint64_t w = status_load(reinterpret_cast<const uint64_t*>(p));
+                h[0] = from_bits<float>(uint32_t(w));
+                h[1] = from_bits<float>(uint32_t(w >> 32));
+                there = uint32_t(w) != 0 && uint32_t(w >> 32) != 0;
+            } else {
+                const uint32_t w = __hip_atomic_load(const_cast<uint32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                h[0] = from_bits<float>(w);
+                there = w != 0;
+            }
+            if (__ballot(!there) == 0 || gives_up(start, lane))
+                return;
+            __builtin_amdgcn_s_sleep(2);
+        }
+    }
+
+    // The map of a place, once it is there (the whole wave).  Returns whether it restarts.
+    __device__ __forceinline__ bool wait_map(int64_t place, int lane, float (&a)[CPL], float (&h)[CPL]) const
+    {
+        const uint64_t* p = maps + place * CH + lane * CPL;
+        uint64_t w[CPL];
+        const uint64_t start = wait_start();
+        for (;;) {
+            bool there = true;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                w[c] = status_load(p + c);
+                there &= w[c] != 0;
+            }
+            if (__ballot(!there) == 0 || gives_up(start, lane))
+                break;
+            __builtin_amdgcn_s_sleep(2);
+        }
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            a[c] = from_bits<float>(uint32_t(w[c]));
+            h[c] = from_bits<float>(uint32_t(w[c] >> 32));
+        }
+        return uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(w[0]))) == RC_RESTART;
+    }
+
+    // A tile's part in the chain.  One wave, the link, hands out the tile's map (a, h; cut: it restarts), ...
+    __device__ __forceinline__ void hand_out(int64_t place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool cut) const
+    {
+        const int at = int(place % RC_GROUP);
+        if (place == places - 1)
+            return;
+        if (at < RC_GROUP - 1)
+            publish_map(place, lane, a, h, cut);
+        else if (cut)
+            publish_front(place / RC_GROUP + 1, lane, h);
+    }
+    // ... each of the other waves (`which` of them, from 0) fetches one of the maps in front of it in its group, ...
+    __device__ __forceinline__ void collect(int64_t place, int which, int lane, GroupParts<CPL>& parts) const
+    {
+        const int count = int(place % RC_GROUP);
+        if (which >= count)
+            return;
+        WaveMap<CPL> m;
+        const bool again = wait_map(place - count + which, lane, m.a, m.h);
+        parts.maps[which][lane] = m;
+        if (lane == 0)
+            parts.restart[which] = again;
+        // a wave's LDS accesses keep their order; the compiler is to keep it too
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        if (lane == 0)
+            __hip_atomic_fetch_add(&parts.arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+    // ... and the link makes of these and the group's front (the first group's: `v`) the value in front of the tile and hands on
+    // what leaves it.  All that can be done before the front is there is done by then: from front to front is
+    // one multiply-add.
+    __device__ __forceinline__ void link(int64_t place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool cut,
+                                         GroupParts<CPL>& parts, float (&v)[CPL], float (&leaves)[CPL]) const
+    {
+        const int count = int(place % RC_GROUP);
+        // the collecting waves end their waits in any case
+        while (__builtin_amdgcn_readfirstlane(__hip_atomic_load(&parts.arrived, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) < count)
+            __builtin_amdgcn_s_sleep(1);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        bool group_cut = false;
+        float ga[CPL], gh[CPL], all_a[CPL], all_h[CPL];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            ga[c] = 1.0f;
+            gh[c] = 0.0f;
+        }
+        for (int j = 0; j < count; ++j) {
+            const WaveMap<CPL> o = parts.maps[j][lane];
+            const bool again = __builtin_amdgcn_readfirstlane(parts.restart[j]) != 0;
+            group_cut |= again;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                gh[c] = again ? o.h[c] : __builtin_fmaf(o.a[c], gh[c], o.h[c]);
+                ga[c] *= o.a[c];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            all_h[c] = cut ? h[c] : __builtin_fmaf(a[c], gh[c], h[c]);
+            all_a[c] = a[c] * ga[c];
+        }
+        if (place >= RC_GROUP)
+            wait_front(place / RC_GROUP, lane, v);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+            leaves[c] = cut || group_cut ? all_h[c] : __builtin_fmaf(all_a[c], v[c], all_h[c]);
+        if (!cut && count == RC_GROUP - 1 && place != places - 1)
+            publish_front(place / RC_GROUP + 1, lane, leaves);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            v[c] = group_cut ? gh[c] : __builtin_fmaf(ga[c], v[c], gh[c]);
+            parts.value[c][lane] = v[c];
+        }
+    }
+
+    // By one wave behind a barrier, when the tile has read all it needs of its group: signs off.
+    __device__ __forceinline__ uint32_t leave(int64_t place, int lane) const
+    {
+        uint32_t before = 0;
+        if (places > 1 && lane == 0)
+            before = __hip_atomic_fetch_add(counts + place / RC_GROUP * RC_COUNTER, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return before;
+    }
+    // Last step, some time later: whoever was the group's last to sign off (`before` of them) sets its words back.
+    __device__ __forceinline__ void clear(int64_t place, int lane, uint32_t before) const
+    {
+        const int64_t group = place / RC_GROUP, first = group * RC_GROUP;
+        const int in_group = int(places - first < RC_GROUP ? places - first : RC_GROUP);
+        if (places == 1 || __builtin_amdgcn_readfirstlane(int(before)) != in_group - 1)
+            return;
+        for (int j = 0; j < in_group - 1; ++j)
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                status_store(maps + (first + j) * CH + lane * CPL + c, 0);
+        if (group > 0) {
+            const uint32_t none[CPL] = {};
+            store_front(group, lane, none);
+        }
+        if (lane == 0)
+            __hip_atomic_store(counts + group * RC_COUNTER, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+};
+
+// What a block works on.
+template <int CPL, bool PACKED, bool CHAINED>
+struct Work {
+    static constexpr int CH = 64 * CPL;
+    int lane, wave, waves, tile_rows, tile_shift;
+    uint32_t chains, which, member, members;  // this block's chain, and which of the chain's blocks it is
+    int64_t chain, c0;                        // sequence, first channel
+    uint32_t here;                            // channels
+    int64_t rows, tiles, places;              // rows there are; tiles of the call, and those with rows
+
+    __device__ __forceinline__ Work(int rows_per_wave, int64_t sequences, int64_t call_rows, int64_t channels, const int64_t* offsets)
+    {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        waves = blockDim.x >> 6;
+        tile_rows = waves * rows_per_wave;
+        tile_shift = __builtin_ctz(uint32_t(tile_rows));
+        const uint32_t groups = uint32_t((channels + CH - 1) / CH);
+        chains = (PACKED ? 1 : uint32_t(sequences)) * groups;
+        which = CHAINED ? blockIdx.x % chains : blockIdx.x;
+        member = CHAINED ? blockIdx.x / chains : 0;
+        members = CHAINED ? gridDim.x / chains : 1;
+        chain = which / groups;
+        c0 = int64_t(which % groups) * CH;
+        here = uint32_t(channels - c0 < CH ? channels - c0 : CH);
+        rows = call_rows;
+        if constexpr (PACKED) {
+            const int64_t live = offsets[sequences];
+            rows = int64_t(uniform(uint64_t(live < 0 ? 0 : live < rows ? live : rows)));
+        }
+        tiles = call_rows > 0 ? (call_rows + tile_rows - 1) >> tile_shift : 1;
+        places = (rows + tile_rows - 1) >> tile_shift;
+    }
+};
+
+// ---------------------------------------------------------------- forward
+
+template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED>
+__global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForward q, void* ws)
 {
     constexpr int CH = 64 * CPL;
-    __shared__ WaveMap<CPL> maps[2][RC_WAVES][64];
-    __shared__ int restart[2][RC_WAVES];
+    __shared__ WaveMap<CPL> maps[CHAINED ? 1 : 2][WAVES][64];
+    __shared__ int restart[CHAINED ? 1 : 2][WAVES];
+    __shared__ GroupParts<CPL> parts;
     __shared__ int head_seq[PACKED ? RC_TILE : 1], end_seq[PACKED ? RC_TILE : 1];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const int tile_rows = waves * RC_ROWS;
-    const int64_t groups = (q.channels + CH - 1) / CH;
-    const int64_t chain = blockIdx.x / groups, c0 = (blockIdx.x % groups) * CH;
-    const uint32_t here = uint32_t(q.channels - c0 < CH ? q.channels - c0 : CH);  // channels of this block
-    const uint32_t bytes = here * E::size, state_bytes = here * 4;
-    const uint32_t voff = lane * CPL * E::size;
-    int64_t rows = q.rows;
-    if constexpr (PACKED) {
-        const int64_t live = q.offsets[q.sequences];
-        rows = live < 0 ? 0 : live < rows ? live : rows;
-    }
+    __shared__ uint32_t place_shared;
+    const Work<CPL, PACKED, CHAINED> w(ROWS, q.sequences, q.rows, q.channels, q.offsets);
+    const int lane = w.lane, wave = w.wave, waves = w.waves;
+    const int64_t chain = w.chain, c0 = w.c0, rows = w.rows;
+    const uint32_t bytes = w.here * E::size, state_bytes = w.here * 4, voff = lane * CPL * E::size;
     const char* x = static_cast<const char*>(q.x) + (chain * q.x_sequence + c0) * E::size;
     const char* g = static_cast<const char*>(q.gate) + (chain * q.gate_sequence + c0) * E::size;
     const char* out = static_cast<const char*>(q.out) + (chain * q.out_sequence + c0) * E::size;
-    const int64_t x_row = q.x_row * E::size, g_row = q.gate_row * E::size, out_row = q.out_row * E::size;
     const int64_t periods = (q.rows + RC_PERIOD - 1) / RC_PERIOD;
 
-    uint32_t rx[RC_ROWS], rg[RC_ROWS];
+    uint32_t rx[ROWS], rg[ROWS];
     auto load_rows = [&](int64_t row) {
+        const int n = rows_left(rows, row, ROWS);
+        RowWalk wx(x, row, q.x_row * E::size, bytes, n), wg(g, row, q.gate_row * E::size, bytes, n);
 #pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j) {
-            rx[j] = load_part<E, CPL>(row_window(x, (row + j) * x_row, row + j < rows, bytes), voff);
-            rg[j] = load_part<E, CPL>(row_window(g, (row + j) * g_row, row + j < rows, bytes), voff);
+        for (int j = 0; j < ROWS; ++j, wx.next(), wg.next()) {
+            rx[j] = load_part<E, CPL>(wx.window(), voff);
+            rg[j] = load_part<E, CPL>(wg.window(), voff);
         }
     };
 
+    Chain<CPL> links;
+    int64_t place = 0;
+    if constexpr (CHAINED) {
+        links = Chain<CPL>(ws, chain_layout(w.chains, w.tiles, CH), w.which);
+        links.places = w.places;
+        if (threadIdx.x == 0)
+            parts.arrived = 0;
+        place = links.take_place(place_shared);
+    }
+    // what is in front of the sequence; of a block that walks, of its next tile
     float carry[CPL] = {};
-    if (!PACKED && q.state != nullptr)
+    if (!PACKED && q.state != nullptr && place < RC_GROUP)  // the first group's front
         load_state<CPL>(make_rsrc(q.state + chain * q.state_row + c0, state_bytes), lane, carry);
-    load_rows(wave * RC_ROWS);
-    int turn = 0;
-    for (int64_t row0 = 0; row0 < rows; row0 += tile_rows, turn ^= 1) {
-        const int64_t row = row0 + wave * RC_ROWS;
-        float a[RC_ROWS][CPL], b[RC_ROWS][CPL];
-        token_maps<E, CPL>(q.gating, rx, rg, a, b);
-        if (row0 + tile_rows < rows)
-            load_rows(row + tile_rows);
-        if (row + RC_ROWS > rows) {
+    if (place < w.places)
+        load_rows((place << w.tile_shift) + wave * ROWS);
+    for (int turn = 0; place < w.places; ++place, turn ^= 1) {
+        const int64_t row0 = place << w.tile_shift, row = row0 + wave * ROWS;
+        float a[ROWS][CPL], b[ROWS][CPL];
 #pragma unroll
-            for (int j = 0; j < RC_ROWS; ++j)
-                if (row + j >= rows) {
+        for (int j = 0; j < ROWS; ++j) {
+            float xv[CPL], gv[CPL];
+            E::unpack(rx[j], xv);
+            E::unpack(rg[j], gv);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                token_map<GATING>(gv[c], xv[c], a[j][c], b[j][c]);
+        }
+        const int have = rows_left(rows, row, ROWS);
+        if (have < ROWS) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                if (j >= have) {
 #pragma unroll
                     for (int c = 0; c < CPL; ++c) {
                         a[j][c] = 1.0f;
@@ -240,29 +615,35 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_forward_kernel(RecurForwa
                     }
                 }
         }
+        if (!CHAINED && place + 1 < w.places)
+            load_rows(row + w.tile_rows);
         uint32_t heads = 0, ends = 0;
         int hs = -1, es = -1;
         if constexpr (PACKED) {
-            mark_rows(q.offsets, q.sequences, row0, tile_rows, head_seq, end_seq, lane);
-            hs = head_seq[wave * RC_ROWS + lane % RC_ROWS];
-            es = end_seq[wave * RC_ROWS + lane % RC_ROWS];
-            heads = uint32_t(__ballot(lane < RC_ROWS && hs >= 0));
-            ends = uint32_t(__ballot(lane < RC_ROWS && es >= 0));
+            mark_rows(q.offsets, q.sequences, row0, w.tile_rows, head_seq, end_seq, lane);
+            hs = head_seq[wave * ROWS + lane % ROWS];
+            es = end_seq[wave * ROWS + lane % ROWS];
+            heads = uint32_t(__ballot(lane < ROWS && hs >= 0));
+            ends = uint32_t(__ballot(lane < ROWS && es >= 0));
             if (heads != 0 && q.state != nullptr) {
-                float h0[RC_ROWS][CPL];
+                // four rows' states on their way at a time
 #pragma unroll
-                for (int j = 0; j < RC_ROWS; ++j) {
-                    const bool head = (heads >> j) & 1;
-                    const int64_t s = head ? read_lane(hs, j) : 0;
-                    load_state<CPL>(row_window(q.state + c0, s * q.state_row * 4, head, state_bytes), lane, h0[j]);
-                }
+                for (int j0 = 0; j0 < ROWS; j0 += 4) {
+                    float h0[4][CPL];
 #pragma unroll
-                for (int j = 0; j < RC_ROWS; ++j)
-                    if ((heads >> j) & 1) {
-#pragma unroll
-                        for (int c = 0; c < CPL; ++c)
-                            b[j][c] = __builtin_fmaf(a[j][c], h0[j][c], b[j][c]);
+                    for (int j = 0; j < 4; ++j) {
+                        const bool head = (heads >> (j0 + j)) & 1;
+                        const int64_t s = head ? read_lane(hs, j0 + j) : 0;
+                        load_state<CPL>(row_window(q.state + c0 + s * q.state_row, head, state_bytes), lane, h0[j]);
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if ((heads >> (j0 + j)) & 1) {
+#pragma unroll
+                            for (int c = 0; c < CPL; ++c)
+                                b[j0 + j][c] = __builtin_fmaf(a[j0 + j][c], h0[j][c], b[j0 + j][c]);
+                        }
+                }
             }
         }
 
@@ -273,7 +654,7 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_forward_kernel(RecurForwa
             m.h[c] = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j) {
+        for (int j = 0; j < ROWS; ++j) {
             const bool head = PACKED && ((heads >> j) & 1);
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
@@ -283,39 +664,94 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_forward_kernel(RecurForwa
                 m.a[c] *= a[j][c];
             }
         }
+        if constexpr (CHAINED && !PACKED) {
+            // the state is here before the map goes out: the chain's end may write it in place
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                asm volatile("" : "+v"(carry[c]));
+        }
         maps[turn][wave][lane] = m;
         if (PACKED && lane == 0)
             restart[turn][wave] = heads != 0;
         __syncthreads();
         float h[CPL];
-        for (int i = 0; i < waves; ++i) {
-            const WaveMap<CPL> o = maps[turn][i][lane];
-            const bool again = PACKED && __builtin_amdgcn_readfirstlane(restart[turn][i]) != 0;
+        uint32_t left = 0;
+        if constexpr (!CHAINED) {
+            for (int i = 0; i < waves; ++i) {
+                const WaveMap<CPL> o = maps[turn][i][lane];
+                const bool again = PACKED && __builtin_amdgcn_readfirstlane(restart[turn][i]) != 0;
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    if (i == wave)
+                        h[c] = carry[c];
+                    carry[c] = again ? o.h[c] : __builtin_fmaf(o.a[c], carry[c], o.h[c]);
+                }
+            }
+        } else {
+            // the waves in front, as a map
+            WaveMap<CPL> before;
+            bool cut = false;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                if (i == wave)
-                    h[c] = carry[c];
-                carry[c] = again ? o.h[c] : __builtin_fmaf(o.a[c], carry[c], o.h[c]);
+                before.a[c] = 1.0f;
+                before.h[c] = 0.0f;
             }
+            for (int i = 0; i < wave; ++i) {
+                const WaveMap<CPL> o = maps[0][i][lane];
+                const bool again = PACKED && __builtin_amdgcn_readfirstlane(restart[0][i]) != 0;
+                cut |= again;
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    before.h[c] = again ? o.h[c] : __builtin_fmaf(o.a[c], before.h[c], o.h[c]);
+                    before.a[c] *= o.a[c];
+                }
+            }
+            if (wave == waves - 1) {
+                const bool any = cut || heads != 0;
+                float leaves[CPL];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    m.h[c] = heads != 0 ? m.h[c] : __builtin_fmaf(m.a[c], before.h[c], m.h[c]);
+                    m.a[c] *= before.a[c];
+                }
+                links.hand_out(place, lane, m.a, m.h, any);
+                links.link(place, lane, m.a, m.h, any, parts, carry, leaves);
+                if (!PACKED && place == w.places - 1)
+                    store_state<CPL>(make_rsrc(q.state_out + chain * q.state_out_row + c0, state_bytes), lane, leaves);
+            } else {
+                links.collect(place, wave, lane, parts);
+            }
+            __syncthreads();
+            if (wave == 0)
+                left = links.leave(place, lane);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                h[c] = cut ? before.h[c] : __builtin_fmaf(before.a[c], parts.value[c][lane], before.h[c]);
         }
         if (q.carries != nullptr && row < rows && row % RC_PERIOD == 0)
             store_state<CPL>(make_rsrc(q.carries + (chain * periods + row / RC_PERIOD) * q.channels + c0, state_bytes), lane, h);
+        RowWalk wo(out, row, q.out_row * E::size, bytes, have);
 #pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j) {
+        for (int j = 0; j < ROWS; ++j, wo.next()) {
             const bool head = PACKED && ((heads >> j) & 1);
 #pragma unroll
             for (int c = 0; c < CPL; ++c)
                 h[c] = __builtin_fmaf(a[j][c], head ? 0.0f : h[c], b[j][c]);
-            store_part<E, CPL>(row_window(out, (row + j) * out_row, row + j < rows, bytes), voff, h);
+            store_part<E, CPL>(wo.window(), voff, h);
             if (PACKED && ((ends >> j) & 1))
                 store_state<CPL>(make_rsrc(q.state_out + read_lane(es, j) * q.state_out_row + c0, state_bytes), lane, h);
         }
+        if constexpr (CHAINED) {
+            if (wave == 0)
+                links.clear(place, lane, left);
+            break;
+        }
     }
-    if (!PACKED) {
-        if (wave == 0)
+    if constexpr (!PACKED) {
+        if (!CHAINED && wave == 0)
             store_state<CPL>(make_rsrc(q.state_out + chain * q.state_out_row + c0, state_bytes), lane, carry);
     } else if (q.state != q.state_out) {
-        for (int64_t s = wave; s < q.sequences; s += waves)
+        for (int64_t s = int64_t(w.member) * waves + wave; s < q.sequences; s += int64_t(w.members) * waves)
             if (q.offsets[s + 1] <= q.offsets[s]) {
                 float h[CPL] = {};
                 if (q.state != nullptr)
@@ -333,26 +769,19 @@ struct alignas(4 * CPL) WaveBack {
     float a[CPL], h[CPL], mu[CPL];
 };
 
-template <class E, int CPL, bool PACKED>
-__global__ __launch_bounds__(RC_WAVES * 64) void recur_backward_kernel(RecurBackward q)
+template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED>
+__global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBackward q, void* ws)
 {
     constexpr int CH = 64 * CPL;
-    __shared__ WaveBack<CPL> maps[2][RC_WAVES][64];
-    __shared__ int restart[2][RC_WAVES][2];
+    __shared__ WaveBack<CPL> maps[CHAINED ? 1 : 2][WAVES][64];
+    __shared__ int restart[CHAINED ? 1 : 2][WAVES][2];
+    __shared__ GroupParts<CPL> parts;
     __shared__ int head_seq[PACKED ? RC_TILE : 1], end_seq[PACKED ? RC_TILE : 1];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const int tile_rows = waves * RC_ROWS;
-    const int64_t groups = (q.channels + CH - 1) / CH;
-    const int64_t chain = blockIdx.x / groups, c0 = (blockIdx.x % groups) * CH;
-    const uint32_t here = uint32_t(q.channels - c0 < CH ? q.channels - c0 : CH);
-    const uint32_t bytes = here * E::size, state_bytes = here * 4;
-    const uint32_t voff = lane * CPL * E::size;
-    int64_t rows = q.rows;
-    if constexpr (PACKED) {
-        const int64_t live = q.offsets[q.sequences];
-        rows = live < 0 ? 0 : live < rows ? live : rows;
-    }
+    __shared__ uint32_t place_shared;
+    const Work<CPL, PACKED, CHAINED> w(ROWS, q.sequences, q.rows, q.channels, q.offsets);
+    const int lane = w.lane, wave = w.wave, waves = w.waves;
+    const int64_t chain = w.chain, c0 = w.c0, rows = w.rows;
+    const uint32_t bytes = w.here * E::size, state_bytes = w.here * 4, voff = lane * CPL * E::size;
     const char* x = static_cast<const char*>(q.x) + (chain * q.x_sequence + c0) * E::size;
     const char* g = static_cast<const char*>(q.gate) + (chain * q.gate_sequence + c0) * E::size;
     const char* dout = static_cast<const char*>(q.dout) + (chain * q.dout_sequence + c0) * E::size;
@@ -360,65 +789,76 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_backward_kernel(RecurBack
     const char* dg = static_cast<const char*>(q.dgate) + (chain * q.dgate_sequence + c0) * E::size;
     const int64_t periods = (q.rows + RC_PERIOD - 1) / RC_PERIOD;
 
+    // place 0 is the last tile
+    auto first_row = [&](int64_t place) { return (w.places - 1 - place) << w.tile_shift; };
+
+    Chain<CPL> links;
+    int64_t place = 0;
+    if constexpr (CHAINED) {
+        links = Chain<CPL>(ws, chain_layout(w.chains, w.tiles, CH), w.which);
+        links.places = w.places;
+        if (threadIdx.x == 0)
+            parts.arrived = 0;
+        place = links.take_place(place_shared);
+    }
     float mu_carry[CPL] = {};
-    if (!PACKED && q.dstate_out != nullptr)
+    if (!PACKED && q.dstate_out != nullptr && place < RC_GROUP)  // the first group's front
         load_state<CPL>(make_rsrc(q.dstate_out + chain * q.dstate_out_row + c0, state_bytes), lane, mu_carry);
-    int turn = 0;
-    const int64_t last0 = rows > 0 ? (rows - 1) / tile_rows * tile_rows : -1;
-    for (int64_t row0 = last0; row0 >= 0; row0 -= tile_rows, turn ^= 1) {
-        const int64_t row = row0 + wave * RC_ROWS;
-        uint32_t rx[RC_ROWS], rg[RC_ROWS], rd[RC_ROWS];
+    for (int turn = 0; place < w.places; ++place, turn ^= 1) {
+        const int64_t row0 = first_row(place), row = row0 + wave * ROWS;
+        const int have = rows_left(rows, row, ROWS);
+        uint32_t rx[ROWS], rg[ROWS], rd[ROWS];
+        float h[CPL];  // in front of the wave's period
+        load_state<CPL>(row_window(q.carries + c0 + (chain * periods + row / RC_PERIOD) * q.channels, have > 0, state_bytes), lane, h);
+        RowWalk wx(x, row, q.x_row * E::size, bytes, have), wg(g, row, q.gate_row * E::size, bytes, have),
+            wd(dout, row, q.dout_row * E::size, bytes, have);
 #pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j) {
-            const bool there = row + j < rows;
-            rx[j] = load_part<E, CPL>(row_window(x, (row + j) * q.x_row * E::size, there, bytes), voff);
-            rg[j] = load_part<E, CPL>(row_window(g, (row + j) * q.gate_row * E::size, there, bytes), voff);
-            rd[j] = load_part<E, CPL>(row_window(dout, (row + j) * q.dout_row * E::size, there, bytes), voff);
+        for (int j = 0; j < ROWS; ++j, wx.next(), wg.next(), wd.next()) {
+            rx[j] = load_part<E, CPL>(wx.window(), voff);
+            rg[j] = load_part<E, CPL>(wg.window(), voff);
+            rd[j] = load_part<E, CPL>(wd.window(), voff);
         }
-        // h in front of the wave's period
-        float h[CPL];
-        const int64_t period = row / RC_PERIOD;
-        load_state<CPL>(row_window(q.carries + c0, (chain * periods + period) * q.channels * 4, row < rows, state_bytes), lane, h);
         uint32_t heads = 0, ends = 0;
         int hs = -1, es = -1;
         if constexpr (PACKED) {
-            mark_rows(q.offsets, q.sequences, row0, tile_rows, head_seq, end_seq, lane);
-            hs = head_seq[wave * RC_ROWS + lane % RC_ROWS];
-            es = end_seq[wave * RC_ROWS + lane % RC_ROWS];
-            heads = uint32_t(__ballot(lane < RC_ROWS && hs >= 0));
-            ends = uint32_t(__ballot(lane < RC_ROWS && es >= 0));
+            mark_rows(q.offsets, q.sequences, row0, w.tile_rows, head_seq, end_seq, lane);
+            hs = head_seq[wave * ROWS + lane % ROWS];
+            es = end_seq[wave * ROWS + lane % ROWS];
+            heads = uint32_t(__ballot(lane < ROWS && hs >= 0));
+            ends = uint32_t(__ballot(lane < ROWS && es >= 0));
         }
         auto state_of = [&](int j, float (&v)[CPL]) {
             const int64_t s = read_lane(hs, j);
-            load_state<CPL>(row_window(q.state + c0, s * q.state_row * 4, q.state != nullptr, state_bytes), lane, v);
+            load_state<CPL>(row_window(q.state + c0 + s * q.state_row, q.state != nullptr, state_bytes), lane, v);
         };
         auto gradient_of = [&](int j, float (&v)[CPL]) {
             const int64_t s = read_lane(es, j);
-            load_state<CPL>(row_window(q.dstate_out + c0, s * q.dstate_out_row * 4, q.dstate_out != nullptr, state_bytes), lane, v);
+            load_state<CPL>(row_window(q.dstate_out + c0 + s * q.dstate_out_row, q.dstate_out != nullptr, state_bytes), lane, v);
         };
 
-        // the decays, with 1 - a to full precision too (see Decay)
-        Decay decay[RC_ROWS][CPL];
+        Decay<GATING> decay[ROWS][CPL];
 #pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j) {
+        for (int j = 0; j < ROWS; ++j) {
             float gv[CPL];
             E::unpack(rg[j], gv);
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                float u = gv[c];
-                if (q.gating == GATE_SIGMOID) {
-                    const float e = gate_exp(-__builtin_fabsf(u));
-                    const float small = e * __builtin_amdgcn_rcpf(1.0f + e);
-                    // a gate so far out that the smaller one is 0 keeps its side
-                    u = u >= 0.0f ? __builtin_fmaxf(small, 1e-38f) : -small;
-                    if (gv[c] != gv[c])
-                        u = gv[c];
-                } else if (q.gating == GATE_LOG) {
-                    u = gate_exp(u);
-                }
-                decay[j][c].u = row + j < rows ? u : (q.gating == GATE_SIGMOID ? 1e-38f : 1.0f);
+                decay[j][c].make(gv[c]);
+                if (j >= have)
+                    decay[j][c].nothing();
             }
         }
+        // Each pass over the rows makes a and 1 - a again: kept, they would take twice the registers, and a CU hold
+        // fewer blocks.
+        auto forget = [&]() {
+            if constexpr (GATING == GATE_SIGMOID) {
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c)
+                        asm volatile("" : "+v"(decay[j][c].u));
+            }
+        };
         WaveBack<CPL> m;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
@@ -426,30 +866,29 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_backward_kernel(RecurBack
             m.h[c] = 0.0f;
             m.mu[c] = 0.0f;
         }
-        const bool sigmoid = q.gating == GATE_SIGMOID;
 #pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j) {
+        for (int j = 0; j < ROWS; ++j) {
             if (PACKED && ((heads >> j) & 1))
                 state_of(j, m.h);
             float xv[CPL];
             E::unpack(rx[j], xv);
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                const float a = decay[j][c].keep(q.gating), u = decay[j][c].u;
-                const float rest = sigmoid ? (u > 0.0f ? u : 1.0f + u) : 1.0f;
-                m.h[c] = __builtin_fmaf(a, m.h[c], rest * xv[c]);
+                const float a = decay[j][c].a();
+                m.h[c] = __builtin_fmaf(a, m.h[c], decay[j][c].rest() * xv[c]);
                 m.a[c] *= a;
             }
         }
+        forget();
 #pragma unroll
-        for (int j = RC_ROWS - 1; j >= 0; --j) {
+        for (int j = ROWS - 1; j >= 0; --j) {
             if (PACKED && ((ends >> j) & 1))
                 gradient_of(j, m.mu);
             float dv[CPL];
             E::unpack(rd[j], dv);
 #pragma unroll
             for (int c = 0; c < CPL; ++c)
-                m.mu[c] = decay[j][c].keep(q.gating) * (dv[c] + m.mu[c]);
+                m.mu[c] = decay[j][c].a() * (dv[c] + m.mu[c]);
         }
         maps[turn][wave][lane] = m;
         if (PACKED && lane == 0) {
@@ -458,7 +897,7 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_backward_kernel(RecurBack
         }
         __syncthreads();
         // h in front of the wave, from its period's carry
-        constexpr int PER = RC_PERIOD / RC_ROWS;
+        constexpr int PER = RC_PERIOD / ROWS;
         for (int i = wave / PER * PER; i < wave; ++i) {
             const WaveBack<CPL> o = maps[turn][i][lane];
             const bool again = PACKED && __builtin_amdgcn_readfirstlane(restart[turn][i][0]) != 0;
@@ -467,19 +906,63 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_backward_kernel(RecurBack
                 h[c] = again ? o.h[c] : __builtin_fmaf(o.a[c], h[c], o.h[c]);
         }
         float mu[CPL];
-        for (int i = waves - 1; i >= 0; --i) {
-            const WaveBack<CPL> o = maps[turn][i][lane];
-            const bool again = PACKED && __builtin_amdgcn_readfirstlane(restart[turn][i][1]) != 0;
+        uint32_t left = 0;
+        if constexpr (!CHAINED) {
+            for (int i = waves - 1; i >= 0; --i) {
+                const WaveBack<CPL> o = maps[turn][i][lane];
+                const bool again = PACKED && __builtin_amdgcn_readfirstlane(restart[turn][i][1]) != 0;
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    if (i == wave)
+                        mu[c] = mu_carry[c];
+                    mu_carry[c] = again ? o.mu[c] : __builtin_fmaf(o.a[c], mu_carry[c], o.mu[c]);
+                }
+            }
+        } else {
+            // the waves behind, as a map
+            WaveMap<CPL> later;
+            bool cut = false;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                if (i == wave)
-                    mu[c] = mu_carry[c];
-                mu_carry[c] = again ? o.mu[c] : __builtin_fmaf(o.a[c], mu_carry[c], o.mu[c]);
+                later.a[c] = 1.0f;
+                later.h[c] = 0.0f;
             }
-        }
-        float before[RC_ROWS][CPL];
+            for (int i = waves - 1; i > wave; --i) {
+                const WaveBack<CPL> o = maps[0][i][lane];
+                const bool again = PACKED && __builtin_amdgcn_readfirstlane(restart[0][i][1]) != 0;
+                cut |= again;
 #pragma unroll
-        for (int j = 0; j < RC_ROWS; ++j) {
+                for (int c = 0; c < CPL; ++c) {
+                    later.h[c] = again ? o.mu[c] : __builtin_fmaf(o.a[c], later.h[c], o.mu[c]);
+                    later.a[c] *= o.a[c];
+                }
+            }
+            if (wave == 0) {
+                const bool any = cut || ends != 0;
+                float leaves[CPL];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    m.mu[c] = ends != 0 ? m.mu[c] : __builtin_fmaf(m.a[c], later.h[c], m.mu[c]);
+                    m.a[c] *= later.a[c];
+                }
+                links.hand_out(place, lane, m.a, m.mu, any);
+                links.link(place, lane, m.a, m.mu, any, parts, mu_carry, leaves);
+                if (!PACKED && place == w.places - 1)
+                    store_state<CPL>(make_rsrc(q.dstate + chain * q.dstate_row + c0, state_bytes), lane, leaves);
+            } else {
+                links.collect(place, wave - 1, lane, parts);
+            }
+            __syncthreads();
+            if (wave == 0)
+                left = links.leave(place, lane);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                mu[c] = cut ? later.h[c] : __builtin_fmaf(later.a[c], parts.value[c][lane], later.h[c]);
+        }
+        float before[ROWS][CPL];
+        forget();
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
             if (PACKED && ((heads >> j) & 1))
                 state_of(j, h);
             float xv[CPL];
@@ -487,13 +970,14 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_backward_kernel(RecurBack
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
                 before[j][c] = h[c];
-                const float a = decay[j][c].keep(q.gating), u = decay[j][c].u;
-                const float rest = sigmoid ? (u > 0.0f ? u : 1.0f + u) : 1.0f;
-                h[c] = __builtin_fmaf(a, h[c], rest * xv[c]);
+                h[c] = __builtin_fmaf(decay[j][c].a(), h[c], decay[j][c].rest() * xv[c]);
             }
         }
+        forget();
+        RowWalk ox(dx, row + ROWS - 1, q.dx_row * E::size, bytes, have == ROWS),
+            og(dg, row + ROWS - 1, q.dgate_row * E::size, bytes, have == ROWS);
 #pragma unroll
-        for (int j = RC_ROWS - 1; j >= 0; --j) {
+        for (int j = ROWS - 1; j >= 0; --j, ox.previous(j < have), og.previous(j < have)) {
             if (PACKED && ((ends >> j) & 1))
                 gradient_of(j, mu);
             float dv[CPL], xv[CPL], gx[CPL], gg[CPL];
@@ -501,25 +985,28 @@ __global__ __launch_bounds__(RC_WAVES * 64) void recur_backward_kernel(RecurBack
             E::unpack(rx[j], xv);
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                const float a = decay[j][c].keep(q.gating), u = decay[j][c].u;
-                const float rest = sigmoid ? (u > 0.0f ? u : 1.0f + u) : 1.0f;
-                const float lam = dv[c] + mu[c];
+                const float a = decay[j][c].a(), lam = dv[c] + mu[c];
                 mu[c] = a * lam;
-                gx[c] = lam * rest;
-                gg[c] = sigmoid ? gx[c] * a * (before[j][c] - xv[c]) : (q.gating == GATE_LOG ? mu[c] : lam) * before[j][c];
+                gx[c] = lam * decay[j][c].rest();
+                gg[c] = GATING == GATE_SIGMOID ? gx[c] * a * (before[j][c] - xv[c])
+                                               : (GATING == GATE_LOG ? mu[c] : lam) * before[j][c];
             }
-            const bool there = row + j < rows;
-            store_part<E, CPL>(row_window(dx, (row + j) * q.dx_row * E::size, there, bytes), voff, gx);
-            store_part<E, CPL>(row_window(dg, (row + j) * q.dgate_row * E::size, there, bytes), voff, gg);
+            store_part<E, CPL>(ox.window(), voff, gx);
+            store_part<E, CPL>(og.window(), voff, gg);
             if (PACKED && ((heads >> j) & 1))
                 store_state<CPL>(make_rsrc(q.dstate + read_lane(hs, j) * q.dstate_row + c0, state_bytes), lane, mu);
         }
+        if constexpr (CHAINED) {
+            if (wave == 0)
+                links.clear(place, lane, left);
+            break;
+        }
     }
-    if (!PACKED) {
-        if (wave == 0)
+    if constexpr (!PACKED) {
+        if (!CHAINED && wave == 0)
             store_state<CPL>(make_rsrc(q.dstate + chain * q.dstate_row + c0, state_bytes), lane, mu_carry);
     } else {
-        for (int64_t s = wave; s < q.sequences; s += waves)
+        for (int64_t s = int64_t(w.member) * waves + wave; s < q.sequences; s += int64_t(w.members) * waves)
             if (q.offsets[s + 1] <= q.offsets[s]) {
                 float v[CPL] = {};
                 if (q.dstate_out != nullptr)
@@ -571,9 +1058,60 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurForward q)
 
 // ---------------------------------------------------------------- launches
 
-size_t recur_workspace_bytes(int64_t, int64_t rows, int64_t, bool packed, int)
+// Blocks that walk keep the carry to themselves and load ahead; they take the call where the chains alone fill the
+// GPU, or where a chain is one tile.
+constexpr int64_t RC_WALKERS = 512;
+
+// Tokens per wave, and waves, of a tile.
+template <int CPL>
+struct ForwardShape {
+    static constexpr int rows = 16, waves = 8;
+};
+template <int CPL>
+struct BackwardShape {
+    static constexpr int rows = CPL == 2 ? 8 : 16, waves = 8;
+};
+
+struct ChainPlan {
+    bool chained;
+    int waves;
+    int64_t chains, tiles;
+};
+static ChainPlan chain_plan(int64_t sequences, int64_t rows, int64_t channels, bool packed, int per_lane, int wave_rows, int most_waves,
+                            int least_waves)
 {
-    return packed || rows > 1 ? sizeof(WsHeader) : 0;
+    const int64_t chains = (packed ? 1 : sequences) * ((channels + 64 * per_lane - 1) / (64 * per_lane));
+    int waves = most_waves;
+    while (waves > least_waves && (waves / 2) * wave_rows >= rows)
+        waves /= 2;
+    const int64_t tiles = (rows + waves * wave_rows - 1) / (waves * wave_rows);
+    return {packed || (tiles > 1 && chains < RC_WALKERS), waves, chains, tiles > 0 ? tiles : 1};
+}
+
+template <int CPL>
+static size_t chain_bytes(int64_t sequences, int64_t rows, int64_t channels, bool packed)
+{
+    size_t most = 0;
+    for (int back = 0; back < 2; ++back) {
+        const ChainPlan p = back ? chain_plan(sequences, rows, channels, packed, CPL, BackwardShape<CPL>::rows, BackwardShape<CPL>::waves,
+                                              RC_PERIOD / BackwardShape<CPL>::rows)
+                                 : chain_plan(sequences, rows, channels, packed, CPL, ForwardShape<CPL>::rows, ForwardShape<CPL>::waves, 1);
+        const size_t n = p.chained ? chain_layout(p.chains, p.tiles, 64 * CPL).bytes : 0;
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
+size_t recur_workspace_bytes(int64_t sequences, int64_t rows, int64_t channels, bool packed, int type)
+{
+    if (!packed && rows <= 1)
+        return 0;
+    size_t most = sizeof(WsHeader);
+    const size_t one = chain_bytes<1>(sequences, rows, channels, packed);
+    const size_t two = type == LOGITS_F32 ? 0 : chain_bytes<2>(sequences, rows, channels, packed);  // which one, the alignment tells
+    most = one > most ? one : most;
+    most = two > most ? two : most;
+    return most;
 }
 
 int64_t recur_carry_rows(int64_t sequences, int64_t rows, bool packed)
@@ -588,19 +1126,26 @@ bool multiples(const void* p, int64_t a, int64_t b, int64_t to)
     return reinterpret_cast<uintptr_t>(p) % uintptr_t(to) == 0 && a % to == 0 && b % to == 0;
 }
 
-int waves_for(int64_t rows, int least)
-{
-    int w = RC_WAVES;
-    while (w > least && (w / 2) * RC_ROWS >= rows)
-        w /= 2;
-    return w;
-}
-
 // A launch holds less than 2^32 threads: most sequences of a launch of `groups` blocks each.
 int64_t sequences_at_once(int64_t groups) { return (int64_t(1) << 22) / groups > 0 ? (int64_t(1) << 22) / groups : 1; }
 
+template <class E, int CPL, int GATING>
+hipError_t forward_of(const RecurForward& q, void* ws, hipStream_t stream)
+{
+    using S = ForwardShape<CPL>;
+    const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, 1);
+    const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
+    if (p.chained && q.offsets != nullptr)
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, true, true><<<blocks, threads, 0, stream>>>(q, ws);
+    else if (p.chained)
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, true><<<blocks, threads, 0, stream>>>(q, ws);
+    else
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, false><<<blocks, threads, 0, stream>>>(q, ws);
+    return hipGetLastError();
+}
+
 template <class E, int CPL>
-hipError_t launch_forward(const RecurForward& q, hipStream_t stream)
+hipError_t launch_forward(const RecurForward& q, void* ws, hipStream_t stream)
 {
     const int64_t groups = (q.channels + 64 * CPL - 1) / (64 * CPL), most = sequences_at_once(groups);
     if (q.offsets == nullptr && q.sequences > most) {
@@ -615,20 +1160,31 @@ hipError_t launch_forward(const RecurForward& q, hipStream_t stream)
         rest.state_out += most * q.state_out_row;
         if (q.carries != nullptr)
             rest.carries += recur_carry_rows(most, q.rows, false) * q.channels;
-        const hipError_t e = launch_forward<E, CPL>(first, stream);
-        return e != hipSuccess ? e : launch_forward<E, CPL>(rest, stream);
+        const hipError_t e = launch_forward<E, CPL>(first, ws, stream);
+        return e != hipSuccess ? e : launch_forward<E, CPL>(rest, ws, stream);
     }
-    const int64_t blocks = (q.offsets ? 1 : q.sequences) * groups;
-    const dim3 threads(64 * waves_for(q.rows, 1));
-    if (q.offsets)
-        recur_forward_kernel<E, CPL, true><<<dim3(uint32_t(blocks)), threads, 0, stream>>>(q);
+    if (q.gating == GATE_DECAY)
+        return forward_of<E, CPL, GATE_DECAY>(q, ws, stream);
+    return q.gating == GATE_LOG ? forward_of<E, CPL, GATE_LOG>(q, ws, stream) : forward_of<E, CPL, GATE_SIGMOID>(q, ws, stream);
+}
+
+template <class E, int CPL, int GATING>
+hipError_t backward_of(const RecurBackward& q, void* ws, hipStream_t stream)
+{
+    using S = BackwardShape<CPL>;
+    const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, RC_PERIOD / S::rows);
+    const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
+    if (p.chained && q.offsets != nullptr)
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, true, true><<<blocks, threads, 0, stream>>>(q, ws);
+    else if (p.chained)
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, true><<<blocks, threads, 0, stream>>>(q, ws);
     else
-        recur_forward_kernel<E, CPL, false><<<dim3(uint32_t(blocks)), threads, 0, stream>>>(q);
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, false><<<blocks, threads, 0, stream>>>(q, ws);
     return hipGetLastError();
 }
 
 template <class E, int CPL>
-hipError_t launch_backward(const RecurBackward& q, hipStream_t stream)
+hipError_t launch_backward(const RecurBackward& q, void* ws, hipStream_t stream)
 {
     const int64_t groups = (q.channels + 64 * CPL - 1) / (64 * CPL), most = sequences_at_once(groups);
     if (q.offsets == nullptr && q.sequences > most) {
@@ -646,16 +1202,12 @@ hipError_t launch_backward(const RecurBackward& q, hipStream_t stream)
             rest.dstate_out += most * q.dstate_out_row;
         rest.dstate += most * q.dstate_row;
         rest.carries += recur_carry_rows(most, q.rows, false) * q.channels;
-        const hipError_t e = launch_backward<E, CPL>(first, stream);
-        return e != hipSuccess ? e : launch_backward<E, CPL>(rest, stream);
+        const hipError_t e = launch_backward<E, CPL>(first, ws, stream);
+        return e != hipSuccess ? e : launch_backward<E, CPL>(rest, ws, stream);
     }
-    const int64_t blocks = (q.offsets ? 1 : q.sequences) * groups;
-    const dim3 threads(64 * waves_for(q.rows, RC_PERIOD / RC_ROWS));
-    if (q.offsets)
-        recur_backward_kernel<E, CPL, true><<<dim3(uint32_t(blocks)), threads, 0, stream>>>(q);
-    else
-        recur_backward_kernel<E, CPL, false><<<dim3(uint32_t(blocks)), threads, 0, stream>>>(q);
-    return hipGetLastError();
+    if (q.gating == GATE_DECAY)
+        return backward_of<E, CPL, GATE_DECAY>(q, ws, stream);
+    return q.gating == GATE_LOG ? backward_of<E, CPL, GATE_LOG>(q, ws, stream) : backward_of<E, CPL, GATE_SIGMOID>(q, ws, stream);
 }
 
 template <class E>
@@ -677,7 +1229,7 @@ hipError_t launch_step(const RecurForward& q, hipStream_t stream)
 
 }  // namespace
 
-hipError_t launch_recurrence(const RecurForward& q, int type, void*, hipStream_t stream)
+hipError_t launch_recurrence(const RecurForward& q, int type, void* ws, hipStream_t stream)
 {
     if (q.sequences == 0 || q.channels == 0)
         return hipSuccess;
@@ -687,28 +1239,28 @@ hipError_t launch_recurrence(const RecurForward& q, int type, void*, hipStream_t
         return type == LOGITS_F16 ? launch_step<F16>(q, stream) : launch_step<BF16>(q, stream);
     }
     if (type == LOGITS_F32)
-        return launch_forward<F32, 1>(q, stream);
+        return launch_forward<F32, 1>(q, ws, stream);
     const bool pairs = q.channels % 2 == 0 && multiples(q.x, q.x_sequence * 2, q.x_row * 2, 4) &&
                        multiples(q.gate, q.gate_sequence * 2, q.gate_row * 2, 4) && multiples(q.out, q.out_sequence * 2, q.out_row * 2, 4);
     if (type == LOGITS_F16)
-        return pairs ? launch_forward<F16, 2>(q, stream) : launch_forward<F16, 1>(q, stream);
-    return pairs ? launch_forward<BF16, 2>(q, stream) : launch_forward<BF16, 1>(q, stream);
+        return pairs ? launch_forward<F16, 2>(q, ws, stream) : launch_forward<F16, 1>(q, ws, stream);
+    return pairs ? launch_forward<BF16, 2>(q, ws, stream) : launch_forward<BF16, 1>(q, ws, stream);
 }
 
-hipError_t launch_recurrence_backward(const RecurBackward& q, int type, void*, hipStream_t stream)
+hipError_t launch_recurrence_backward(const RecurBackward& q, int type, void* ws, hipStream_t stream)
 {
     if (q.sequences == 0 || q.channels == 0)
         return hipSuccess;
     if (type == LOGITS_F32)
-        return launch_backward<F32, 1>(q, stream);
+        return launch_backward<F32, 1>(q, ws, stream);
     const bool pairs = q.channels % 2 == 0 && multiples(q.x, q.x_sequence * 2, q.x_row * 2, 4) &&
                        multiples(q.gate, q.gate_sequence * 2, q.gate_row * 2, 4) &&
                        multiples(q.dout, q.dout_sequence * 2, q.dout_row * 2, 4) &&
                        multiples(q.dx, q.dx_sequence * 2, q.dx_row * 2, 4) &&
                        multiples(q.dgate, q.dgate_sequence * 2, q.dgate_row * 2, 4);
     if (type == LOGITS_F16)
-        return pairs ? launch_backward<F16, 2>(q, stream) : launch_backward<F16, 1>(q, stream);
-    return pairs ? launch_backward<BF16, 2>(q, stream) : launch_backward<BF16, 1>(q, stream);
+        return pairs ? launch_backward<F16, 2>(q, ws, stream) : launch_backward<F16, 1>(q, ws, stream);
+    return pairs ? launch_backward<BF16, 2>(q, ws, stream) : launch_backward<BF16, 1>(q, ws, stream);
 }
 
 }  // namespace ls

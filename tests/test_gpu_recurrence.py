@@ -384,6 +384,45 @@ def test_two_streams_and_repeats():
         assert ps.workspace_error_flags(DEV, s) == 0
 
 
+@pytest.mark.parametrize("batch,channels", [(1, 64), (1, 512), (16, 2048), (64, 512), (520, 128)])
+def test_many_tiles_and_chains(batch, channels):
+    """Long sequences, and more chains of tiles than blocks that fit the GPU at once (a chain for each 128
+    channels of each sequence): against the recurrence in float64 by doubling windows."""
+    length = 20000 if batch == 1 else 1300
+    g = torch.Generator(device=DEV).manual_seed(batch)
+    x = torch.randn(batch, length, channels, device=DEV, generator=g).bfloat16()
+    gate = (torch.randn(batch, length, channels, device=DEV, generator=g) + 1).bfloat16()
+    c = ps.recurrence_carries(x)
+    out, last = ps.gated_recurrence(x, gate, carries=c)
+    dx, dg, ds = ps.gated_recurrence_backward(x, x, gate, c)
+
+    def scan(a, b):
+        step = 1
+        while step < length:
+            b = torch.cat([b[:, :step], b[:, step:] + a[:, step:] * b[:, :-step]], 1)
+            a = torch.cat([a[:, :step], a[:, step:] * a[:, :-step]], 1)
+            step *= 2
+        return b
+
+    for s in range(0, batch, max(1, batch // 4)):
+        xs, a = x[s:s + 1].double(), torch.sigmoid(gate[s:s + 1].double())
+        h = scan(a, (1 - a) * xs)
+        # decays are below 0.995 (gates below 5.3), so what float32 rounds away is some (10 + 6) * 200 * 2^-24 =
+        # 2e-4 of |h| < 6 or lambda < 50 at the very worst; 2^-8 of a value is bfloat16's rounding (2^-9) and more
+        assert bool(((out[s:s + 1].double() - h).abs() <= h.abs() * 2.0**-8 + 1e-3).all())
+        assert bool(((last[s] - h[0, -1]).abs() <= 1e-3).all())
+        behind = torch.cat([torch.zeros_like(a[:, :1]), a.flip(1)[:, :-1]], 1)
+        lam = scan(behind, xs.flip(1)).flip(1)
+        before = torch.cat([torch.zeros_like(h[:, :1]), h[:, :-1]], 1)
+        want = lam * (1 - a)
+        assert bool(((dx[s:s + 1].double() - want).abs() <= want.abs() * 2.0**-8 + 1e-3).all())
+        want = lam * (before - xs) * a * (1 - a)
+        assert bool(((dg[s:s + 1].double() - want).abs() <= want.abs() * 2.0**-8 + 1e-2).all())
+        assert bool(((ds[s] - (a * lam)[0, 0]).abs() <= 1e-2).all())
+    again = ps.gated_recurrence(x, gate)[0]
+    assert torch.equal(again, out) and ps.workspace_error_flags(DEV) == 0
+
+
 def test_refused_by_the_binding():
     x = torch.zeros(2, 5, 8, device=DEV)
     with pytest.raises(ValueError):
