@@ -58,16 +58,23 @@ struct Elements {
     static constexpr int per_word = VEC == 1 ? 1 : 4 / E::size;
     static constexpr int words = VEC / per_word;
     uint32_t w[words];
+    // once: the bytes are not asked for again soon, and need no place in the caches
+    template <bool ONCE = false>
     __device__ __forceinline__ void load(const void* p)
     {
         if constexpr (VEC * E::size == 2) {
             w[0] = *static_cast<const uint16_t*>(p);
         } else {
             typedef uint32_t v __attribute__((ext_vector_type(words)));
-            const v t = *static_cast<const v*>(p);
+            v t;
+            if constexpr (ONCE)
+                t = __builtin_nontemporal_load(static_cast<const v*>(p));
+            else
+                t = *static_cast<const v*>(p);
             __builtin_memcpy(w, &t, sizeof w);
         }
     }
+    template <bool ONCE = false>
     __device__ __forceinline__ void store(void* p) const
     {
         if constexpr (VEC * E::size == 2) {
@@ -76,7 +83,10 @@ struct Elements {
             typedef uint32_t v __attribute__((ext_vector_type(words)));
             v t;
             __builtin_memcpy(&t, w, sizeof w);
-            *static_cast<v*>(p) = t;
+            if constexpr (ONCE)
+                __builtin_nontemporal_store(t, static_cast<v*>(p));
+            else
+                *static_cast<v*>(p) = t;
         }
     }
     __device__ __forceinline__ void get(float (&f)[VEC]) const
