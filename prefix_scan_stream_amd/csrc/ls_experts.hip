@@ -15,9 +15,12 @@ namespace ls {
 
 // ---------------------------------------------------------------- sort
 
+// Pairs per turn and sort of 16384 x 8, 8192 x 4, 32768 x 8 and 131072 x 8 pairs by 256, 64, 128 and 256 experts: 2048 10.7, 8.5,
+// 10.9, 28.4 us; 1024 10.8, 8.1, 11.2, 29.8; 4096 13.5, 11.4, 13.1, 27.5 (too few blocks but for the last).  What is left are
+// two launches of a few microseconds: the counts, and each block's sums over the tiles' counts and its ranks.
 constexpr int EX_BLOCK = 512;
 constexpr int EX_WAVES = EX_BLOCK / 64;
-constexpr int EX_STEPS = 8;                              // pairs per lane and turn
+constexpr int EX_STEPS = 4;                              // pairs per lane and turn
 constexpr int EX_TURN = EX_BLOCK * EX_STEPS;             // pairs per block and turn
 constexpr int EX_TILES = 128;                            // most tiles
 
@@ -27,7 +30,9 @@ struct ExpertsTiles {
 };
 static ExpertsTiles experts_tiles(int64_t n)
 {
-    const int64_t turns = n > 0 ? (n + EX_TURN - 1) / EX_TURN : 1, per = (turns + EX_TILES - 1) / EX_TILES;
+    const int64_t turns = n > 0 ? (n + EX_TURN - 1) / EX_TURN : 1;
+    // two turns of one block are sooner done than a launch more: 2331 pairs 7.2 us against 8.2
+    const int64_t per = turns <= 2 ? turns : (turns + EX_TILES - 1) / EX_TILES;
     return {n, per * EX_TURN, int((turns + per - 1) / per)};
 }
 
@@ -76,22 +81,34 @@ __global__ __launch_bounds__(EX_BLOCK) void experts_place_kernel(const I* ids, E
             atomicAdd(&seen[expert_of(ids, p, t.n, experts)], 1u);
         __syncthreads();
     }
+    // each expert's pairs in all tiles and in the tiles in front, by several threads an expert where these are few
+    uint32_t* before = shared + (1 + EX_WAVES) * (experts + 1);  // [experts]
+    if (counts != nullptr) {
+        for (int e = tid; e < experts; e += EX_BLOCK)
+            seen[e] = before[e] = 0;
+        __syncthreads();
+        int wide = 64;
+        while (wide < experts && wide < EX_BLOCK)
+            wide *= 2;
+        const int split = EX_BLOCK / wide, part = tid / wide;
+        for (int e = tid % wide; e < experts; e += wide) {
+            uint32_t total = 0, front = 0;
+#pragma unroll 8
+            for (int i = part; i < t.tiles; i += split) {
+                const uint32_t c = counts[int64_t(i) * experts + e];
+                total += c;
+                front += i < int(blockIdx.x) ? c : 0;
+            }
+            atomicAdd(&seen[e], total);
+            atomicAdd(&before[e], front);
+        }
+        __syncthreads();
+    }
     // prefix sums over the experts, EX_BLOCK of them at a time
     uint32_t carry = 0;
     for (int e0 = 0; e0 < experts; e0 += EX_BLOCK) {
         const int e = e0 + tid;
-        uint32_t total = 0, before = 0;
-        if (e < experts) {
-            if (counts == nullptr) {
-                total = seen[e];
-            } else {
-                for (int i = 0; i < t.tiles; ++i) {
-                    const uint32_t c = counts[int64_t(i) * experts + e];
-                    total += c;
-                    before += i < int(blockIdx.x) ? c : 0;
-                }
-            }
-        }
+        const uint32_t total = e < experts ? seen[e] : 0, front = e < experts && counts != nullptr ? before[e] : 0;
         const uint32_t incl = wave_inclusive_scan<SumU32>(total);
         if (lane == 63)
             wave_total[wave] = incl;
@@ -102,7 +119,7 @@ __global__ __launch_bounds__(EX_BLOCK) void experts_place_kernel(const I* ids, E
             carry += wave_total[w];
         }
         if (e < experts) {
-            base[e] = first + incl - total + before;
+            base[e] = first + incl - total + front;
             if (blockIdx.x == 0)
                 offsets[e] = first + incl - total;
         }
@@ -183,7 +200,7 @@ static hipError_t experts_sort_of(const I* ids, int64_t pairs, int experts, int6
     const size_t row = size_t(experts + 1) * 4;
     if (counts != nullptr)
         experts_count_kernel<I><<<dim3(t.tiles), dim3(EX_BLOCK), row, stream>>>(ids, t, experts, counts);
-    experts_place_kernel<I><<<dim3(t.tiles), dim3(EX_BLOCK), row * (1 + EX_WAVES), stream>>>(
+    experts_place_kernel<I><<<dim3(t.tiles), dim3(EX_BLOCK), row * (2 + EX_WAVES), stream>>>(
         ids, t, experts, bits, counts, offsets, order, places);
     return hipGetLastError();
 }

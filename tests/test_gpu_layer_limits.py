@@ -1,0 +1,221 @@
+"""The gated recurrence and the experts' calls at their limits: waits that run out, graphs that share a
+stream, host threads, indexes past 32 bits, more sequences and tokens than one launch holds."""
+import ctypes
+import os
+import threading
+
+import pytest
+import torch
+
+import prefix_scan_stream_amd as ps
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+SPIN = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "prefix_scan_stream_amd", "libscan_spin1.so")
+
+
+def rand(*shape, seed=0, dtype=torch.bfloat16):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(*shape, device=DEV, generator=g).to(dtype)
+
+
+def test_waits_that_run_out_are_reported():
+    """libscan_spin1.so ends every wait at its first empty poll: a call of many tiles says so, stays inside its
+    buffers, and the workspace is good again once it is initialised."""
+    if not os.path.exists(SPIN):
+        pytest.fail(f"{SPIN} is missing: run __graft_entry__.build() first")
+    normal = ps.load_library()
+    spin = ctypes.CDLL(SPIN)
+    for name in ("gated_recurrence", "gated_recurrence_backward", "ls_recurrence_workspace_bytes", "ls_workspace_init", "ls_workspace_check"):
+        getattr(spin, name).argtypes = getattr(normal, name).argtypes
+    length, d = 30000, 64
+    x, gate = rand(1, length, d), rand(1, length, d, seed=1)
+    want, last = ps.gated_recurrence(x, gate)
+    size = ctypes.c_size_t(0)
+    assert normal.ls_recurrence_workspace_bytes(1, length, d, 0, 2, ctypes.byref(size)) == 0 and size.value > 256
+    ws = torch.empty(size.value + 256, dtype=torch.uint8, device=DEV)
+    ws[size.value:] = 77
+    stream = torch.cuda.current_stream(DEV).cuda_stream
+    guarded = torch.full((length + 2, d), 5.0, dtype=torch.bfloat16, device=DEV)
+    out, state = guarded[1:-1], torch.full((3, d), 5.0, device=DEV)
+    flags = ctypes.c_uint32(0)
+    n = (size.value + 15) // 16 * 16
+
+    def call(lib):
+        assert lib.gated_recurrence(x.data_ptr(), length * d, d, gate.data_ptr(), length * d, d, out.data_ptr(), length * d, d,
+                                    None, d, state[1].data_ptr(), d, None, None, 1, length, d, 2, 2, ws.data_ptr(), size.value,
+                                    stream) == 0
+        return lib.ls_workspace_check(ws.data_ptr(), ctypes.byref(flags), stream)
+
+    assert normal.ls_workspace_init(ws.data_ptr(), n, stream) == 0
+    assert call(spin) == ps.LS_ERR_INCOMPLETE and flags.value == 1
+    assert bool((guarded[0] == 5.0).all()) and bool((guarded[-1] == 5.0).all()) and bool((ws[n:] == 77).all())
+    assert bool((state[0] == 5.0).all()) and bool((state[2] == 5.0).all())
+    assert normal.ls_workspace_init(ws.data_ptr(), n, stream) == 0
+    for _ in range(3):
+        assert call(normal) == ps.LS_OK and flags.value == 0
+        assert torch.equal(out, want[0]) and torch.equal(state[1], last[0])
+
+
+def work_of(size, seed):
+    x, gate = rand(2, size, 192, seed=seed), rand(2, size, 192, seed=seed + 1)
+    packed = torch.tensor([0, size // 3, size // 3, size], device=DEV)
+    experts = torch.randint(-1, 30, (size, 4), device=DEV, generator=torch.Generator(device=DEV).manual_seed(seed))
+    state = rand(2, 192, seed=seed + 2, dtype=torch.float32)
+
+    def work():
+        c = ps.recurrence_carries(x)
+        out, last = ps.gated_recurrence(x, gate, state=state, carries=c)
+        back = ps.gated_recurrence_backward(out, x, gate, c, state=state)
+        return [out, last, *back, ps.gated_recurrence(x[0], gate[0], offsets=packed)[0], *ps.experts_sort(experts, 30)]
+    return work
+
+
+def test_graphs_in_any_order():
+    works = [work_of(size, 10 * size) for size in (3000, 1700, 2500)]
+    wants = [[v.clone() for v in w()] for w in works]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        works[0]()
+    torch.cuda.synchronize()
+    graphs = []
+    for w in works:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            kept = w()
+        graphs.append((graph, kept))
+    for turn in ((0, 1, 2), (2, 0, 0, 1), (1, 1, 2, 0)):
+        for i in turn:
+            for v in graphs[i][1]:
+                v.zero_()
+            graphs[i][0].replay()
+            with torch.cuda.stream(side):
+                eager = works[(i + 1) % 3]()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(graphs[i][1], wants[i]))
+            assert all(torch.equal(a, b) for a, b in zip(eager, wants[(i + 1) % 3]))
+    # beside each other, on streams of their own
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for (graph, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, kept), want in zip(graphs, wants):
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+def test_threads_on_one_stream():
+    works = [work_of(size, size) for size in (2000, 900, 1500, 40)]
+    wants = [[v.clone() for v in w()] for w in works]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def go(i):
+        for _ in range(15):
+            got = works[i]()
+            torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, wants[i])):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=go, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_more_chains_than_blocks_on_three_streams():
+    """More blocks that wait than the GPU holds, from calls beside each other: all of them end."""
+    data = [(rand(40, 400, 768, seed=i), rand(40, 400, 768, seed=9 + i)) for i in range(3)]
+    wants = [ps.gated_recurrence(x, g)[0].clone() for x, g in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    for _ in range(6):
+        got = []
+        for s, (x, g) in zip(streams, data):
+            with torch.cuda.stream(s):
+                got.append(ps.gated_recurrence(x, g)[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, wants))
+    assert all(ps.workspace_error_flags(DEV, s) == 0 for s in streams)
+
+
+def test_elements_past_32_bits():
+    """A sequence of more than 2^31 elements: its end is as of the last 4000 tokens alone (decays below 0.9
+    leave nothing of what was before them after 1000: 0.9^1000 < 2^-150), and so are the gradients at its start."""
+    d, length = 2048, (1 << 20) + 3000
+    x = torch.empty(1, length, d, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, length, 1 << 17):
+        x[:, r:r + (1 << 17)] = rand(1, min(1 << 17, length - r), d, seed=r)
+    gate = x.clamp_max(2.0)
+    c = ps.recurrence_carries(x)
+    out, last = ps.gated_recurrence(x, gate, carries=c)
+    tail, tail_last = ps.gated_recurrence(x[:, -4032:], gate[:, -4032:])
+    assert torch.allclose(out[:, -2000:].float(), tail[:, -2000:].float(), rtol=2.0**-7, atol=1e-5)
+    assert torch.allclose(last, tail_last, rtol=1e-5, atol=1e-6)
+    dx, dg, ds = ps.gated_recurrence_backward(out, x, gate, c)
+    hc = ps.recurrence_carries(x[:, :4000])
+    ps.gated_recurrence(x[:, :4000], gate[:, :4000], carries=hc)
+    hx, hg, hs = ps.gated_recurrence_backward(out[:, :4000], x[:, :4000], gate[:, :4000], hc)
+    for a, b in ((dx, hx), (dg, hg)):
+        assert torch.allclose(a[:, :2000].float(), b[:, :2000].float(), rtol=2.0**-7, atol=1e-5)
+    assert torch.allclose(ds, hs, rtol=1e-5, atol=1e-6)
+    assert bool(torch.isfinite(dx[:, -1]).all()) and ps.workspace_error_flags(DEV) == 0
+
+
+def test_rows_past_32_bits():
+    tokens, top, d = 150000, 4, 4096
+    assert tokens * top * d > 1 << 31
+    x = rand(tokens, d)
+    experts = torch.randint(0, 64, (tokens, top), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    offsets, order, places = ps.experts_sort(experts, 64)
+    rows = ps.experts_gather(x, places)
+    some = torch.cat([torch.arange(0, tokens * top, 997, device=DEV), torch.arange(tokens * top - 5, tokens * top, device=DEV)])
+    assert torch.equal(rows[some], x[order[some].long() // top])
+    weights = torch.rand(tokens, top, device=DEV)
+    out = ps.experts_combine(rows, places, weights)
+    at = some[some < tokens]
+    want = x[at].double() * weights[at].double().sum(1, keepdim=True)
+    # the four products are of one value each: three additions and a rounding
+    assert bool(((out[at].double() - want).abs() <= want.abs() * (2.0**-8 + 2.0**-20) + 1e-30).all())
+    drows, dweights = ps.experts_combine_backward(x, rows, places, weights, drows=rows.clone())
+    p = order[some].long()
+    want = x[p // top].double() * weights.reshape(-1)[p].double()[:, None]
+    assert bool(((drows[some].double() - want).abs() <= want.abs() * (2.0**-8 + 2.0**-20) + 1e-30).all())
+    want = (x[at].double() ** 2).sum(1, keepdim=True).expand(-1, top)
+    assert bool(((dweights[at].double() - want).abs() <= want * d * 2.0**-24).all())
+
+
+def test_more_sequences_than_a_launch_holds():
+    batch = (1 << 22) + 1001
+    x, gate = rand(batch, 2, 2), rand(batch, 2, 2, seed=1)
+    state = rand(batch, 2, seed=2, dtype=torch.float32)
+    c = ps.recurrence_carries(x)
+    out, last = ps.gated_recurrence(x, gate, state=state, carries=c)
+    dx, dg, ds = ps.gated_recurrence_backward(x, x, gate, c, state=state)
+    xs, a = x.double(), torch.sigmoid(gate.double())
+    h0 = state.double()
+    h1 = a[:, 0] * h0 + (1 - a[:, 0]) * xs[:, 0]
+    h2 = a[:, 1] * h1 + (1 - a[:, 1]) * xs[:, 1]
+    l2 = xs[:, 1]
+    l1 = xs[:, 0] + a[:, 1] * l2
+    near = lambda got, want: bool(((got.double() - want).abs() <= want.abs() * 2.0**-8 + 1e-5).all())
+    assert near(out[:, 0], h1) and near(out[:, 1], h2) and near(last, h2)
+    assert near(dx[:, 1], l2 * (1 - a[:, 1])) and near(dx[:, 0], l1 * (1 - a[:, 0])) and near(ds, l1 * a[:, 0])
+    assert near(dg[:, 1], l2 * (h1 - xs[:, 1]) * a[:, 1] * (1 - a[:, 1]))
+
+
+def test_more_tokens_than_blocks():
+    tokens = (1 << 25) + 77  # 32 tokens of 8 channels a block, 2^20 blocks
+    x = torch.arange(tokens, device=DEV, dtype=torch.int32)[:, None].expand(tokens, 8).to(torch.bfloat16)
+    places = torch.arange(tokens - 1, -1, -1, device=DEV, dtype=torch.int32)[:, None]
+    rows = ps.experts_gather(x, places)
+    assert torch.equal(rows, x.flip(0))
+    back = ps.experts_combine(rows, places)
+    assert torch.equal(back, x)
+    weights = torch.full((tokens, 1), 2.0, device=DEV)
+    drows, dw = ps.experts_combine_backward(torch.ones_like(x), rows, places, weights)
+    assert bool((drows == 2.0).all()) and torch.equal(dw[:, 0], 8 * x[:, 0].float())
