@@ -198,29 +198,49 @@ __device__ __forceinline__ int64_t sequence_of_row(const int64_t* offsets, int64
     return lo;
 }
 
-// For each row of the tile the sequence that starts there and the one that ends there, or -1.
-// Offsets out of order mark wrong rows, never ones outside the tile.
-__device__ __forceinline__ void mark_rows(const int64_t* offsets, int64_t sequences, int64_t row0, int rows, int (&heads)[RC_TILE],
-                                          int (&ends)[RC_TILE], int lane)
-{
-    const int tid = threadIdx.x, threads = blockDim.x;
-    for (int i = tid; i < rows; i += threads)
-        heads[i] = ends[i] = -1;
-    const int64_t first = sequence_of_row(offsets, sequences, row0, lane);
-    __syncthreads();
-    for (int64_t s = first + tid; s < sequences; s += threads) {
-        const int64_t from = offsets[s], to = offsets[s + 1];
-        if (from >= row0 + rows)
-            break;
-        if (to > from) {
-            if (from >= row0)
-                heads[from - row0] = int(s);
-            if (to > row0 && to <= row0 + rows)
-                ends[to - 1 - row0] = int(s);
+// For each row of a tile the sequence that starts there and the one that ends there, or -1.  Where the block has a
+// thread for each sequence, its offsets are on their way before the tile is known; with more sequences they are searched
+// for the tile's first.  Offsets out of order mark wrong rows, never ones outside the tile.
+struct RowMarks {
+    int64_t from, to;
+    __device__ __forceinline__ RowMarks(const int64_t* offsets, int64_t sequences, int (&heads)[RC_TILE], int (&ends)[RC_TILE])
+        : from(0), to(0)
+    {
+        if (threadIdx.x < sequences) {
+            from = offsets[threadIdx.x];
+            to = offsets[threadIdx.x + 1];
+        }
+        for (int i = threadIdx.x; i < RC_TILE; i += blockDim.x)
+            heads[i] = ends[i] = -1;
+    }
+    // Between two barriers.
+    __device__ __forceinline__ void mark(const int64_t* offsets, int64_t sequences, int64_t row0, int rows, int (&heads)[RC_TILE],
+                                         int (&ends)[RC_TILE], int lane)
+    {
+        const int tid = threadIdx.x, threads = blockDim.x;
+        int64_t s = tid;
+        if (sequences > threads) {
+            s += sequence_of_row(offsets, sequences, row0, lane);
+            if (s < sequences) {
+                from = offsets[s];
+                to = offsets[s + 1];
+            }
+        }
+        while (s < sequences && from < row0 + rows) {
+            if (to > from) {
+                if (from >= row0)
+                    heads[from - row0] = int(s);
+                if (to > row0 && to <= row0 + rows)
+                    ends[to - 1 - row0] = int(s);
+            }
+            s += threads;
+            if (s < sequences) {
+                from = offsets[s];
+                to = offsets[s + 1];
+            }
         }
     }
-    __syncthreads();
-}
+};
 
 // ---------------------------------------------------------------- maps
 
@@ -304,9 +324,7 @@ struct Chain {
     // The block's place, in the order blocks start; `most`: the workspace is not as it should be.
     __device__ __forceinline__ int64_t take_place(uint32_t& shared) const
     {
-        if (most == 1)
-            return 0;
-        if (threadIdx.x == 0) {
+        if (most > 1 && threadIdx.x == 0) {
             const uint32_t t = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             if (int64_t(t) == most - 1)
                 __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -315,6 +333,8 @@ struct Chain {
             shared = t;
         }
         __syncthreads();
+        if (most == 1)
+            return 0;
         const int64_t t = uint32_t(__builtin_amdgcn_readfirstlane(shared));
         return t < most ? t : most;
     }
@@ -583,7 +603,14 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForwa
         links.places = w.places;
         if (threadIdx.x == 0)
             parts.arrived = 0;
-        place = links.take_place(place_shared);
+        if constexpr (PACKED) {
+            RowMarks marks(q.offsets, q.sequences, head_seq, end_seq);
+            place = links.take_place(place_shared);
+            marks.mark(q.offsets, q.sequences, place << w.tile_shift, w.tile_rows, head_seq, end_seq, lane);
+            __syncthreads();
+        } else {
+            place = links.take_place(place_shared);
+        }
     }
     // what is in front of the sequence; of a block that walks, of its next tile
     float carry[CPL] = {};
@@ -620,7 +647,6 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForwa
         uint32_t heads = 0, ends = 0;
         int hs = -1, es = -1;
         if constexpr (PACKED) {
-            mark_rows(q.offsets, q.sequences, row0, w.tile_rows, head_seq, end_seq, lane);
             hs = head_seq[wave * ROWS + lane % ROWS];
             es = end_seq[wave * ROWS + lane % ROWS];
             heads = uint32_t(__ballot(lane < ROWS && hs >= 0));
@@ -799,7 +825,14 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBack
         links.places = w.places;
         if (threadIdx.x == 0)
             parts.arrived = 0;
-        place = links.take_place(place_shared);
+        if constexpr (PACKED) {
+            RowMarks marks(q.offsets, q.sequences, head_seq, end_seq);
+            place = links.take_place(place_shared);
+            marks.mark(q.offsets, q.sequences, first_row(place), w.tile_rows, head_seq, end_seq, lane);
+            __syncthreads();
+        } else {
+            place = links.take_place(place_shared);
+        }
     }
     float mu_carry[CPL] = {};
     if (!PACKED && q.dstate_out != nullptr && place < RC_GROUP)  // the first group's front
@@ -821,7 +854,6 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBack
         uint32_t heads = 0, ends = 0;
         int hs = -1, es = -1;
         if constexpr (PACKED) {
-            mark_rows(q.offsets, q.sequences, row0, w.tile_rows, head_seq, end_seq, lane);
             hs = head_seq[wave * ROWS + lane % ROWS];
             es = end_seq[wave * ROWS + lane % ROWS];
             heads = uint32_t(__ballot(lane < ROWS && hs >= 0));
