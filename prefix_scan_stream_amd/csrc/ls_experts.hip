@@ -291,7 +291,7 @@ __device__ __forceinline__ int64_t first_token()
     return int64_t(blockIdx.x) * blockDim.y + y;
 }
 
-template <class E, int VEC, bool WAVE>
+template <class E, int VEC, bool WAVE, bool PAST>
 __global__ __launch_bounds__(256) void experts_gather_kernel(ExpertsRows q)
 {
     const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * VEC;
@@ -307,13 +307,13 @@ __global__ __launch_bounds__(256) void experts_gather_kernel(ExpertsRows q)
 #pragma unroll
             for (int i = 0; i < EX_FLIGHT; ++i)
                 if (at[i] >= 0)
-                    v.store(static_cast<char*>(q.rows_out) + (at[i] * q.rows_out_row + c) * E::size);
+                    v.template store<PAST>(static_cast<char*>(q.rows_out) + (at[i] * q.rows_out_row + c) * E::size);
         }
     }
 }
 
 // N rows at once, as many as a token has or EX_FLIGHT: with 8 for every call, 4096 tokens of 2 rows took 76 us against 65.
-template <class E, int VEC, int N, bool WAVE, bool ONCE>
+template <class E, int VEC, int N, bool WAVE, bool ONCE, bool PAST>
 __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsRows q)
 {
     const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * VEC;
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsRows q)
         }
         Elements<E, VEC> o;
         o.set(sum);
-        o.template store<ONCE>(static_cast<char*>(q.out) + (t * q.out_row + c) * E::size);
+        o.template store<PAST>(static_cast<char*>(q.out) + (t * q.out_row + c) * E::size);
     }
 }
 
@@ -364,32 +364,33 @@ __device__ __forceinline__ void store_weight(void* weights, int type, int64_t p,
 
 // The lanes of a token go over its channels together, so that its rows are read and written in long pieces (a
 // wave a token, 1 KiB of each row at a time, took 241 us for 16384 tokens of 8 rows of 2048 bfloat16, and left most of
-// the GPU idle with few tokens).
-template <class E, int VEC, bool WAVE, bool ONCE>
+// the GPU idle with few tokens; 128 lanes take 247 us for 8192 of 8 rows of 4096 against 230).  N as above: with 8 for every call,
+// 16384 tokens of 2 rows of 2048 took 105 us against 60; with 4 for 8 rows of 4096, 240 against 230.
+template <class E, int VEC, int N, bool WAVE, bool ONCE, bool PAST>
 __global__ __launch_bounds__(256) void experts_combine_backward_kernel(ExpertsRows q)
 {
-    __shared__ float part[EX_FLIGHT][4];  // of each wave
+    __shared__ float part[N][4];  // of each wave
     const int x = blockDim.x, y = blockDim.y, tx = threadIdx.x;
     const int ty = WAVE ? __builtin_amdgcn_readfirstlane(int(threadIdx.y)) : int(threadIdx.y);
     const int wave = (ty * x + tx) >> 6, waves = x > 64 ? x / 64 : 1;  // (of a token)
     for (int64_t t0 = int64_t(blockIdx.x) * y; t0 < q.tokens; t0 += int64_t(gridDim.x) * y) {
         const int64_t t = t0 + ty;
         const bool live = t < q.tokens;
-        for (int j0 = 0; j0 < q.top; j0 += EX_FLIGHT) {
-            float dot[EX_FLIGHT] = {}, w[EX_FLIGHT];
-            int64_t at[EX_FLIGHT];
+        for (int j0 = 0; j0 < q.top; j0 += N) {
+            float dot[N] = {}, w[N];
+            int64_t at[N];
             pairs_of(q, live ? t : q.tokens - 1, j0, at, w);
             for (int64_t c = int64_t(tx) * VEC; live && c < q.channels; c += int64_t(x) * VEC) {
-                Elements<E, VEC> d, v[EX_FLIGHT];
+                Elements<E, VEC> d, v[N];
                 d.template load<ONCE>(static_cast<const char*>(q.x) + (t * q.x_row + c) * E::size);
 #pragma unroll
-                for (int i = 0; i < EX_FLIGHT; ++i)
+                for (int i = 0; i < N; ++i)
                     if (at[i] >= 0)
                         v[i].template load<ONCE>(static_cast<const char*>(q.rows) + (at[i] * q.rows_row + c) * E::size);
                 float df[VEC];
                 d.get(df);
 #pragma unroll
-                for (int i = 0; i < EX_FLIGHT; ++i)
+                for (int i = 0; i < N; ++i)
                     if (at[i] >= 0) {
                         float f[VEC], g[VEC];
                         v[i].get(f);
@@ -399,22 +400,22 @@ __global__ __launch_bounds__(256) void experts_combine_backward_kernel(ExpertsRo
                             g[k] = w[i] * df[k];
                         }
                         v[i].set(g);
-                        v[i].store(static_cast<char*>(q.rows_out) + (at[i] * q.rows_out_row + c) * E::size);
+                        v[i].template store<PAST>(static_cast<char*>(q.rows_out) + (at[i] * q.rows_out_row + c) * E::size);
                     }
             }
             const int lanes = x < 64 ? x : 64;
 #pragma unroll
-            for (int i = 0; i < EX_FLIGHT; ++i)
+            for (int i = 0; i < N; ++i)
                 dot[i] = sum_of_lanes(dot[i], lanes);
             if (waves > 1) {
                 if ((tx & 63) == 0) {
 #pragma unroll
-                    for (int i = 0; i < EX_FLIGHT; ++i)
+                    for (int i = 0; i < N; ++i)
                         part[i][wave] = dot[i];
                 }
                 __syncthreads();
 #pragma unroll
-                for (int i = 0; i < EX_FLIGHT; ++i) {
+                for (int i = 0; i < N; ++i) {
                     dot[i] = 0.0f;
                     for (int k = 0; k < waves; ++k)
                         dot[i] += part[i][ty * waves + k];
@@ -423,7 +424,7 @@ __global__ __launch_bounds__(256) void experts_combine_backward_kernel(ExpertsRo
             }
             if (live && tx == 0) {
 #pragma unroll
-                for (int i = 0; i < EX_FLIGHT; ++i)
+                for (int i = 0; i < N; ++i)
                     if (j0 + i < q.top)
                         store_weight(q.dweights, q.weight_type, t * q.top + j0 + i, at[i] >= 0 ? dot[i] : 0.0f);
             }
@@ -441,20 +442,68 @@ static bool wide_rows(const ExpertsRows& q, int size)
            q.rows_out_row % vec == 0;
 }
 
-// Rows that are read once and are too many to be in the caches still are loaded past them: 8192 tokens of 8 rows of 4096
-// bfloat16 are combined in 100 us against 120.  Rows shorter than 1 KiB gain nothing, and few rows, that the experts'
-// product has just written, lose (32 tokens' gradients 16.6 us against 11.9).
-constexpr int64_t EX_ONCE_ROW = 1024, EX_ONCE_ALL = 64 << 20;
+// How many rows a call moves decides how they pass the caches.
+//   once: rows that are read once and are too many to be in the second-level caches still are loaded past them: 8192 tokens of 8
+//     rows of 4096 bfloat16 are combined in 100 us against 120.  Rows shorter than 1 KiB gain nothing, and few rows, that the
+//     experts' product has just written, lose (32 tokens' gradients 16.6 us against 11.9).
+//   past: where the rows fill the memory-side cache, 256 MiB, a call writes past the caches, too.  Gather, and gather and
+//     a product of all rows that follows it: 8192 tokens of 8 rows of 4096 bfloat16 101 and 268 us against 113 and 297, of 4
+//     rows 55 and 144 against 68 and 156; the gradient 119 and 196 against 127 and 206.  Fewer rows the product finds in
+//     that cache: 2560 tokens of 8 rows of 2048, 17 and 53 against 17 and 50, the gradient 41 and 78 against 38 and 68.
+//     Sums, and sums and an addition to them: 8192 tokens of 8 rows of 4096 104 and 141 against 108 and 145; 4096 of 8 rows
+//     of 2048, 26 and 37 against 28 and 36.
+constexpr int64_t EX_ONCE_ROW = 1024, EX_ONCE_ALL = 64 << 20, EX_PAST_ALL = 256 << 20;
+struct Caching {
+    bool wave, once, past;  // a wave has one token; past: also once
+};
+
+template <class E, int VEC>
+static void gather_of(const ExpertsRows& q, const RowGrid& g, const Caching& how, hipStream_t stream)
+{
+    if constexpr (VEC > 1)
+        if (how.past) {
+            experts_gather_kernel<E, VEC, true, true><<<g.grid, g.block, 0, stream>>>(q);
+            return;
+        }
+    if (how.wave)
+        experts_gather_kernel<E, VEC, true, false><<<g.grid, g.block, 0, stream>>>(q);
+    else
+        experts_gather_kernel<E, VEC, false, false><<<g.grid, g.block, 0, stream>>>(q);
+}
 
 template <class E, int VEC, int N>
-static void combine_of(const ExpertsRows& q, const RowGrid& g, bool wave, bool once, hipStream_t stream)
+static void combine_of(const ExpertsRows& q, const RowGrid& g, const Caching& how, hipStream_t stream)
 {
-    if (once)
-        experts_combine_kernel<E, VEC, N, true, true><<<g.grid, g.block, 0, stream>>>(q);
-    else if (wave)
-        experts_combine_kernel<E, VEC, N, true, false><<<g.grid, g.block, 0, stream>>>(q);
+    if constexpr (VEC > 1)
+        if (how.once) {
+            if (how.past)
+                experts_combine_kernel<E, VEC, N, true, true, true><<<g.grid, g.block, 0, stream>>>(q);
+            else
+                experts_combine_kernel<E, VEC, N, true, true, false><<<g.grid, g.block, 0, stream>>>(q);
+            return;
+        }
+    if (how.wave)
+        experts_combine_kernel<E, VEC, N, true, false, false><<<g.grid, g.block, 0, stream>>>(q);
     else
-        experts_combine_kernel<E, VEC, N, false, false><<<g.grid, g.block, 0, stream>>>(q);
+        experts_combine_kernel<E, VEC, N, false, false, false><<<g.grid, g.block, 0, stream>>>(q);
+}
+
+template <class E, int VEC, int N>
+static void combine_backward_of(const ExpertsRows& q, const RowGrid& g, const Caching& how, hipStream_t stream)
+{
+    const dim3 grid(g.grid.x);  // a block's lanes go over all channels
+    if constexpr (VEC > 1)
+        if (how.once) {
+            if (how.past)
+                experts_combine_backward_kernel<E, VEC, N, true, true, true><<<grid, g.block, 0, stream>>>(q);
+            else
+                experts_combine_backward_kernel<E, VEC, N, true, true, false><<<grid, g.block, 0, stream>>>(q);
+            return;
+        }
+    if (how.wave)
+        experts_combine_backward_kernel<E, VEC, N, true, false, false><<<grid, g.block, 0, stream>>>(q);
+    else
+        experts_combine_backward_kernel<E, VEC, N, false, false, false><<<grid, g.block, 0, stream>>>(q);
 }
 
 template <class E, int VEC>
@@ -462,27 +511,23 @@ static hipError_t rows_of(const ExpertsRows& q, ExpertsMove move, hipStream_t st
 {
     const int64_t parts = (q.channels + VEC - 1) / VEC;
     const RowGrid g = row_grid(q.tokens, parts, 256);
-    const bool wave = g.block.x >= 64;
-    const bool once = VEC > 1 && q.channels * E::size >= EX_ONCE_ROW && q.tokens * q.top * q.channels * E::size >= EX_ONCE_ALL;
-    if (move == EXPERTS_GATHER && wave)
-        experts_gather_kernel<E, VEC, true><<<g.grid, g.block, 0, stream>>>(q);
-    else if (move == EXPERTS_GATHER)
-        experts_gather_kernel<E, VEC, false><<<g.grid, g.block, 0, stream>>>(q);
+    const int64_t row = q.channels * E::size, all = q.tokens * q.top * row;
+    const bool wide = VEC > 1 && row >= EX_ONCE_ROW;
+    const Caching how{g.block.x >= 64, wide && all >= EX_ONCE_ALL, wide && all >= EX_PAST_ALL};
+    if (move == EXPERTS_GATHER)
+        gather_of<E, VEC>(q, g, how, stream);
     else if (move == EXPERTS_COMBINE && q.top <= 2)
-        combine_of<E, VEC, 2>(q, g, wave, once, stream);
+        combine_of<E, VEC, 2>(q, g, how, stream);
     else if (move == EXPERTS_COMBINE && q.top <= 4)
-        combine_of<E, VEC, 4>(q, g, wave, once, stream);
+        combine_of<E, VEC, 4>(q, g, how, stream);
     else if (move == EXPERTS_COMBINE)
-        combine_of<E, VEC, EX_FLIGHT>(q, g, wave, once, stream);
-    else {
-        const dim3 grid(g.grid.x);  // a block's lanes go over all channels
-        if (once)
-            experts_combine_backward_kernel<E, VEC, true, true><<<grid, g.block, 0, stream>>>(q);
-        else if (wave)
-            experts_combine_backward_kernel<E, VEC, true, false><<<grid, g.block, 0, stream>>>(q);
-        else
-            experts_combine_backward_kernel<E, VEC, false, false><<<grid, g.block, 0, stream>>>(q);
-    }
+        combine_of<E, VEC, EX_FLIGHT>(q, g, how, stream);
+    else if (q.top <= 2)
+        combine_backward_of<E, VEC, 2>(q, g, how, stream);
+    else if (q.top <= 4)
+        combine_backward_of<E, VEC, 4>(q, g, how, stream);
+    else
+        combine_backward_of<E, VEC, EX_FLIGHT>(q, g, how, stream);
     return hipGetLastError();
 }
 

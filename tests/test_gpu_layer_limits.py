@@ -219,3 +219,49 @@ def test_more_tokens_than_blocks():
     weights = torch.full((tokens, 1), 2.0, device=DEV)
     drows, dw = ps.experts_combine_backward(torch.ones_like(x), rows, places, weights)
     assert bool((drows == 2.0).all()) and torch.equal(dw[:, 0], 8 * x[:, 0].float())
+
+
+@pytest.mark.parametrize("top", [1, 2, 3, 4, 5, 8, 11])
+@pytest.mark.parametrize("mib", [40, 72, 300])
+def test_many_rows(mib, top):
+    """Few rows, more than the near caches hold and more than all caches hold move by different loads and stores,
+    which change no value: the rows and sums of some tokens are those of these tokens alone."""
+    d = 1032
+    tokens = (mib << 20) // (2 * d * top) + 3
+    x, rows = rand(tokens, d), rand(tokens * top, d, seed=1)
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    places = torch.randperm(tokens * top, device=DEV, generator=gen).view(tokens, top).to(torch.int32)
+    places[5::97, 0] = -1
+    weights = torch.rand(tokens, top, device=DEV, generator=gen)
+    some = torch.cat([torch.arange(40, device=DEV), torch.randint(0, tokens, (200,), device=DEV, generator=gen).unique(),
+                      torch.arange(tokens - 40, tokens, device=DEV)]).unique()
+    held = places >= 0
+
+    drows = torch.full_like(rows, 7.0)
+    got = ps.experts_gather(x, places, out=drows)
+    assert torch.equal(got[places[held].long()], x[held.nonzero()[:, 0]])
+    untouched = torch.ones(tokens * top, dtype=torch.bool, device=DEV)
+    untouched[places[held].long()] = False
+    assert bool((got[untouched] == 7.0).all())
+
+    sums = ps.experts_combine(rows, places, weights)
+    assert torch.equal(sums[some], ps.experts_combine(rows, places[some], weights[some]))
+    at = places[some].long().clamp(min=0)
+    w = torch.where(held[some], weights[some], 0).double()
+    parts = rows[at].double() * w[..., None]
+    # a sum of `top` products in float32, rounded to bfloat16
+    bound = parts.abs().sum(1) * (top + 1) * 2.0**-24 + (parts.sum(1).abs() * (1 + 2.0**-20) + 2.0**-133) * 2.0**-8
+    assert bool(((sums[some].double() - parts.sum(1)).abs() <= bound).all())
+
+    drows.fill_(7.0)
+    drows, dweights = ps.experts_combine_backward(x, rows, places, weights, drows=drows)
+    few, few_weights = ps.experts_combine_backward(x[some], rows, places[some], weights[some], drows=torch.full_like(rows, 7.0))
+    named = places[some][held[some]].long()
+    assert torch.equal(drows[named], few[named]) and torch.equal(dweights[some], few_weights)
+    assert bool((drows[untouched] == 7.0).all())
+    exact = (weights[some].double()[..., None] * x[some].double()[:, None])[held[some]]
+    # one product in float32, rounded to bfloat16
+    assert bool(((drows[named].double() - exact).abs() <= exact.abs() * (2.0**-8 + 2.0**-23) + 2.0**-133).all())
+    dots = x[some].double()[:, None] * rows[at].double()
+    wrong = (dweights[some].double() - torch.where(held[some], dots.sum(2), 0)).abs()
+    assert bool((wrong <= dots.abs().sum(2) * (d + 1) * 2.0**-24).all())
