@@ -35,13 +35,15 @@ constexpr int RC_PERIOD = 64;  // a carry is kept of every 64th row
 template <class E, int CPL>
 constexpr bool whole_word = E::size * CPL == 4;
 
-template <class E, int CPL>
+// once: past the caches
+template <class E, int CPL, bool ONCE>
 __device__ __forceinline__ uint32_t load_part(__amdgpu_buffer_rsrc_t rs, uint32_t voff)
 {
+    constexpr int policy = ONCE ? CACHE_NT : 0;
     if constexpr (whole_word<E, CPL>)
-        return __builtin_amdgcn_raw_buffer_load_b32(rs, voff, 0, CACHE_NT);
+        return __builtin_amdgcn_raw_buffer_load_b32(rs, voff, 0, policy);
     else
-        return uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, voff, 0, CACHE_NT));
+        return uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, voff, 0, policy));
 }
 template <class E, int CPL>
 __device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t rs, uint32_t voff, const float (&v)[CPL])
@@ -567,7 +569,7 @@ struct Work {
 
 // ---------------------------------------------------------------- forward
 
-template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED>
+template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED, bool ONCE>
 __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForward q, void* ws)
 {
     constexpr int CH = 64 * CPL;
@@ -591,8 +593,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForwa
         RowWalk wx(x, row, q.x_row * E::size, bytes, n), wg(g, row, q.gate_row * E::size, bytes, n);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j, wx.next(), wg.next()) {
-            rx[j] = load_part<E, CPL>(wx.window(), voff);
-            rg[j] = load_part<E, CPL>(wg.window(), voff);
+            rx[j] = load_part<E, CPL, ONCE>(wx.window(), voff);
+            rg[j] = load_part<E, CPL, ONCE>(wg.window(), voff);
         }
     };
 
@@ -795,7 +797,7 @@ struct alignas(4 * CPL) WaveBack {
     float a[CPL], h[CPL], mu[CPL];
 };
 
-template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED>
+template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED, bool ONCE>
 __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBackward q, void* ws)
 {
     constexpr int CH = 64 * CPL;
@@ -847,9 +849,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBack
             wd(dout, row, q.dout_row * E::size, bytes, have);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j, wx.next(), wg.next(), wd.next()) {
-            rx[j] = load_part<E, CPL>(wx.window(), voff);
-            rg[j] = load_part<E, CPL>(wg.window(), voff);
-            rd[j] = load_part<E, CPL>(wd.window(), voff);
+            rx[j] = load_part<E, CPL, ONCE>(wx.window(), voff);
+            rg[j] = load_part<E, CPL, ONCE>(wg.window(), voff);
+            rd[j] = load_part<E, CPL, ONCE>(wd.window(), voff);
         }
         uint32_t heads = 0, ends = 0;
         int hs = -1, es = -1;
@@ -1158,22 +1160,44 @@ bool multiples(const void* p, int64_t a, int64_t b, int64_t to)
     return reinterpret_cast<uintptr_t>(p) % uintptr_t(to) == 0 && a % to == 0 && b % to == 0;
 }
 
+// x and gate that the memory-side cache (256 MiB) holds beside what the call writes are loaded as usual: it may have them,
+// from the products that made them or from the forward pass.  More are loaded past the caches.  Forward and backward, one after
+// the other on inputs that were not there before, loads as usual and past the caches: x and gate of 128 MiB (4 x 4096 x
+// 2048 bfloat16) 127 and 127 us, the same inputs again 102 and 126; 41 MiB (3 x 1777 x 1001 float32) 48 and 60;
+// 256 MiB 264 and 250; 512 MiB 486 and 453.
+constexpr int64_t RC_ONCE_ALL = 192 << 20;
+template <class Q>
+bool loads_once(const Q& q, int size)
+{
+    return (q.offsets != nullptr ? 1 : q.sequences) * q.rows * q.channels * size * 2 >= RC_ONCE_ALL;
+}
+
 // A launch holds less than 2^32 threads: most sequences of a launch of `groups` blocks each.
 int64_t sequences_at_once(int64_t groups) { return (int64_t(1) << 22) / groups > 0 ? (int64_t(1) << 22) / groups : 1; }
 
-template <class E, int CPL, int GATING>
+template <class E, int CPL, int GATING, bool ONCE>
 hipError_t forward_of(const RecurForward& q, void* ws, hipStream_t stream)
 {
     using S = ForwardShape<CPL>;
     const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, 1);
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
     if (p.chained && q.offsets != nullptr)
-        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, true, true><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, true, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
     else if (p.chained)
-        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, true><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
     else
-        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, false><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, false, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
     return hipGetLastError();
+}
+
+template <class E, int CPL, bool ONCE>
+hipError_t forward_by(const RecurForward& q, void* ws, hipStream_t stream)
+{
+    if (q.gating == GATE_DECAY)
+        return forward_of<E, CPL, GATE_DECAY, ONCE>(q, ws, stream);
+    if (q.gating == GATE_LOG)
+        return forward_of<E, CPL, GATE_LOG, ONCE>(q, ws, stream);
+    return forward_of<E, CPL, GATE_SIGMOID, ONCE>(q, ws, stream);
 }
 
 template <class E, int CPL>
@@ -1195,24 +1219,32 @@ hipError_t launch_forward(const RecurForward& q, void* ws, hipStream_t stream)
         const hipError_t e = launch_forward<E, CPL>(first, ws, stream);
         return e != hipSuccess ? e : launch_forward<E, CPL>(rest, ws, stream);
     }
-    if (q.gating == GATE_DECAY)
-        return forward_of<E, CPL, GATE_DECAY>(q, ws, stream);
-    return q.gating == GATE_LOG ? forward_of<E, CPL, GATE_LOG>(q, ws, stream) : forward_of<E, CPL, GATE_SIGMOID>(q, ws, stream);
+    return loads_once(q, E::size) ? forward_by<E, CPL, true>(q, ws, stream) : forward_by<E, CPL, false>(q, ws, stream);
 }
 
-template <class E, int CPL, int GATING>
+template <class E, int CPL, int GATING, bool ONCE>
 hipError_t backward_of(const RecurBackward& q, void* ws, hipStream_t stream)
 {
     using S = BackwardShape<CPL>;
     const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, RC_PERIOD / S::rows);
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
     if (p.chained && q.offsets != nullptr)
-        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, true, true><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, true, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
     else if (p.chained)
-        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, true><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
     else
-        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, false><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, false, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
     return hipGetLastError();
+}
+
+template <class E, int CPL, bool ONCE>
+hipError_t backward_by(const RecurBackward& q, void* ws, hipStream_t stream)
+{
+    if (q.gating == GATE_DECAY)
+        return backward_of<E, CPL, GATE_DECAY, ONCE>(q, ws, stream);
+    if (q.gating == GATE_LOG)
+        return backward_of<E, CPL, GATE_LOG, ONCE>(q, ws, stream);
+    return backward_of<E, CPL, GATE_SIGMOID, ONCE>(q, ws, stream);
 }
 
 template <class E, int CPL>
@@ -1237,9 +1269,7 @@ hipError_t launch_backward(const RecurBackward& q, void* ws, hipStream_t stream)
         const hipError_t e = launch_backward<E, CPL>(first, ws, stream);
         return e != hipSuccess ? e : launch_backward<E, CPL>(rest, ws, stream);
     }
-    if (q.gating == GATE_DECAY)
-        return backward_of<E, CPL, GATE_DECAY>(q, ws, stream);
-    return q.gating == GATE_LOG ? backward_of<E, CPL, GATE_LOG>(q, ws, stream) : backward_of<E, CPL, GATE_SIGMOID>(q, ws, stream);
+    return loads_once(q, E::size) ? backward_by<E, CPL, true>(q, ws, stream) : backward_by<E, CPL, false>(q, ws, stream);
 }
 
 template <class E>

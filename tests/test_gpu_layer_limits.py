@@ -265,3 +265,31 @@ def test_many_rows(mib, top):
     dots = x[some].double()[:, None] * rows[at].double()
     wrong = (dweights[some].double() - torch.where(held[some], dots.sum(2), 0)).abs()
     assert bool((wrong <= dots.abs().sum(2) * (d + 1) * 2.0**-24).all())
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("gating", ["sigmoid", "log", "decay"])
+@pytest.mark.parametrize("dtype, d", [(torch.float32, 129), (torch.float16, 258), (torch.bfloat16, 259)], ids=str)
+def test_many_tokens(dtype, d, gating, packed):
+    """Tokens that fill the caches are loaded by other loads than fewer, which changes no value: two halves of a
+    call, tile by tile the same work, give what the call gives."""
+    half = -(-(60 << 20) // (2 * d * dtype.itemsize)) // 1024 * 1024 + 1024
+    x, gate, dout = (rand(2, half, d, seed=i, dtype=dtype) for i in range(3))
+    if gating != "sigmoid":
+        gate = torch.sigmoid(gate.float()).to(dtype) if gating == "decay" else -gate.abs()
+    state, dstate = rand(2, d, seed=3, dtype=torch.float32), rand(2, d, seed=4, dtype=torch.float32)
+
+    def call(x, gate, dout, state, dstate):
+        n, offsets = x.shape[0], None
+        if packed:
+            offsets = torch.arange(n + 1, device=DEV) * half
+            x, gate, dout = (t.reshape(-1, d) for t in (x, gate, dout))
+        carries = ps.recurrence_carries(x, offsets)
+        out, last = ps.gated_recurrence(x, gate, state, gating, offsets=offsets, carries=carries)
+        grads = ps.gated_recurrence_backward(dout, x, gate, carries, state=state, dstate_out=dstate, gating=gating, offsets=offsets)
+        return [t.reshape(n, -1) for t in (out, last, *grads)]
+
+    whole = call(x, gate, dout, state, dstate)
+    parts = [call(x[i:i + 1], gate[i:i + 1], dout[i:i + 1], state[i:i + 1], dstate[i:i + 1]) for i in range(2)]
+    for got, *want in zip(whole, *parts):
+        assert torch.equal(got, torch.cat(want)) and bool(torch.isfinite(got).all())
