@@ -87,7 +87,7 @@ extern "C" {
 typedef enum ls_status {
     LS_OK = 0,
     LS_ERR_INVALID_ARG = 1, /* bad size, NULL, alignment, enum value, or overlap */
-    LS_ERR_UNSUPPORTED = 2, /* an operator not defined for the element type (see ls_op) */
+    LS_ERR_UNSUPPORTED = 2, /* an operator not defined for the element type (see ls_op); a recurrence of too many tiles */
     LS_ERR_WORKSPACE = 3,   /* workspace NULL or smaller than the size query returned */
     LS_ERR_HIP = 4,         /* the HIP runtime reported an error when enqueuing */
     LS_ERR_INCOMPLETE = 5   /* ls_workspace_check: a call on the workspace gave up a wait */
@@ -560,10 +560,14 @@ ls_status ls_recurrence_workspace_bytes(int64_t sequences, int64_t rows, int64_t
  *   ws             >= ls_recurrence_workspace_bytes bytes, 16-byte aligned, zero-filled once by
  *                  ls_workspace_init before its first use; each call leaves it ready for the next.
  *                  It serves the two recurrence calls only.  May be NULL where the size is 0.
+ * A call whose sequences are cut into 2^23 or more tiles (64 tokens or more by 64 channels or more each; only rows
+ * of few channels come to that) is refused with LS_ERR_UNSUPPORTED.
+ * A tile waits for the ones in front of it.  A wait that lasts 1 s, which no correct run does, gives up: the outputs
+ * are then incomplete, ls_workspace_check reports it, and the workspace has to be initialised again.
  * Decays of magnitude up to 1 are meant; larger ones work while the products of the decays of
  * any run of tokens stay within float32.  A sequence's infinities and NaN stay its own.
  * Errors: LS_ERR_INVALID_ARG (sizes, strides, NULL, alignment to the element, overlap, enums),
- * LS_ERR_WORKSPACE. */
+ * LS_ERR_WORKSPACE, LS_ERR_UNSUPPORTED. */
 ls_status gated_recurrence(const void *x, int64_t x_sequence_stride, int64_t x_row_stride, const void *gate,
                            int64_t gate_sequence_stride, int64_t gate_row_stride, void *out,
                            int64_t out_sequence_stride, int64_t out_row_stride, const float *state,
@@ -619,7 +623,7 @@ ls_status experts_gather(const void *x, int64_t x_stride, const int32_t *places,
  * out[token] = sum over j of weights[token * top + j] * rows[places[token * top + j]]; zeros for
  * a token without a row.
  *   weights      tokens * top elements of type weight_type, or NULL: ones.  The weight of a
- *                pair without a row is not read.
+ *                pair without a row takes no part.
  * Other arguments as for experts_gather.  Without weights, its gradient is experts_gather. */
 ls_status experts_combine(const void *rows, int64_t rows_stride, const int32_t *places, const void *weights,
                           ls_logits weight_type, void *out, int64_t out_stride, int64_t tokens, int64_t top,

@@ -272,9 +272,9 @@ struct alignas(8 * CPL) WaveMap {
 // one sets its words and the counter back to 0; so does the last place with the chain's
 // counter.  So a call leaves the workspace as it found it: all 0.
 
-constexpr int RC_GROUP = 8;                   // a wave of a block for each
+constexpr int RC_GROUP = 8;                   // a wave of a block for each: the link and one for every map
 constexpr int RC_COUNTER = 32;                // 32-bit words from counter to counter: a line each
-constexpr uint32_t RC_RESTART = 0x7fc0c0deu;  // for a factor: nothing passes (a NaN that no product makes)
+constexpr uint32_t RC_RESTART = 0x7fc0c0deu;  // for a factor: nothing passes (a NaN that no factor is)
 
 struct ChainLayout {
     int64_t chains, most, groups;  // most places of a chain, and its groups
@@ -360,7 +360,8 @@ struct Chain {
     {
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            const uint32_t f = restart ? RC_RESTART : to_bits(a[c]);
+            // (a NaN of a gate's may have these bits)
+            const uint32_t own = to_bits(a[c]) == RC_RESTART ? 0x7fc00000u : to_bits(a[c]), f = restart ? RC_RESTART : own;
             const uint64_t w = (uint64_t(to_bits(h[c])) << 32) | f;
             status_store(maps + place * CH + lane * CPL + c, w == 0 ? 0x80000000ull : w);
         }
@@ -573,6 +574,7 @@ template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool C
 __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForward q, void* ws)
 {
     constexpr int CH = 64 * CPL;
+    static_assert(WAVES >= RC_GROUP && ROWS * WAVES <= RC_TILE, "each map of a group needs a wave");
     __shared__ WaveMap<CPL> maps[CHAINED ? 1 : 2][WAVES][64];
     __shared__ int restart[CHAINED ? 1 : 2][WAVES];
     __shared__ GroupParts<CPL> parts;
@@ -801,6 +803,7 @@ template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool C
 __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBackward q, void* ws)
 {
     constexpr int CH = 64 * CPL;
+    static_assert(WAVES >= RC_GROUP && ROWS * WAVES <= RC_TILE && RC_PERIOD % ROWS == 0, "each map of a group needs a wave");
     __shared__ WaveBack<CPL> maps[CHAINED ? 1 : 2][WAVES][64];
     __shared__ int restart[CHAINED ? 1 : 2][WAVES][2];
     __shared__ GroupParts<CPL> parts;
@@ -1172,7 +1175,10 @@ bool loads_once(const Q& q, int size)
     return (q.offsets != nullptr ? 1 : q.sequences) * q.rows * q.channels * size * 2 >= RC_ONCE_ALL;
 }
 
-// A launch holds less than 2^32 threads: most sequences of a launch of `groups` blocks each.
+// A launch holds less than 2^32 threads.  Of tiles as blocks, 2^23 - 1 of 512 threads: a call of more is refused.
+constexpr int64_t RC_BLOCKS = (int64_t(1) << 23) - 1;
+// Of blocks that walk: most sequences of a launch of `groups` blocks each.  More are halved, so that each half still has chains
+// enough to walk: what a call takes of its workspace goes by all its sequences.
 int64_t sequences_at_once(int64_t groups) { return (int64_t(1) << 22) / groups > 0 ? (int64_t(1) << 22) / groups : 1; }
 
 template <class E, int CPL, int GATING, bool ONCE>
@@ -1180,6 +1186,8 @@ hipError_t forward_of(const RecurForward& q, void* ws, hipStream_t stream)
 {
     using S = ForwardShape<CPL>;
     const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, 1);
+    if (p.chained && p.chains * p.tiles > RC_BLOCKS)
+        return hipErrorInvalidConfiguration;
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
     if (p.chained && q.offsets != nullptr)
         recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, true, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
@@ -1203,19 +1211,20 @@ hipError_t forward_by(const RecurForward& q, void* ws, hipStream_t stream)
 template <class E, int CPL>
 hipError_t launch_forward(const RecurForward& q, void* ws, hipStream_t stream)
 {
-    const int64_t groups = (q.channels + 64 * CPL - 1) / (64 * CPL), most = sequences_at_once(groups);
-    if (q.offsets == nullptr && q.sequences > most) {
+    const int64_t groups = (q.channels + 64 * CPL - 1) / (64 * CPL);
+    if (q.offsets == nullptr && q.sequences > sequences_at_once(groups)) {
+        const int64_t half = q.sequences / 2;
         RecurForward first = q, rest = q;
-        first.sequences = most;
-        rest.sequences -= most;
-        rest.x = static_cast<const char*>(q.x) + most * q.x_sequence * E::size;
-        rest.gate = static_cast<const char*>(q.gate) + most * q.gate_sequence * E::size;
-        rest.out = static_cast<char*>(q.out) + most * q.out_sequence * E::size;
+        first.sequences = half;
+        rest.sequences -= half;
+        rest.x = static_cast<const char*>(q.x) + half * q.x_sequence * E::size;
+        rest.gate = static_cast<const char*>(q.gate) + half * q.gate_sequence * E::size;
+        rest.out = static_cast<char*>(q.out) + half * q.out_sequence * E::size;
         if (q.state != nullptr)
-            rest.state += most * q.state_row;
-        rest.state_out += most * q.state_out_row;
+            rest.state += half * q.state_row;
+        rest.state_out += half * q.state_out_row;
         if (q.carries != nullptr)
-            rest.carries += recur_carry_rows(most, q.rows, false) * q.channels;
+            rest.carries += recur_carry_rows(half, q.rows, false) * q.channels;
         const hipError_t e = launch_forward<E, CPL>(first, ws, stream);
         return e != hipSuccess ? e : launch_forward<E, CPL>(rest, ws, stream);
     }
@@ -1227,6 +1236,8 @@ hipError_t backward_of(const RecurBackward& q, void* ws, hipStream_t stream)
 {
     using S = BackwardShape<CPL>;
     const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, RC_PERIOD / S::rows);
+    if (p.chained && p.chains * p.tiles > RC_BLOCKS)
+        return hipErrorInvalidConfiguration;
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
     if (p.chained && q.offsets != nullptr)
         recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, true, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
@@ -1250,22 +1261,23 @@ hipError_t backward_by(const RecurBackward& q, void* ws, hipStream_t stream)
 template <class E, int CPL>
 hipError_t launch_backward(const RecurBackward& q, void* ws, hipStream_t stream)
 {
-    const int64_t groups = (q.channels + 64 * CPL - 1) / (64 * CPL), most = sequences_at_once(groups);
-    if (q.offsets == nullptr && q.sequences > most) {
+    const int64_t groups = (q.channels + 64 * CPL - 1) / (64 * CPL);
+    if (q.offsets == nullptr && q.sequences > sequences_at_once(groups)) {
+        const int64_t half = q.sequences / 2;
         RecurBackward first = q, rest = q;
-        first.sequences = most;
-        rest.sequences -= most;
-        rest.dout = static_cast<const char*>(q.dout) + most * q.dout_sequence * E::size;
-        rest.x = static_cast<const char*>(q.x) + most * q.x_sequence * E::size;
-        rest.gate = static_cast<const char*>(q.gate) + most * q.gate_sequence * E::size;
-        rest.dx = static_cast<char*>(q.dx) + most * q.dx_sequence * E::size;
-        rest.dgate = static_cast<char*>(q.dgate) + most * q.dgate_sequence * E::size;
+        first.sequences = half;
+        rest.sequences -= half;
+        rest.dout = static_cast<const char*>(q.dout) + half * q.dout_sequence * E::size;
+        rest.x = static_cast<const char*>(q.x) + half * q.x_sequence * E::size;
+        rest.gate = static_cast<const char*>(q.gate) + half * q.gate_sequence * E::size;
+        rest.dx = static_cast<char*>(q.dx) + half * q.dx_sequence * E::size;
+        rest.dgate = static_cast<char*>(q.dgate) + half * q.dgate_sequence * E::size;
         if (q.state != nullptr)
-            rest.state += most * q.state_row;
+            rest.state += half * q.state_row;
         if (q.dstate_out != nullptr)
-            rest.dstate_out += most * q.dstate_out_row;
-        rest.dstate += most * q.dstate_row;
-        rest.carries += recur_carry_rows(most, q.rows, false) * q.channels;
+            rest.dstate_out += half * q.dstate_out_row;
+        rest.dstate += half * q.dstate_row;
+        rest.carries += recur_carry_rows(half, q.rows, false) * q.channels;
         const hipError_t e = launch_backward<E, CPL>(first, ws, stream);
         return e != hipSuccess ? e : launch_backward<E, CPL>(rest, ws, stream);
     }

@@ -208,6 +208,42 @@ def test_more_sequences_than_a_launch_holds():
     assert near(dg[:, 1], l2 * (h1 - xs[:, 1]) * a[:, 1] * (1 - a[:, 1]))
 
 
+@pytest.mark.parametrize("extra", [1, 1001])
+def test_more_long_sequences_than_a_launch_holds(extra):
+    """Sequences of several tiles: those of the second launch walk as the first's do, and take nothing of the
+    workspace, which is none."""
+    batch, length = (1 << 22) + extra, 130
+    x, gate = rand(1, length, 1).expand(batch, -1, -1), rand(1, length, 1, seed=1).expand(batch, -1, -1)
+    size = ctypes.c_size_t(0)
+    assert ps.load_library().ls_recurrence_workspace_bytes(batch, length, 1, 0, 2, ctypes.byref(size)) == 0 and size.value <= 256
+    c = ps.recurrence_carries(x)
+    out, last = ps.gated_recurrence(x, gate, carries=c)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(last, last[:1].expand_as(last))
+    h, want = 0.0, []
+    for xt, gt in zip(x[0, :, 0].double().tolist(), torch.sigmoid(gate[0, :, 0].double()).tolist()):
+        h = gt * h + (1 - gt) * xt
+        want.append(h)
+    want = torch.tensor(want, device=DEV, dtype=torch.float64)
+    # 2^-8 of the rounding to bfloat16, 1e-5 for 130 steps in float32 (values up to 4)
+    assert bool(((out[0, :, 0].double() - want).abs() <= want.abs() * 2.0**-8 + 1e-5).all())
+    dx, dg, ds = ps.gated_recurrence_backward(x, x, gate, c)
+    one = ps.gated_recurrence_backward(x[:512], x[:512], gate[:512], c[: 512 * 3])
+    for got, few in zip((dx, dg, ds), one):
+        assert torch.equal(got, few[:1].expand_as(got))
+
+
+def test_nan_of_any_bits_stays_in_its_channel():
+    """float32 gates may be NaN of any bits, those of the kernels' own marks among them."""
+    length, d = 4000, 64
+    x, gate = rand(1, length, d, dtype=torch.float32), torch.sigmoid(rand(1, length, d, seed=1, dtype=torch.float32))
+    want = ps.gated_recurrence(x, gate, gating="decay")
+    bits = gate.clone().view(torch.int32)
+    bits[0, 500, 0], bits[0, 2500, 0] = 0x7FC0C0DE, 0x7FC0C0DE
+    out, last = ps.gated_recurrence(x, bits.view(torch.float32), gating="decay")
+    assert torch.equal(out[:, :, 1:], want[0][:, :, 1:]) and torch.equal(last[:, 1:], want[1][:, 1:])
+    assert torch.equal(out[0, :500, 0], want[0][0, :500, 0]) and bool(out[0, 500:, 0].isnan().all())
+
+
 def test_more_tokens_than_blocks():
     tokens = (1 << 25) + 77  # 32 tokens of 8 channels a block, 2^20 blocks
     x = torch.arange(tokens, device=DEV, dtype=torch.int32)[:, None].expand(tokens, 8).to(torch.bfloat16)

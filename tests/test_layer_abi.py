@@ -51,6 +51,15 @@ def test_recurrence_refuses(lib, change):
     assert status(lib, "gated_recurrence", RECUR, **change) == INV
 
 
+def test_recurrence_refuses_too_many_tiles(lib):
+    """2^31 - 1 tokens of a channel are 2^24 tiles: more than a launch holds."""
+    many = dict(sequences=1, rows=(1 << 31) - 1, channels=1, x_s=0, x_r=0, g_s=0, g_r=0)
+    for offsets in (None, A[9]):
+        assert status(lib, "gated_recurrence", RECUR, **many, o_s=0, o_r=1, offsets=offsets) == ps.LS_ERR_UNSUPPORTED
+        assert status(lib, "gated_recurrence_backward", BACK, **many, do_s=0, do_r=0, dx=A[10], dx_s=0, dx_r=1, dg=A[11], dg_s=0,
+                      dg_r=1, offsets=offsets) == ps.LS_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("change", SIZES + [
     dict(dout=None), dict(dout=A[6] + 3), dict(x=None), dict(g=None), dict(carries=None), dict(carries=A[4] + 2),
     dict(state=A[2] + 1), dict(dstate_out=A[3] + 2), dict(dx=None), dict(dg=None), dict(dx=A[7] + 2), dict(dstate=None),
