@@ -260,85 +260,97 @@ struct alignas(8 * CPL) WaveMap {
 // does.  (A block that stays to hand values to later places would not do: 256 chains filled the GPU
 // with such blocks, and the later ones never started.)
 //
-// Places form groups of RC_GROUP.  A tile publishes its map, composes those in front of it in its group (each
-// wave fetches one),
-// and applies them to the group's front, the value in front of its first place.  The group's last
-// tile publishes the next group's front.  So a value passes a group with one store and one load,
-// while a tile reads at most RC_GROUP - 1 maps.  A tile with a sequence's start (backward: end)
-// does not depend on what is in front, and maps say so.
+// RC_GROUP places are a group, and groups a stretch.  A tile publishes its map, and a group's last tile the map of its
+// group.  A tile composes the maps of the tiles in front of it in its group and of the groups in front of its own in
+// the stretch (each wave fetches one of either), and applies them to the stretch's front, the value in front of its
+// first place.  The stretch's last tile publishes the next one's front.  So a value passes a stretch with one store and one
+// load, and a tile reads at most 2 (RC_GROUP - 1) maps.  A tile with a sequence's start (backward: end) does not depend on
+// what is in front, and maps say so.
+// A stretch is one group: with few chains, whose tiles are all under way at once, the steps from front to front are what
+// takes the time, and there it is RC_GROUP groups.  65536 tokens of 128, 256, 384, 512, 768 and 2048 bfloat16 channels (128 a
+// chain), forward and backward: one group 49 and 87, 50 and 91, 55 and 98, 58 and 105, 76 and 139, 187 and 345 us; eight 23 and
+// 36, 33 and 57, 43 and 77, 57 and 104, 82 and 150, 207 and 376, as a tile waits once more.
+// Groups of 4, 16 and 32: 512 channels 83 us forward with 4 against 58; 2048 channels 209 and 388 with 16.
 //
 // A word that is 0 is empty; values are made not to be 0 (a zero becomes -0, which shows in
-// nothing but the sign of a zero).  A group counts the tiles that have read all they need, and the last
-// one sets its words and the counter back to 0; so does the last place with the chain's
+// nothing but the sign of a zero).  A group counts the tiles that have read all they need, a stretch its groups, and the last
+// one to sign off sets the words back to 0, the counter too; so does the last place with the chain's
 // counter.  So a call leaves the workspace as it found it: all 0.
 
 constexpr int RC_GROUP = 8;                   // a wave of a block for each: the link and one for every map
+constexpr int RC_GROUP_SHIFT = 3;
+constexpr int64_t RC_FEW = 4;                 // chains up to which a stretch is RC_GROUP groups; of more it is one
 constexpr int RC_COUNTER = 32;                // 32-bit words from counter to counter: a line each
 constexpr uint32_t RC_RESTART = 0x7fc0c0deu;  // for a factor: nothing passes (a NaN that no factor is)
 
+constexpr int chain_levels(int64_t chains) { return chains <= RC_FEW ? 2 : 1; }
+
 struct ChainLayout {
-    int64_t chains, most, groups;  // most places of a chain, and its groups
-    size_t maps, fronts, counts, bytes;  // offsets
+    int64_t chains, most, groups, stretches;  // most places of a chain, its groups and stretches
+    size_t counts, maps, fronts, bytes;       // offsets
 };
-__host__ __device__ inline ChainLayout chain_layout(int64_t chains, int64_t most, int lanes_channels)
+static ChainLayout chain_layout(int64_t chains, int64_t most, int lanes_channels)
 {
     ChainLayout l;
     l.chains = chains;
     l.most = most;
-    l.groups = (most + RC_GROUP - 1) / RC_GROUP;
+    const int stretch_shift = RC_GROUP_SHIFT * chain_levels(chains);
+    l.groups = ((most - 1) >> RC_GROUP_SHIFT) + 1;
+    l.stretches = ((most - 1) >> stretch_shift) + 1;
     l.counts = sizeof(WsHeader) + size_t(chains) * RC_COUNTER * 4;
-    l.maps = l.counts + size_t(chains) * size_t(l.groups) * RC_COUNTER * 4;
-    l.fronts = l.maps + size_t(chains) * size_t(most) * size_t(lanes_channels) * 8;
-    l.bytes = l.fronts + size_t(chains) * size_t(l.groups) * size_t(lanes_channels) * 4;
+    l.maps = l.counts + size_t(chains) * size_t(l.groups) * 2 * RC_COUNTER * 4;
+    l.fronts = l.maps + size_t(chains) * size_t(l.groups) * RC_GROUP * size_t(lanes_channels) * 8;
+    l.bytes = l.fronts + size_t(chains) * size_t(l.stretches) * size_t(lanes_channels) * 4;
     return l;
 }
 
-// What a tile's waves fetch of its group, in LDS; `arrived` starts at 0.
-template <int CPL>
-struct GroupParts {
-    WaveMap<CPL> maps[RC_GROUP - 1][64];
+// What a tile's waves fetch, in LDS: the maps of tiles [0] and of groups [1]; `arrived` starts at 0.
+template <int CPL, int LEVELS>
+struct ChainParts {
+    WaveMap<CPL> maps[LEVELS][RC_GROUP - 1][64];
     float value[CPL][64];  // in front of the tile
-    int restart[RC_GROUP - 1], arrived;
+    int restart[LEVELS][RC_GROUP - 1], arrived[2];
 };
 
-template <int CPL>
+template <int CPL, int LEVELS>
 struct Chain {
     WsHeader* header;
     uint32_t* counter;  // places given out
-    uint32_t* counts;   // of each group: tiles that have read what they need
-    uint64_t* maps;     // [place][64 CPL]: factor | value << 32
-    uint32_t* fronts;   // [group][64 CPL]
-    int64_t most, places;
+    uint32_t* counts;   // of each group: tiles that have read what they need; at a stretch's first also the groups that have
+    uint64_t* maps;     // [place][64 CPL]: factor | value << 32; at a group's last place that of the group
+    uint32_t* fronts;   // [stretch][64 CPL]
+    int most, places;
 
     static constexpr int CH = 64 * CPL;
+    static constexpr int STRETCH = 1 << (RC_GROUP_SHIFT * LEVELS);  // places
 
     __device__ __forceinline__ Chain() {}
     __device__ __forceinline__ Chain(void* ws, const ChainLayout& l, int64_t chain)
-        : header(static_cast<WsHeader*>(ws)), most(l.most), places(l.most)
+        : header(static_cast<WsHeader*>(ws)), most(int(l.most)), places(int(l.most))
     {
         char* p = static_cast<char*>(ws);
         counter = reinterpret_cast<uint32_t*>(p + sizeof(WsHeader)) + chain * RC_COUNTER;
-        counts = reinterpret_cast<uint32_t*>(p + l.counts) + chain * l.groups * RC_COUNTER;
-        maps = reinterpret_cast<uint64_t*>(p + l.maps) + chain * l.most * CH;
-        fronts = reinterpret_cast<uint32_t*>(p + l.fronts) + chain * l.groups * CH;
+        counts = reinterpret_cast<uint32_t*>(p + l.counts) + chain * l.groups * 2 * RC_COUNTER;
+        maps = reinterpret_cast<uint64_t*>(p + l.maps) + chain * l.groups * RC_GROUP * CH;
+        fronts = reinterpret_cast<uint32_t*>(p + l.fronts) + chain * l.stretches * CH;
     }
 
     // The block's place, in the order blocks start; `most`: the workspace is not as it should be.
-    __device__ __forceinline__ int64_t take_place(uint32_t& shared) const
+    __device__ __forceinline__ int take_place(uint32_t& shared) const
     {
         if (most > 1 && threadIdx.x == 0) {
             const uint32_t t = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (int64_t(t) == most - 1)
+            if (t == uint32_t(most) - 1)
                 __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (int64_t(t) >= most)
+            if (t >= uint32_t(most))
                 flag_error(header, WS_ERR_BAD_TICKET);
             shared = t;
         }
         __syncthreads();
         if (most == 1)
             return 0;
-        const int64_t t = uint32_t(__builtin_amdgcn_readfirstlane(shared));
-        return t < most ? t : most;
+        const uint32_t t = uint32_t(__builtin_amdgcn_readfirstlane(shared));
+        return t < uint32_t(most) ? int(t) : most;
     }
 
     // Whether a wait is to end without what it waits for, for the whole wave: it has lasted too long, which is then on
@@ -356,37 +368,37 @@ struct Chain {
         return true;
     }
 
-    __device__ __forceinline__ void publish_map(int64_t place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool restart) const
+    __device__ __forceinline__ void publish_map(uint64_t* p, int lane, const float (&a)[CPL], const float (&h)[CPL], bool restart) const
     {
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             // (a NaN of a gate's may have these bits)
             const uint32_t own = to_bits(a[c]) == RC_RESTART ? 0x7fc00000u : to_bits(a[c]), f = restart ? RC_RESTART : own;
             const uint64_t w = (uint64_t(to_bits(h[c])) << 32) | f;
-            status_store(maps + place * CH + lane * CPL + c, w == 0 ? 0x80000000ull : w);
+            status_store(p + lane * CPL + c, w == 0 ? 0x80000000ull : w);
         }
     }
 
     // Two 32-bit words at once where a lane has two.
-    __device__ __forceinline__ void store_front(int64_t group, int lane, const uint32_t (&w)[CPL]) const
+    __device__ __forceinline__ void store_front(int stretch, int lane, const uint32_t (&w)[CPL]) const
     {
-        uint32_t* p = fronts + group * CH + lane * CPL;
+        uint32_t* p = fronts + int64_t(stretch) * CH + lane * CPL;
         if constexpr (CPL == 2)
             status_store(reinterpret_cast<uint64_t*>(p), (uint64_t(w[1]) << 32) | w[0]);
         else
             __hip_atomic_store(p, w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __device__ __forceinline__ void publish_front(int64_t group, int lane, const float (&h)[CPL]) const
+    __device__ __forceinline__ void publish_front(int stretch, int lane, const float (&h)[CPL]) const
     {
         uint32_t w[CPL];
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
             w[c] = to_bits(h[c]) == 0 ? 0x80000000u : to_bits(h[c]);
-        store_front(group, lane, w);
+        store_front(stretch, lane, w);
     }
-    __device__ __forceinline__ void wait_front(int64_t group, int lane, float (&h)[CPL]) const
+    __device__ __forceinline__ void wait_front(int stretch, int lane, float (&h)[CPL]) const
     {
-        const uint32_t* p = fronts + group * CH + lane * CPL;
+        const uint32_t* p = fronts + int64_t(stretch) * CH + lane * CPL;
         const uint64_t start = wait_start();
         for (;;) {
             bool there;
@@ -406,10 +418,10 @@ struct Chain {
         }
     }
 
-    // The map of a place, once it is there (the whole wave).  Returns whether it restarts.
-    __device__ __forceinline__ bool wait_map(int64_t place, int lane, float (&a)[CPL], float (&h)[CPL]) const
+    // A map, once it is there (the whole wave).  Returns whether it restarts.
+    __device__ __forceinline__ bool wait_map(const uint64_t* first, int lane, float (&a)[CPL], float (&h)[CPL]) const
     {
-        const uint64_t* p = maps + place * CH + lane * CPL;
+        const uint64_t* p = first + lane * CPL;
         uint64_t w[CPL];
         const uint64_t start = wait_start();
         for (;;) {
@@ -431,105 +443,164 @@ struct Chain {
         return uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(w[0]))) == RC_RESTART;
     }
 
+    __device__ __forceinline__ static int stretch_of(int place) { return place / STRETCH; }
+    // Tiles in front of this one in its group; groups in front of its own in the stretch.
+    __device__ __forceinline__ static int tiles_before(int place) { return place % RC_GROUP; }
+    __device__ __forceinline__ static int groups_before(int place) { return place % STRETCH / RC_GROUP; }
+    __device__ __forceinline__ static bool ends_group(int place) { return place % RC_GROUP == RC_GROUP - 1; }
+    __device__ __forceinline__ static bool ends_stretch(int place) { return place % STRETCH == STRETCH - 1; }
+    __device__ __forceinline__ uint64_t* map_of(int place) const { return maps + int64_t(place) * CH; }
+    __device__ __forceinline__ uint32_t* count_of(int place) const { return counts + int64_t(place / RC_GROUP) * 2 * RC_COUNTER; }
+
     // A tile's part in the chain.  One wave, the link, hands out the tile's map (a, h; cut: it restarts), ...
-    __device__ __forceinline__ void hand_out(int64_t place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool cut) const
+    __device__ __forceinline__ void hand_out(int place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool cut) const
     {
-        const int at = int(place % RC_GROUP);
         if (place == places - 1)
             return;
-        if (at < RC_GROUP - 1)
-            publish_map(place, lane, a, h, cut);
+        if (!ends_group(place))
+            publish_map(map_of(place), lane, a, h, cut);
         else if (cut)
-            publish_front(place / RC_GROUP + 1, lane, h);
+            hand_out_group(place, lane, a, h, true);
     }
-    // ... each of the other waves (`which` of them, from 0) fetches one of the maps in front of it in its group, ...
-    __device__ __forceinline__ void collect(int64_t place, int which, int lane, GroupParts<CPL>& parts) const
+    // (a group's last tile) ... the group's, or, as the stretch's last, the next one's front, which a restart alone tells, ...
+    __device__ __forceinline__ void hand_out_group(int place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool cut) const
     {
-        const int count = int(place % RC_GROUP);
-        if (which >= count)
-            return;
+        if (!ends_stretch(place))
+            publish_map(map_of(place), lane, a, h, cut);
+        else if (cut)
+            publish_front(stretch_of(place) + 1, lane, h);
+    }
+    __device__ __forceinline__ void fetch(const uint64_t* map, int level, int which, int lane, ChainParts<CPL, LEVELS>& parts) const
+    {
         WaveMap<CPL> m;
-        const bool again = wait_map(place - count + which, lane, m.a, m.h);
-        parts.maps[which][lane] = m;
+        const bool again = wait_map(map, lane, m.a, m.h);
+        parts.maps[level][which][lane] = m;
         if (lane == 0)
-            parts.restart[which] = again;
+            parts.restart[level][which] = again;
         // a wave's LDS accesses keep their order; the compiler is to keep it too
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         if (lane == 0)
-            __hip_atomic_fetch_add(&parts.arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __hip_atomic_fetch_add(&parts.arrived[level], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
-    // ... and the link makes of these and the group's front (the first group's: `v`) the value in front of the tile and hands on
-    // what leaves it.  All that can be done before the front is there is done by then: from front to front is
-    // one multiply-add.
-    __device__ __forceinline__ void link(int64_t place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool cut,
-                                         GroupParts<CPL>& parts, float (&v)[CPL], float (&leaves)[CPL]) const
+    // ... each of the other waves (`which` of them, from 0) fetches one of the maps in front of it in its group and one of
+    // the groups' in front, ...
+    __device__ __forceinline__ void collect(int place, int which, int lane, ChainParts<CPL, LEVELS>& parts) const
     {
-        const int count = int(place % RC_GROUP);
+        const int tiles = tiles_before(place), groups = groups_before(place);
+        if (which < tiles)
+            fetch(map_of(place - tiles + which), 0, which, lane, parts);
+        if (LEVELS > 1 && which < groups)
+            fetch(map_of((place / RC_GROUP - groups + which) * RC_GROUP + RC_GROUP - 1), 1, which, lane, parts);
+    }
+    // Fetched maps composed, onto (a, h; cut).
+    __device__ __forceinline__ void compose(int level, int count, int lane, ChainParts<CPL, LEVELS>& parts, float (&a)[CPL], float (&h)[CPL],
+                                            bool& cut) const
+    {
         // the collecting waves end their waits in any case
-        while (__builtin_amdgcn_readfirstlane(__hip_atomic_load(&parts.arrived, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) < count)
+        while (__builtin_amdgcn_readfirstlane(__hip_atomic_load(&parts.arrived[level], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) <
+               count)
             __builtin_amdgcn_s_sleep(1);
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        bool group_cut = false;
-        float ga[CPL], gh[CPL], all_a[CPL], all_h[CPL];
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            ga[c] = 1.0f;
-            gh[c] = 0.0f;
-        }
         for (int j = 0; j < count; ++j) {
-            const WaveMap<CPL> o = parts.maps[j][lane];
-            const bool again = __builtin_amdgcn_readfirstlane(parts.restart[j]) != 0;
-            group_cut |= again;
+            const WaveMap<CPL> o = parts.maps[level][j][lane];
+            const bool again = __builtin_amdgcn_readfirstlane(parts.restart[level][j]) != 0;
+            cut |= again;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                gh[c] = again ? o.h[c] : __builtin_fmaf(o.a[c], gh[c], o.h[c]);
-                ga[c] *= o.a[c];
+                h[c] = again ? o.h[c] : __builtin_fmaf(o.a[c], h[c], o.h[c]);
+                a[c] *= o.a[c];
             }
         }
+    }
+    // ... and the link makes of these and the stretch's front (the first one's: `v`) the value in front of the tile and hands on
+    // what leaves it.  What can be done before the front is there is done by then: from front to front are two
+    // multiply-adds.
+    __device__ __forceinline__ void link(int place, int lane, const float (&a)[CPL], const float (&h)[CPL], bool cut,
+                                         ChainParts<CPL, LEVELS>& parts, float (&v)[CPL], float (&leaves)[CPL]) const
+    {
+        bool group_cut = false, any_cut = false;
+        float ga[CPL], gh[CPL], fa[CPL], fh[CPL];
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            all_h[c] = cut ? h[c] : __builtin_fmaf(a[c], gh[c], h[c]);
-            all_a[c] = a[c] * ga[c];
+            ga[c] = fa[c] = 1.0f;
+            gh[c] = fh[c] = 0.0f;
         }
-        if (place >= RC_GROUP)
-            wait_front(place / RC_GROUP, lane, v);
+        compose(0, tiles_before(place), lane, parts, ga, gh, group_cut);
+        if (LEVELS > 1 && !cut && ends_group(place) && place != places - 1) {
+            float all_a[CPL], all_h[CPL];
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                all_h[c] = __builtin_fmaf(a[c], gh[c], h[c]);
+                all_a[c] = a[c] * ga[c];
+            }
+            hand_out_group(place, lane, all_a, all_h, group_cut);
+        }
+        if constexpr (LEVELS > 1) {
+            compose(1, groups_before(place), lane, parts, fa, fh, any_cut);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                gh[c] = group_cut ? gh[c] : __builtin_fmaf(ga[c], fh[c], gh[c]);
+                ga[c] *= fa[c];
+            }
+        }
+        any_cut |= group_cut;
+        if (stretch_of(place) > 0)
+            wait_front(stretch_of(place), lane, v);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            v[c] = any_cut ? gh[c] : __builtin_fmaf(ga[c], v[c], gh[c]);
+            leaves[c] = cut ? h[c] : __builtin_fmaf(a[c], v[c], h[c]);
+        }
+        if (!cut && !(LEVELS > 1 && group_cut) && ends_stretch(place) && place != places - 1)
+            publish_front(stretch_of(place) + 1, lane, leaves);
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
-            leaves[c] = cut || group_cut ? all_h[c] : __builtin_fmaf(all_a[c], v[c], all_h[c]);
-        if (!cut && count == RC_GROUP - 1 && place != places - 1)
-            publish_front(place / RC_GROUP + 1, lane, leaves);
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            v[c] = group_cut ? gh[c] : __builtin_fmaf(ga[c], v[c], gh[c]);
             parts.value[c][lane] = v[c];
-        }
     }
 
-    // By one wave behind a barrier, when the tile has read all it needs of its group: signs off.
-    __device__ __forceinline__ uint32_t leave(int64_t place, int lane) const
+    // By one wave behind a barrier, when the tile has read all it needs: signs off.
+    __device__ __forceinline__ uint32_t leave(int place, int lane) const
     {
         uint32_t before = 0;
         if (places > 1 && lane == 0)
-            before = __hip_atomic_fetch_add(counts + place / RC_GROUP * RC_COUNTER, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            before = __hip_atomic_fetch_add(count_of(place), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         return before;
     }
-    // Last step, some time later: whoever was the group's last to sign off (`before` of them) sets its words back.
-    __device__ __forceinline__ void clear(int64_t place, int lane, uint32_t before) const
+    __device__ __forceinline__ void clear_map(int place, int lane) const
     {
-        const int64_t group = place / RC_GROUP, first = group * RC_GROUP;
-        const int in_group = int(places - first < RC_GROUP ? places - first : RC_GROUP);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+            status_store(map_of(place) + lane * CPL + c, 0);
+    }
+    // Last step, some time later: whoever was the group's last to sign off (`before` of them) sets its words back, and
+    // the last group's of a stretch those of the stretch.
+    __device__ __forceinline__ void clear(int place, int lane, uint32_t before) const
+    {
+        const int first = place / RC_GROUP * RC_GROUP;
+        const int in_group = places - first < RC_GROUP ? places - first : RC_GROUP;
         if (places == 1 || __builtin_amdgcn_readfirstlane(int(before)) != in_group - 1)
             return;
-        for (int j = 0; j < in_group - 1; ++j)
-#pragma unroll
-            for (int c = 0; c < CPL; ++c)
-                status_store(maps + (first + j) * CH + lane * CPL + c, 0);
-        if (group > 0) {
-            const uint32_t none[CPL] = {};
-            store_front(group, lane, none);
+        const int start = stretch_of(place) * STRETCH;  // the stretch's first place
+        const int behind = (places - 1) / RC_GROUP + 1 - start / RC_GROUP;
+        const int in_stretch = behind < STRETCH / RC_GROUP ? behind : STRETCH / RC_GROUP;
+        uint32_t groups = 0;
+        if (lane == 0) {
+            if (in_stretch > 1)
+                groups = __hip_atomic_fetch_add(count_of(start) + RC_COUNTER, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(count_of(place), 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (lane == 0)
-            __hip_atomic_store(counts + group * RC_COUNTER, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int j = 0; j < in_group - 1; ++j)
+            clear_map(first + j, lane);
+        if (__builtin_amdgcn_readfirstlane(int(groups)) != in_stretch - 1)
+            return;
+        for (int j = 0; j < in_stretch - 1; ++j)
+            clear_map(start + j * RC_GROUP + RC_GROUP - 1, lane);
+        if (start > 0) {
+            const uint32_t none[CPL] = {};
+            store_front(stretch_of(place), lane, none);
+        }
+        if (in_stretch > 1 && lane == 0)
+            __hip_atomic_store(count_of(start) + RC_COUNTER, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 };
 
@@ -541,7 +612,8 @@ struct Work {
     uint32_t chains, which, member, members;  // this block's chain, and which of the chain's blocks it is
     int64_t chain, c0;                        // sequence, first channel
     uint32_t here;                            // channels
-    int64_t rows, tiles, places;              // rows there are; tiles of the call, and those with rows
+    int64_t rows;                             // there are
+    int tiles, places;                        // tiles of the call, and those with rows
 
     __device__ __forceinline__ Work(int rows_per_wave, int64_t sequences, int64_t call_rows, int64_t channels, const int64_t* offsets)
     {
@@ -563,21 +635,21 @@ struct Work {
             const int64_t live = offsets[sequences];
             rows = int64_t(uniform(uint64_t(live < 0 ? 0 : live < rows ? live : rows)));
         }
-        tiles = call_rows > 0 ? (call_rows + tile_rows - 1) >> tile_shift : 1;
-        places = (rows + tile_rows - 1) >> tile_shift;
+        tiles = call_rows > 0 ? int((call_rows + tile_rows - 1) >> tile_shift) : 1;
+        places = int((rows + tile_rows - 1) >> tile_shift);
     }
 };
 
 // ---------------------------------------------------------------- forward
 
-template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED, bool ONCE>
-__global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForward q, void* ws)
+template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, int LEVELS, bool ONCE>
+__global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForward q, void* ws, ChainLayout layout)
 {
-    constexpr int CH = 64 * CPL;
+    constexpr bool CHAINED = LEVELS > 0;
     static_assert(WAVES >= RC_GROUP && ROWS * WAVES <= RC_TILE, "each map of a group needs a wave");
     __shared__ WaveMap<CPL> maps[CHAINED ? 1 : 2][WAVES][64];
     __shared__ int restart[CHAINED ? 1 : 2][WAVES];
-    __shared__ GroupParts<CPL> parts;
+    __shared__ ChainParts<CPL, CHAINED ? LEVELS : 1> parts;
     __shared__ int head_seq[PACKED ? RC_TILE : 1], end_seq[PACKED ? RC_TILE : 1];
     __shared__ uint32_t place_shared;
     const Work<CPL, PACKED, CHAINED> w(ROWS, q.sequences, q.rows, q.channels, q.offsets);
@@ -600,17 +672,17 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForwa
         }
     };
 
-    Chain<CPL> links;
-    int64_t place = 0;
+    Chain<CPL, CHAINED ? LEVELS : 1> links;
+    int place = 0;
     if constexpr (CHAINED) {
-        links = Chain<CPL>(ws, chain_layout(w.chains, w.tiles, CH), w.which);
+        links = Chain<CPL, LEVELS>(ws, layout, w.which);
         links.places = w.places;
-        if (threadIdx.x == 0)
-            parts.arrived = 0;
+        if (threadIdx.x < 2)
+            parts.arrived[threadIdx.x] = 0;
         if constexpr (PACKED) {
             RowMarks marks(q.offsets, q.sequences, head_seq, end_seq);
             place = links.take_place(place_shared);
-            marks.mark(q.offsets, q.sequences, place << w.tile_shift, w.tile_rows, head_seq, end_seq, lane);
+            marks.mark(q.offsets, q.sequences, int64_t(place) << w.tile_shift, w.tile_rows, head_seq, end_seq, lane);
             __syncthreads();
         } else {
             place = links.take_place(place_shared);
@@ -618,12 +690,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForwa
     }
     // what is in front of the sequence; of a block that walks, of its next tile
     float carry[CPL] = {};
-    if (!PACKED && q.state != nullptr && place < RC_GROUP)  // the first group's front
+    if (!PACKED && q.state != nullptr && (!CHAINED || links.stretch_of(place) == 0))  // the first stretch's front
         load_state<CPL>(make_rsrc(q.state + chain * q.state_row + c0, state_bytes), lane, carry);
     if (place < w.places)
-        load_rows((place << w.tile_shift) + wave * ROWS);
+        load_rows((int64_t(place) << w.tile_shift) + wave * ROWS);
     for (int turn = 0; place < w.places; ++place, turn ^= 1) {
-        const int64_t row0 = place << w.tile_shift, row = row0 + wave * ROWS;
+        const int64_t row0 = int64_t(place) << w.tile_shift, row = row0 + wave * ROWS;
         float a[ROWS][CPL], b[ROWS][CPL];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
@@ -799,14 +871,14 @@ struct alignas(4 * CPL) WaveBack {
     float a[CPL], h[CPL], mu[CPL];
 };
 
-template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, bool CHAINED, bool ONCE>
-__global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBackward q, void* ws)
+template <class E, int CPL, int ROWS, int WAVES, int GATING, bool PACKED, int LEVELS, bool ONCE>
+__global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBackward q, void* ws, ChainLayout layout)
 {
-    constexpr int CH = 64 * CPL;
+    constexpr bool CHAINED = LEVELS > 0;
     static_assert(WAVES >= RC_GROUP && ROWS * WAVES <= RC_TILE && RC_PERIOD % ROWS == 0, "each map of a group needs a wave");
     __shared__ WaveBack<CPL> maps[CHAINED ? 1 : 2][WAVES][64];
     __shared__ int restart[CHAINED ? 1 : 2][WAVES][2];
-    __shared__ GroupParts<CPL> parts;
+    __shared__ ChainParts<CPL, CHAINED ? LEVELS : 1> parts;
     __shared__ int head_seq[PACKED ? RC_TILE : 1], end_seq[PACKED ? RC_TILE : 1];
     __shared__ uint32_t place_shared;
     const Work<CPL, PACKED, CHAINED> w(ROWS, q.sequences, q.rows, q.channels, q.offsets);
@@ -821,15 +893,15 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBack
     const int64_t periods = (q.rows + RC_PERIOD - 1) / RC_PERIOD;
 
     // place 0 is the last tile
-    auto first_row = [&](int64_t place) { return (w.places - 1 - place) << w.tile_shift; };
+    auto first_row = [&](int place) { return int64_t(w.places - 1 - place) << w.tile_shift; };
 
-    Chain<CPL> links;
-    int64_t place = 0;
+    Chain<CPL, CHAINED ? LEVELS : 1> links;
+    int place = 0;
     if constexpr (CHAINED) {
-        links = Chain<CPL>(ws, chain_layout(w.chains, w.tiles, CH), w.which);
+        links = Chain<CPL, LEVELS>(ws, layout, w.which);
         links.places = w.places;
-        if (threadIdx.x == 0)
-            parts.arrived = 0;
+        if (threadIdx.x < 2)
+            parts.arrived[threadIdx.x] = 0;
         if constexpr (PACKED) {
             RowMarks marks(q.offsets, q.sequences, head_seq, end_seq);
             place = links.take_place(place_shared);
@@ -840,7 +912,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBack
         }
     }
     float mu_carry[CPL] = {};
-    if (!PACKED && q.dstate_out != nullptr && place < RC_GROUP)  // the first group's front
+    if (!PACKED && q.dstate_out != nullptr && (!CHAINED || links.stretch_of(place) == 0))  // the first stretch's front
         load_state<CPL>(make_rsrc(q.dstate_out + chain * q.dstate_out_row + c0, state_bytes), lane, mu_carry);
     for (int turn = 0; place < w.places; ++place, turn ^= 1) {
         const int64_t row0 = first_row(place), row = row0 + wave * ROWS;
@@ -1170,9 +1242,11 @@ bool multiples(const void* p, int64_t a, int64_t b, int64_t to)
 // 256 MiB 264 and 250; 512 MiB 486 and 453.
 constexpr int64_t RC_ONCE_ALL = 192 << 20;
 template <class Q>
-bool loads_once(const Q& q, int size)
+bool loads_once(const Q& q, int size, int per_lane)
 {
-    return (q.offsets != nullptr ? 1 : q.sequences) * q.rows * q.channels * size * 2 >= RC_ONCE_ALL;
+    // few chains wait for each other more than for memory, and have kernels of their own
+    const int64_t chains = (q.offsets != nullptr ? 1 : q.sequences) * ((q.channels + 64 * per_lane - 1) / (64 * per_lane));
+    return chain_levels(chains) == 1 && (q.offsets != nullptr ? 1 : q.sequences) * q.rows * q.channels * size * 2 >= RC_ONCE_ALL;
 }
 
 // A launch holds less than 2^32 threads.  Of tiles as blocks, 2^23 - 1 of 512 threads: a call of more is refused.
@@ -1188,13 +1262,23 @@ hipError_t forward_of(const RecurForward& q, void* ws, hipStream_t stream)
     const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, 1);
     if (p.chained && p.chains * p.tiles > RC_BLOCKS)
         return hipErrorInvalidConfiguration;
+    const ChainLayout layout = chain_layout(p.chains, p.tiles, 64 * CPL);
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
+    if constexpr (!ONCE) {
+        if (p.chained && chain_levels(p.chains) == 2) {
+            if (q.offsets != nullptr)
+                recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, true, 2, false><<<blocks, threads, 0, stream>>>(q, ws, layout);
+            else
+                recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, 2, false><<<blocks, threads, 0, stream>>>(q, ws, layout);
+            return hipGetLastError();
+        }
+    }
     if (p.chained && q.offsets != nullptr)
-        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, true, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, true, 1, ONCE><<<blocks, threads, 0, stream>>>(q, ws, layout);
     else if (p.chained)
-        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, 1, ONCE><<<blocks, threads, 0, stream>>>(q, ws, layout);
     else
-        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, false, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_forward_kernel<E, CPL, S::rows, S::waves, GATING, false, 0, ONCE><<<blocks, threads, 0, stream>>>(q, ws, layout);
     return hipGetLastError();
 }
 
@@ -1228,7 +1312,7 @@ hipError_t launch_forward(const RecurForward& q, void* ws, hipStream_t stream)
         const hipError_t e = launch_forward<E, CPL>(first, ws, stream);
         return e != hipSuccess ? e : launch_forward<E, CPL>(rest, ws, stream);
     }
-    return loads_once(q, E::size) ? forward_by<E, CPL, true>(q, ws, stream) : forward_by<E, CPL, false>(q, ws, stream);
+    return loads_once(q, E::size, CPL) ? forward_by<E, CPL, true>(q, ws, stream) : forward_by<E, CPL, false>(q, ws, stream);
 }
 
 template <class E, int CPL, int GATING, bool ONCE>
@@ -1238,13 +1322,23 @@ hipError_t backward_of(const RecurBackward& q, void* ws, hipStream_t stream)
     const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, RC_PERIOD / S::rows);
     if (p.chained && p.chains * p.tiles > RC_BLOCKS)
         return hipErrorInvalidConfiguration;
+    const ChainLayout layout = chain_layout(p.chains, p.tiles, 64 * CPL);
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
+    if constexpr (!ONCE) {
+        if (p.chained && chain_levels(p.chains) == 2) {
+            if (q.offsets != nullptr)
+                recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, true, 2, false><<<blocks, threads, 0, stream>>>(q, ws, layout);
+            else
+                recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, 2, false><<<blocks, threads, 0, stream>>>(q, ws, layout);
+            return hipGetLastError();
+        }
+    }
     if (p.chained && q.offsets != nullptr)
-        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, true, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, true, 1, ONCE><<<blocks, threads, 0, stream>>>(q, ws, layout);
     else if (p.chained)
-        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, true, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, 1, ONCE><<<blocks, threads, 0, stream>>>(q, ws, layout);
     else
-        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, false, ONCE><<<blocks, threads, 0, stream>>>(q, ws);
+        recur_backward_kernel<E, CPL, S::rows, S::waves, GATING, false, 0, ONCE><<<blocks, threads, 0, stream>>>(q, ws, layout);
     return hipGetLastError();
 }
 
@@ -1281,7 +1375,7 @@ hipError_t launch_backward(const RecurBackward& q, void* ws, hipStream_t stream)
         const hipError_t e = launch_backward<E, CPL>(first, ws, stream);
         return e != hipSuccess ? e : launch_backward<E, CPL>(rest, ws, stream);
     }
-    return loads_once(q, E::size) ? backward_by<E, CPL, true>(q, ws, stream) : backward_by<E, CPL, false>(q, ws, stream);
+    return loads_once(q, E::size, CPL) ? backward_by<E, CPL, true>(q, ws, stream) : backward_by<E, CPL, false>(q, ws, stream);
 }
 
 template <class E>
