@@ -3,10 +3,9 @@
 //
 // A token is the affine map h -> a h + b of each channel, and maps compose:
 //     (a1, b1) then (a2, b2)  =  (a2 a1, a2 b1 + b2),
-// so the recurrence is a scan. Channels lie beside each
-// other in memory and are independent: a lane owns CPL neighbouring
-// channels (4 bytes of a row), a wave some consecutive tokens of its 64 CPL channels, and a
-// block's waves lie one behind the other in time.  Per tile (64 or 128 tokens):
+// so the recurrence is a scan.  Channels lie beside each other in memory and are independent: a
+// lane owns CPL neighbouring channels (4 bytes of a row), a wave some consecutive tokens of its
+// 64 CPL channels, and a block's waves lie one behind the other in time.  Per tile (64 or 128 tokens):
 //   1. every wave loads its rows (each load 256 consecutive bytes), makes a and b of them in
 //      float32 and composes its map;
 //   2. the waves' maps meet in LDS; every wave applies those in front of it to the value in
@@ -20,6 +19,14 @@
 // the same maps' factors from the last token to the first.  A tile needs h again: it is
 // made from x and gate, from the carries that the forward pass kept of every RC_PERIOD-th
 // row, in 32 bits; the output h would cost as many bytes and is rounded.
+//
+// What bounds it: memory, three elements a token and channel forward and five backward, where blocks walk (64 sequences
+// of 512 tokens of 2048 bfloat16 channels: 74 us forward, 5.4 TB/s, 132 backward, 5.1); and where tiles are
+// blocks also the wait for the value in front, which holds a block's registers while nothing of it is
+// under way (1 x 65536 x 2048: 186 and 342 us, 4.3 and 3.9 TB/s; without the link, so with wrong values, 137 forward).
+// A CU holds two such blocks (three backward).  Tried there and not kept: blocks that stay and load the next tile while they
+// wait (230 to 365 us forward: one block a CU), raw rows kept and the maps made again for three or four blocks a CU (185 to 193:
+// registers spill), one 16-bit channel a lane (backward 310, but 323 against 272 for 8 x 4096 x 4096).
 //
 // A sequence's first row takes its state in place of the carry, by selection and not by a
 // factor of 0, so that an infinity in one sequence never reaches the next.
@@ -1127,7 +1134,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBack
 
 // ---------------------------------------------------------------- one token a sequence
 
-// VEC neighbouring channels per thread: 16 bytes of x, or one element where rows are not aligned.
+// VEC neighbouring channels per thread: 16 bytes of x, or one element where rows are not aligned.  One pass: x, gate and
+// state in, out and state out; 256 sequences of 4096 bfloat16 channels take 4.7 us (14.7 MB: 2.4 at 6.2 TB/s and the launch's 2),
+// one sequence of 2048 2.2.
 template <class E, int VEC>
 __global__ __launch_bounds__(256) void recur_step_kernel(RecurForward q)
 {
@@ -1168,10 +1177,12 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurForward q)
 // ---------------------------------------------------------------- launches
 
 // Blocks that walk keep the carry to themselves and load ahead; they take the call where the chains alone fill the
-// GPU, or where a chain is one tile.
+// GPU, or where a chain is one tile.  From 256 chains on: 8 x 4096 x 4096 (256) forward 151 us against 166, but 6 x 4096 x
+// 8192 (384) 256 against 238, and backward slower in both; from 2048 on: 64 x 512 x 2048 (1024) 84 against 75.
 constexpr int64_t RC_WALKERS = 512;
 
-// Tokens per wave, and waves, of a tile.
+// Tokens per wave, and waves, of a tile.  1 x 65536 x 2048 forward with 8 tokens a wave 237 us against 183; backward of two
+// channels a lane with 16 waves of 8 tokens 340 against 342, but 319 against 273 for 8 x 4096 x 4096.
 template <int CPL>
 struct ForwardShape {
     static constexpr int rows = 16, waves = 8;
@@ -1236,10 +1247,10 @@ bool multiples(const void* p, int64_t a, int64_t b, int64_t to)
 }
 
 // x and gate that the memory-side cache (256 MiB) holds beside what the call writes are loaded as usual: it may have them,
-// from the products that made them or from the forward pass.  More are loaded past the caches.  Forward and backward, one after
-// the other on inputs that were not there before, loads as usual and past the caches: x and gate of 128 MiB (4 x 4096 x
-// 2048 bfloat16) 127 and 127 us, the same inputs again 102 and 126; 41 MiB (3 x 1777 x 1001 float32) 48 and 60;
-// 256 MiB 264 and 250; 512 MiB 486 and 453.
+// from the products that made them or from the forward pass.  More are loaded past the caches.  Forward and backward one after
+// the other, loads as usual and past the caches, on five sets of inputs in turn and on the same inputs again: x and
+// gate of 128 MiB (4 x 4096 x 2048 bfloat16) 135 and 128 us, 107 and 126; 41 MiB (3 x 1777 x 1001 float32) 52 and 60,
+// 46 and 57; 256 MiB 264 and 250, 255 and 250; 512 MiB 486 and 453, 480 and 452.
 constexpr int64_t RC_ONCE_ALL = 192 << 20;
 template <class Q>
 bool loads_once(const Q& q, int size, int per_lane)
