@@ -305,7 +305,8 @@ def test_many_rows(mib, top):
 
 @pytest.mark.parametrize("packed", [False, True])
 @pytest.mark.parametrize("gating", ["sigmoid", "log", "decay"])
-@pytest.mark.parametrize("dtype, d", [(torch.float32, 129), (torch.float16, 258), (torch.bfloat16, 259)], ids=str)
+@pytest.mark.parametrize("dtype, d", [(torch.float32, 129), (torch.float16, 258), (torch.bfloat16, 259), (torch.float32, 325),
+                                      (torch.float16, 643), (torch.bfloat16, 1282)], ids=str)
 def test_many_tokens(dtype, d, gating, packed):
     """Tokens that fill the caches are loaded by other loads than fewer, which changes no value: two halves of a
     call, tile by tile the same work, give what the call gives."""
