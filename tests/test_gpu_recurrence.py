@@ -129,6 +129,8 @@ PACKED = {
     "one token": [0, 1, 0],
     "many empty": [0] * 700 + [3] + [0] * 900 + [200] + [0] * 300,
     "long": [3000, 1, 500],
+    # at the borders of tiles, groups of tiles and stretches of groups, and inside them
+    "stretches": [8192, 1, 127, 896, 128, 7168, 1, 4095, 4096, 9000, 0, 63],
 }
 
 
