@@ -52,11 +52,13 @@ struct BF16 {
     }
 };
 
-// VEC neighbouring elements at p, aligned to all of them.
+// VEC neighbouring elements at p, aligned to all of them or to 16 bytes (eight float32 values are 32 bytes; a
+// vector type's own alignment, its size, would promise the compiler more than the launchers ask for).
 template <class E, int VEC>
 struct Elements {
     static constexpr int per_word = VEC == 1 ? 1 : 4 / E::size;
     static constexpr int words = VEC / per_word;
+    static constexpr int align = words < 4 ? 4 * words : 16;
     uint32_t w[words];
     // once: the bytes are not asked for again soon, and need no place in the caches
     template <bool ONCE = false>
@@ -65,7 +67,7 @@ struct Elements {
         if constexpr (VEC * E::size == 2) {
             w[0] = *static_cast<const uint16_t*>(p);
         } else {
-            typedef uint32_t v __attribute__((ext_vector_type(words)));
+            typedef uint32_t v __attribute__((ext_vector_type(words), aligned(align)));
             v t;
             if constexpr (ONCE)
                 t = __builtin_nontemporal_load(static_cast<const v*>(p));
@@ -80,7 +82,7 @@ struct Elements {
         if constexpr (VEC * E::size == 2) {
             *static_cast<uint16_t*>(p) = uint16_t(w[0]);
         } else {
-            typedef uint32_t v __attribute__((ext_vector_type(words)));
+            typedef uint32_t v __attribute__((ext_vector_type(words), aligned(align)));
             v t;
             __builtin_memcpy(&t, w, sizeof w);
             if constexpr (ONCE)

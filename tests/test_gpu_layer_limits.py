@@ -330,3 +330,28 @@ def test_many_tokens(dtype, d, gating, packed):
     parts = [call(x[i:i + 1], gate[i:i + 1], dout[i:i + 1], state[i:i + 1], dstate[i:i + 1]) for i in range(2)]
     for got, *want in zip(whole, *parts):
         assert torch.equal(got, torch.cat(want)) and bool(torch.isfinite(got).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+def test_a_token_each_with_states_off_32_bytes(dtype):
+    """States and carries at 16 bytes past a border of 32, with rows an odd multiple of 16 bytes apart."""
+    batch, d = 37, 264
+    x, gate = rand(batch, d, dtype=dtype), rand(batch, d, seed=1, dtype=dtype)
+    state = rand(batch, d, seed=2, dtype=torch.float32)
+    kept = ps.recurrence_carries(x)
+    want = ps.gated_recurrence(x, gate, state=state, carries=kept)
+
+    def off(columns):
+        flat = torch.full((batch * columns + 8,), 5.0, device=DEV)
+        first = (16 - flat.data_ptr() % 32) % 32 // 4
+        return flat, flat[first:first + batch * columns].view(batch, columns)
+
+    (_, before), (_, after), (flat, carries) = off(d + 4), off(d + 4), off(d)
+    for t in (before, after, carries):
+        assert t.data_ptr() % 32 == 16
+    before[:, :d] = state
+    out, last = ps.gated_recurrence(x, gate, state=before[:, :d], state_out=after[:, :d], carries=carries)
+    assert torch.equal(out, want[0]) and torch.equal(last, want[1]) and torch.equal(carries, kept)
+    assert bool((after[:, d:] == 5.0).all()) and int((flat == 5.0).sum()) >= 8
+    out, last = ps.gated_recurrence(x, gate, state=before[:, :d], state_out=before[:, :d])  # in place
+    assert torch.equal(out, want[0]) and torch.equal(last, want[1])
