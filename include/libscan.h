@@ -563,7 +563,7 @@ ls_status ls_recurrence_workspace_bytes(int64_t sequences, int64_t rows, int64_t
  *                  ls_workspace_init before its first use; each call leaves it ready for the next.
  *                  It serves the two recurrence calls only.  May be NULL where the size is 0.
  * A call whose sequences are cut into 2^23 or more tiles (64 tokens or more by 64 channels or more each; only rows
- * of few channels come to that) is refused with LS_ERR_UNSUPPORTED.
+ * of few channels come to that) is refused with LS_ERR_UNSUPPORTED, whatever its workspace.
  * A tile waits for the ones in front of it.  A wait that lasts 1 s, which no correct run does, gives up: the outputs
  * are then incomplete, ls_workspace_check reports it, and the workspace has to be initialised again.
  * Decays of magnitude up to 1 are meant; larger ones work while the products of the decays of

@@ -1138,14 +1138,16 @@ def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, state: torch.Tensor | 
 
 def _with_workspace(fn, args: tuple, kind: str, index: int, need) -> tuple:
     """(status, workspace) of a call on the current stream's workspace of this kind, which is replaced where the
-    call finds it too small; need() is its size then."""
+    call finds it too small; need() is its size then.  The call is asked without a workspace first where a new one
+    would be made: one that is refused for another reason leaves none."""
     handle = _raw_stream(index)
     with _ws_lock:
         ws = _ws_cache.get((index, handle, kind))
-        if ws is not None and (handle == 0 or _capture_of(handle) is None):
-            st = fn(*args, ws.data_ptr(), ws.numel(), handle)
-            if st != LS_ERR_WORKSPACE:
-                return st, ws
+        if handle != 0 and _capture_of(handle) is not None:
+            ws = None
+        st = fn(*args, None, 0, handle) if ws is None else fn(*args, ws.data_ptr(), ws.numel(), handle)
+        if st != LS_ERR_WORKSPACE:
+            return st, ws
         device = torch.device("cuda", index)
         ws = workspace_for(device, torch.cuda.current_stream(device), need(), kind)
         return fn(*args, ws.data_ptr(), ws.numel(), handle), ws

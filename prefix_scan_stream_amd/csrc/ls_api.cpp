@@ -316,8 +316,6 @@ bool recurrence_sizes_ok(int64_t sequences, int64_t rows, int64_t channels)
 {
     return count_ok(sequences) && count_ok(rows) && channels_ok(channels);
 }
-// A call of more tiles than a launch holds is refused by its launcher before anything is enqueued.
-ls_status from_launch(hipError_t e) { return e == hipErrorInvalidConfiguration ? LS_ERR_UNSUPPORTED : from_hip(e); }
 bool gating_ok(ls_gating g) { return g >= LS_GATE_DECAY && g <= LS_GATE_SIGMOID; }
 
 bool experts_sizes_ok(int64_t tokens, int64_t top, int64_t num_rows, int64_t channels)
@@ -704,15 +702,18 @@ ls_status gated_recurrence(const void* x, int64_t x_sequence_stride, int64_t x_r
     };
     if (!all_rows_ok(all))
         return LS_ERR_INVALID_ARG;
+    const ls::RecurForward call = {x, gate, out, x_sequence_stride, x_row_stride, gate_sequence_stride, gate_row_stride,
+                                   out_sequence_stride, out_row_stride, state, state_out, state_stride, state_out_stride,
+                                   carries, offsets, sequences, rows, channels, int(gating)};
+    // before its workspace, which may be gigabytes, is asked for
+    if (!ls::recurrence_fits(call, int(t)))
+        return LS_ERR_UNSUPPORTED;
     if (need > 0) {
         const ls_status st = check_ws(ws, ws_bytes, need);
         if (st != LS_OK)
             return st;
     }
-    const ls::RecurForward call = {x, gate, out, x_sequence_stride, x_row_stride, gate_sequence_stride, gate_row_stride,
-                                   out_sequence_stride, out_row_stride, state, state_out, state_stride, state_out_stride,
-                                   carries, offsets, sequences, rows, channels, int(gating)};
-    return from_launch(ls::launch_recurrence(call, int(t), ws, reinterpret_cast<hipStream_t>(stream)));
+    return from_hip(ls::launch_recurrence(call, int(t), ws, reinterpret_cast<hipStream_t>(stream)));
 }
 
 ls_status gated_recurrence_backward(const void* dout, int64_t dout_sequence_stride, int64_t dout_row_stride,
@@ -750,16 +751,19 @@ ls_status gated_recurrence_backward(const void* dout, int64_t dout_sequence_stri
     };
     if (!all_rows_ok(all))
         return LS_ERR_INVALID_ARG;
+    const ls::RecurBackward call = {dout, x, gate, dx, dgate, dout_sequence_stride, dout_row_stride, x_sequence_stride,
+                                    x_row_stride, gate_sequence_stride, gate_row_stride, dx_sequence_stride, dx_row_stride,
+                                    dgate_sequence_stride, dgate_row_stride, state, dstate_out, dstate, state_stride,
+                                    dstate_out_stride, dstate_stride, carries, offsets, sequences, rows, channels, int(gating)};
+    // before its workspace, which may be gigabytes, is asked for
+    if (!ls::recurrence_fits(call, int(t)))
+        return LS_ERR_UNSUPPORTED;
     if (need > 0) {
         const ls_status st = check_ws(ws, ws_bytes, need);
         if (st != LS_OK)
             return st;
     }
-    const ls::RecurBackward call = {dout, x, gate, dx, dgate, dout_sequence_stride, dout_row_stride, x_sequence_stride,
-                                    x_row_stride, gate_sequence_stride, gate_row_stride, dx_sequence_stride, dx_row_stride,
-                                    dgate_sequence_stride, dgate_row_stride, state, dstate_out, dstate, state_stride,
-                                    dstate_out_stride, dstate_stride, carries, offsets, sequences, rows, channels, int(gating)};
-    return from_launch(ls::launch_recurrence_backward(call, int(t), ws, reinterpret_cast<hipStream_t>(stream)));
+    return from_hip(ls::launch_recurrence_backward(call, int(t), ws, reinterpret_cast<hipStream_t>(stream)));
 }
 
 ls_status ls_experts_workspace_bytes(int64_t pairs, int64_t num_experts, size_t* bytes)

@@ -122,6 +122,9 @@ struct RecurBackward {
 };
 size_t recur_workspace_bytes(int64_t sequences, int64_t rows, int64_t channels, bool packed, int type);
 int64_t recur_carry_rows(int64_t sequences, int64_t rows, bool packed);
+// Whether one launch holds the call's tiles; to be asked before the launch.
+bool recurrence_fits(const RecurForward& call, int type);
+bool recurrence_fits(const RecurBackward& call, int type);
 hipError_t launch_recurrence(const RecurForward& call, int type, void* ws, hipStream_t stream);
 hipError_t launch_recurrence_backward(const RecurBackward& call, int type, void* ws, hipStream_t stream);
 

@@ -1209,13 +1209,20 @@ static ChainPlan chain_plan(int64_t sequences, int64_t rows, int64_t channels, b
 }
 
 template <int CPL>
+static ChainPlan plan_of(bool backward, int64_t sequences, int64_t rows, int64_t channels, bool packed)
+{
+    using F = ForwardShape<CPL>;
+    using B = BackwardShape<CPL>;
+    return backward ? chain_plan(sequences, rows, channels, packed, CPL, B::rows, B::waves, RC_PERIOD / B::rows)
+                    : chain_plan(sequences, rows, channels, packed, CPL, F::rows, F::waves, 1);
+}
+
+template <int CPL>
 static size_t chain_bytes(int64_t sequences, int64_t rows, int64_t channels, bool packed)
 {
     size_t most = 0;
     for (int back = 0; back < 2; ++back) {
-        const ChainPlan p = back ? chain_plan(sequences, rows, channels, packed, CPL, BackwardShape<CPL>::rows, BackwardShape<CPL>::waves,
-                                              RC_PERIOD / BackwardShape<CPL>::rows)
-                                 : chain_plan(sequences, rows, channels, packed, CPL, ForwardShape<CPL>::rows, ForwardShape<CPL>::waves, 1);
+        const ChainPlan p = plan_of<CPL>(back != 0, sequences, rows, channels, packed);
         const size_t n = p.chained ? chain_layout(p.chains, p.tiles, 64 * CPL).bytes : 0;
         most = n > most ? n : most;
     }
@@ -1260,7 +1267,7 @@ bool loads_once(const Q& q, int size, int per_lane)
     return chain_levels(chains) == 1 && (q.offsets != nullptr ? 1 : q.sequences) * q.rows * q.channels * size * 2 >= RC_ONCE_ALL;
 }
 
-// A launch holds less than 2^32 threads.  Of tiles as blocks, 2^23 - 1 of 512 threads: a call of more is refused.
+// A launch holds less than 2^32 threads.  Of tiles as blocks, 2^23 - 1 of 512 threads: a call of more does not fit.
 constexpr int64_t RC_BLOCKS = (int64_t(1) << 23) - 1;
 // Of blocks that walk: most sequences of a launch of `groups` blocks each.  More are halved, so that each half still has chains
 // enough to walk: what a call takes of its workspace goes by all its sequences.
@@ -1270,9 +1277,7 @@ template <class E, int CPL, int GATING, bool ONCE>
 hipError_t forward_of(const RecurForward& q, void* ws, hipStream_t stream)
 {
     using S = ForwardShape<CPL>;
-    const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, 1);
-    if (p.chained && p.chains * p.tiles > RC_BLOCKS)
-        return hipErrorInvalidConfiguration;
+    const ChainPlan p = plan_of<CPL>(false, q.sequences, q.rows, q.channels, q.offsets != nullptr);
     const ChainLayout layout = chain_layout(p.chains, p.tiles, 64 * CPL);
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
     if constexpr (!ONCE) {
@@ -1330,9 +1335,7 @@ template <class E, int CPL, int GATING, bool ONCE>
 hipError_t backward_of(const RecurBackward& q, void* ws, hipStream_t stream)
 {
     using S = BackwardShape<CPL>;
-    const ChainPlan p = chain_plan(q.sequences, q.rows, q.channels, q.offsets != nullptr, CPL, S::rows, S::waves, RC_PERIOD / S::rows);
-    if (p.chained && p.chains * p.tiles > RC_BLOCKS)
-        return hipErrorInvalidConfiguration;
+    const ChainPlan p = plan_of<CPL>(true, q.sequences, q.rows, q.channels, q.offsets != nullptr);
     const ChainLayout layout = chain_layout(p.chains, p.tiles, 64 * CPL);
     const dim3 blocks(uint32_t(p.chained ? p.chains * p.tiles : p.chains)), threads(64 * p.waves);
     if constexpr (!ONCE) {
@@ -1389,6 +1392,24 @@ hipError_t launch_backward(const RecurBackward& q, void* ws, hipStream_t stream)
     return loads_once(q, E::size, CPL) ? backward_by<E, CPL, true>(q, ws, stream) : backward_by<E, CPL, false>(q, ws, stream);
 }
 
+// Channels a lane: a word of two 16-bit ones where every row is aligned to that.
+int lane_channels(const RecurForward& q, int type)
+{
+    const bool pairs = type != LOGITS_F32 && q.channels % 2 == 0 && multiples(q.x, q.x_sequence * 2, q.x_row * 2, 4) &&
+                       multiples(q.gate, q.gate_sequence * 2, q.gate_row * 2, 4) &&
+                       multiples(q.out, q.out_sequence * 2, q.out_row * 2, 4);
+    return pairs ? 2 : 1;
+}
+int lane_channels(const RecurBackward& q, int type)
+{
+    const bool pairs = type != LOGITS_F32 && q.channels % 2 == 0 && multiples(q.x, q.x_sequence * 2, q.x_row * 2, 4) &&
+                       multiples(q.gate, q.gate_sequence * 2, q.gate_row * 2, 4) &&
+                       multiples(q.dout, q.dout_sequence * 2, q.dout_row * 2, 4) &&
+                       multiples(q.dx, q.dx_sequence * 2, q.dx_row * 2, 4) &&
+                       multiples(q.dgate, q.dgate_sequence * 2, q.dgate_row * 2, 4);
+    return pairs ? 2 : 1;
+}
+
 template <class E>
 hipError_t launch_step(const RecurForward& q, hipStream_t stream)
 {
@@ -1406,7 +1427,19 @@ hipError_t launch_step(const RecurForward& q, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <class Q>
+bool fits(const Q& q, int type, bool backward)
+{
+    const bool packed = q.offsets != nullptr;
+    const ChainPlan p = lane_channels(q, type) == 2 ? plan_of<2>(backward, q.sequences, q.rows, q.channels, packed)
+                                                    : plan_of<1>(backward, q.sequences, q.rows, q.channels, packed);
+    return q.sequences == 0 || !p.chained || p.chains * p.tiles <= RC_BLOCKS;
+}
+
 }  // namespace
+
+bool recurrence_fits(const RecurForward& q, int type) { return fits(q, type, false); }
+bool recurrence_fits(const RecurBackward& q, int type) { return fits(q, type, true); }
 
 hipError_t launch_recurrence(const RecurForward& q, int type, void* ws, hipStream_t stream)
 {
@@ -1419,8 +1452,7 @@ hipError_t launch_recurrence(const RecurForward& q, int type, void* ws, hipStrea
     }
     if (type == LOGITS_F32)
         return launch_forward<F32, 1>(q, ws, stream);
-    const bool pairs = q.channels % 2 == 0 && multiples(q.x, q.x_sequence * 2, q.x_row * 2, 4) &&
-                       multiples(q.gate, q.gate_sequence * 2, q.gate_row * 2, 4) && multiples(q.out, q.out_sequence * 2, q.out_row * 2, 4);
+    const bool pairs = lane_channels(q, type) == 2;
     if (type == LOGITS_F16)
         return pairs ? launch_forward<F16, 2>(q, ws, stream) : launch_forward<F16, 1>(q, ws, stream);
     return pairs ? launch_forward<BF16, 2>(q, ws, stream) : launch_forward<BF16, 1>(q, ws, stream);
@@ -1432,11 +1464,7 @@ hipError_t launch_recurrence_backward(const RecurBackward& q, int type, void* ws
         return hipSuccess;
     if (type == LOGITS_F32)
         return launch_backward<F32, 1>(q, ws, stream);
-    const bool pairs = q.channels % 2 == 0 && multiples(q.x, q.x_sequence * 2, q.x_row * 2, 4) &&
-                       multiples(q.gate, q.gate_sequence * 2, q.gate_row * 2, 4) &&
-                       multiples(q.dout, q.dout_sequence * 2, q.dout_row * 2, 4) &&
-                       multiples(q.dx, q.dx_sequence * 2, q.dx_row * 2, 4) &&
-                       multiples(q.dgate, q.dgate_sequence * 2, q.dgate_row * 2, 4);
+    const bool pairs = lane_channels(q, type) == 2;
     if (type == LOGITS_F16)
         return pairs ? launch_backward<F16, 2>(q, ws, stream) : launch_backward<F16, 1>(q, ws, stream);
     return pairs ? launch_backward<BF16, 2>(q, ws, stream) : launch_backward<BF16, 1>(q, ws, stream);

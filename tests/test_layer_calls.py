@@ -1,0 +1,36 @@
+"""The layer's calls on the CPU: what is answered before anything is allocated or enqueued."""
+import pytest
+import torch
+
+import prefix_scan_stream_amd as ps
+from test_layer_abi import A, BACK, RECUR, lib, status  # noqa: F401  (lib is a fixture)
+
+
+@pytest.mark.parametrize("offsets", [None, A[9]])
+@pytest.mark.parametrize("ws", [dict(ws=None, ws_bytes=0), dict(ws_bytes=256)], ids=str)
+def test_too_many_tiles_are_refused_before_the_workspace(lib, offsets, ws):  # noqa: F811
+    """2^31 - 1 tokens of a channel are 2^24 tiles: a caller is told so, and not to come back with gigabytes."""
+    many = dict(sequences=1, rows=(1 << 31) - 1, channels=1, x_s=0, x_r=0, g_s=0, g_r=0, offsets=offsets, **ws)
+    assert status(lib, "gated_recurrence", RECUR, **many, o_s=0, o_r=1) == ps.LS_ERR_UNSUPPORTED
+    assert status(lib, "gated_recurrence_backward", BACK, **many, do_s=0, do_r=0, dx=A[10], dx_s=0, dx_r=1, dg=A[11], dg_s=0,
+                  dg_r=1) == ps.LS_ERR_UNSUPPORTED
+    # what is wrong with the arguments comes first
+    assert status(lib, "gated_recurrence", RECUR, **many, o_s=0, o_r=0) == ps.LS_ERR_INVALID_ARG
+    # a quarter of the rows fit, and want their workspace
+    many["rows"] >>= 2
+    assert status(lib, "gated_recurrence", RECUR, **many, o_s=0, o_r=1) == ps.LS_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("kind", ["recurrence", "experts"])
+@pytest.mark.parametrize("capturing", [False, True])
+@pytest.mark.parametrize("held", [False, True])
+def test_a_refused_call_makes_no_workspace(monkeypatch, kind, capturing, held):
+    made = []
+    monkeypatch.setattr(ps, "_raw_stream", lambda index: 7)
+    monkeypatch.setattr(ps, "_capture_of", lambda handle: 3 if capturing else None)
+    monkeypatch.setattr(ps, "_ws_cache", {(0, 7, kind): torch.zeros(64, dtype=torch.uint8)} if held else {})
+    monkeypatch.setattr(ps, "workspace_for", lambda *a: made.append(a))
+    need = lambda: made.append("size")
+    for refusal in (ps.LS_ERR_INVALID_ARG, ps.LS_ERR_UNSUPPORTED):
+        st, _ = ps._with_workspace(lambda *a: refusal, (1, 2), kind, 0, need)
+        assert st == refusal and made == []
