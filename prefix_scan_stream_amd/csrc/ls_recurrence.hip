@@ -32,6 +32,7 @@
 // factor of 0, so that an infinity in one sequence never reaches the next.
 #include "ls_elements.hpp"
 #include "ls_internal.hpp"
+#include "ls_marks.hpp"
 
 namespace ls {
 
@@ -181,74 +182,6 @@ struct Decay {
     __device__ __forceinline__ void nothing() { u = GATING == GATE_SIGMOID ? 1e-38f : 1.0f; }  // a = 1
     __device__ __forceinline__ float a() const { return GATING != GATE_SIGMOID ? u : u > 0.0f ? 1.0f - u : -u; }
     __device__ __forceinline__ float rest() const { return GATING != GATE_SIGMOID ? 1.0f : u > 0.0f ? u : 1.0f + u; }
-};
-
-// ---------------------------------------------------------------- packed rows
-
-// First s in [0, n) with offsets[s + 1] > row (n: none), the whole wave together: 64 probes a round.
-__device__ __forceinline__ int64_t sequence_of_row(const int64_t* offsets, int64_t n, int64_t row, int lane)
-{
-    int64_t lo = 0, hi = n;  // the answer is in [lo, hi]
-    while (hi - lo > 0) {
-        const int64_t step = (hi - lo + 63) / 64;
-        const int64_t at = lo + lane * step;
-        const bool past = at < hi && offsets[at + 1] > row;
-        const uint64_t found = __ballot(past);
-        if (found == 0) {
-            // the last probe in range stands before the answer
-            const int64_t last = lo + (hi - 1 - lo) / step * step;
-            lo = last + 1;
-        } else {
-            const int first = __builtin_ctzll(found);
-            hi = lo + first * step;
-            lo = first == 0 ? lo : lo + (first - 1) * step + 1;
-        }
-    }
-    return lo;
-}
-
-// For each row of a tile the sequence that starts there and the one that ends there, or -1.  Where the block has a
-// thread for each sequence, its offsets are on their way before the tile is known; with more sequences they are searched
-// for the tile's first.  Offsets out of order mark wrong rows, never ones outside the tile.
-struct RowMarks {
-    int64_t from, to;
-    __device__ __forceinline__ RowMarks(const int64_t* offsets, int64_t sequences, int (&heads)[RC_TILE], int (&ends)[RC_TILE])
-        : from(0), to(0)
-    {
-        if (threadIdx.x < sequences) {
-            from = offsets[threadIdx.x];
-            to = offsets[threadIdx.x + 1];
-        }
-        for (int i = threadIdx.x; i < RC_TILE; i += blockDim.x)
-            heads[i] = ends[i] = -1;
-    }
-    // Between two barriers.
-    __device__ __forceinline__ void mark(const int64_t* offsets, int64_t sequences, int64_t row0, int rows, int (&heads)[RC_TILE],
-                                         int (&ends)[RC_TILE], int lane)
-    {
-        const int tid = threadIdx.x, threads = blockDim.x;
-        int64_t s = tid;
-        if (sequences > threads) {
-            s += sequence_of_row(offsets, sequences, row0, lane);
-            if (s < sequences) {
-                from = offsets[s];
-                to = offsets[s + 1];
-            }
-        }
-        while (s < sequences && from < row0 + rows) {
-            if (to > from) {
-                if (from >= row0)
-                    heads[from - row0] = int(s);
-                if (to > row0 && to <= row0 + rows)
-                    ends[to - 1 - row0] = int(s);
-            }
-            s += threads;
-            if (s < sequences) {
-                from = offsets[s];
-                to = offsets[s + 1];
-            }
-        }
-    }
 };
 
 // ---------------------------------------------------------------- maps
@@ -687,7 +620,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForwa
         if (threadIdx.x < 2)
             parts.arrived[threadIdx.x] = 0;
         if constexpr (PACKED) {
-            RowMarks marks(q.offsets, q.sequences, head_seq, end_seq);
+            RowMarks<const int64_t*> marks(q.offsets, q.sequences, head_seq, end_seq);
             place = links.take_place(place_shared);
             marks.mark(q.offsets, q.sequences, int64_t(place) << w.tile_shift, w.tile_rows, head_seq, end_seq, lane);
             __syncthreads();
@@ -910,7 +843,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_backward_kernel(RecurBack
         if (threadIdx.x < 2)
             parts.arrived[threadIdx.x] = 0;
         if constexpr (PACKED) {
-            RowMarks marks(q.offsets, q.sequences, head_seq, end_seq);
+            RowMarks<const int64_t*> marks(q.offsets, q.sequences, head_seq, end_seq);
             place = links.take_place(place_shared);
             marks.mark(q.offsets, q.sequences, first_row(place), w.tile_rows, head_seq, end_seq, lane);
             __syncthreads();

@@ -355,3 +355,28 @@ def test_a_token_each_with_states_off_32_bytes(dtype):
     assert bool((after[:, d:] == 5.0).all()) and int((flat == 5.0).sum()) >= 8
     out, last = ps.gated_recurrence(x, gate, state=before[:, :d], state_out=before[:, :d])  # in place
     assert torch.equal(out, want[0]) and torch.equal(last, want[1])
+
+
+@pytest.mark.parametrize("d", [2, 65, 700])
+def test_empty_sequences_in_any_number(d):
+    """Hundreds of thousands of empty sequences in front of, between and behind others change nothing for these, and
+    hand on their states."""
+    lengths = [0] * 200000 + [50] + [0] * 9000 + [300] + [0] * 300000 + [1, 0, 2] + [0] * 8192 + [90] + [0] * 100000
+    lens = torch.tensor(lengths, device=DEV)
+    offsets = torch.cat([lens.new_zeros(1), lens.cumsum(0)])
+    held, empty = (lens > 0).nonzero()[:, 0], lens == 0
+    n = int(offsets[-1])
+    x, gate, dout = (rand(n, d, seed=i) for i in range(3))
+    state, dstate = (rand(len(lengths), d, seed=3 + i, dtype=torch.float32) for i in range(2))
+
+    def call(offsets, state, dstate):
+        carries = ps.recurrence_carries(x, offsets)
+        out, last = ps.gated_recurrence(x, gate, state, offsets=offsets, carries=carries)
+        return [out, *ps.gated_recurrence_backward(dout, x, gate, carries, state=state, dstate_out=dstate, offsets=offsets), last]
+
+    out, dx, dgate, ds, last = call(offsets, state, dstate)
+    few = call(torch.cat([offsets[:1], offsets[held + 1]]), state[held], dstate[held])
+    for got, want in zip((out, dx, dgate, ds[held], last[held]), few):
+        assert torch.equal(got, want)
+    assert torch.equal(last[empty], state[empty]) and torch.equal(ds[empty], dstate[empty])
+    assert ps.workspace_error_flags(DEV) == 0
