@@ -981,19 +981,43 @@ def _element_code(t) -> int:
 
 
 # A tensor on the current GPU without torch's dispatch: 0.7 us against 1.4 of new_empty; a step's calls make two or three.
+# Where torch fills new tensors (deterministic mode) or a dispatch mode watches them, and in a torch build whose inner
+# function is not what it was, torch's own call serves.
 try:
-    from torch._C._dynamo.guards import _empty_strided_cuda
-except ImportError:  # pragma: no cover - a torch build without it
-    def _empty_strided_cuda(shape, stride, dtype):
-        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+    from torch._C._dynamo.guards import _empty_strided_cuda as _quick_empty
+    from torch._C import _get_deterministic_algorithms, _len_torch_dispatch_stack
+except ImportError:  # pragma: no cover - a torch build without them
+    _quick_empty = None
+_quick_empty_holds: bool | None = None  # None: not tried yet
+
+
+def _is_as_asked(t, shape: tuple, stride: tuple, dtype) -> bool:
+    return t.is_cuda and t.get_device() == _current_device() and t.dtype is dtype and t.shape == shape and t.stride() == stride
+
+
+def _try_quick_empty() -> bool:
+    global _quick_empty_holds
+    asked = (2, 3), (3, 1), torch.float16
+    try:
+        _quick_empty_holds = _quick_empty is not None and _is_as_asked(_quick_empty(*asked), *asked)
+    except (TypeError, ValueError, RuntimeError):
+        _quick_empty_holds = False
+    return _quick_empty_holds
+
+
+def _empty_strided(shape: tuple, stride: tuple, dtype):
+    holds = _quick_empty_holds
+    if (_try_quick_empty() if holds is None else holds) and not _get_deterministic_algorithms() and not _len_torch_dispatch_stack():
+        return _quick_empty(shape, stride, dtype)
+    return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
 
 
 def _vector_of(n: int, dtype):
-    return _empty_strided_cuda((n,), (1,), dtype)
+    return _empty_strided((n,), (1,), dtype)
 
 
 def _matrix_of(rows: int, columns: int, dtype):
-    return _empty_strided_cuda((rows, columns), (columns or 1, 1), dtype)
+    return _empty_strided((rows, columns), (columns or 1, 1), dtype)
 
 
 def _rows_of(shape, dtype):
@@ -1002,7 +1026,7 @@ def _rows_of(shape, dtype):
         return _matrix_of(*shape, dtype)
     if len(shape) == 3:
         columns = shape[2] or 1
-        return _empty_strided_cuda(tuple(shape), ((shape[1] or 1) * columns, columns, 1), dtype)
+        return _empty_strided(tuple(shape), ((shape[1] or 1) * columns, columns, 1), dtype)
     return torch.empty(shape, dtype=dtype, device="cuda")
 
 

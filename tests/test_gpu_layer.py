@@ -156,3 +156,24 @@ def test_a_step_continues_where_the_last_ended():
     # |h| < 6; each way rounds an h some 300 times at most, with decays below 1
     assert float((torch.cat(parts) - whole[0]).abs().max()) < 300 * 6 * 2.0**-24 * 12
     assert float((state - final).abs().max()) < 300 * 6 * 2.0**-24 * 12
+
+
+def test_rows_that_no_place_names_in_deterministic_mode():
+    """torch's deterministic mode fills new tensors, and the rows that the calls leave alone show it: the same on
+    every run."""
+    x = torch.randn(6, 40, device=DEV)
+    places = torch.tensor([[0, 2], [1, -1], [-1, 3], [4, 5], [6, 7], [9, -1]], dtype=torch.int32, device=DEV)
+    named = places[places >= 0].long()
+    free = torch.ones(12, dtype=torch.bool, device=DEV)
+    free[named] = False
+    weights = torch.rand(6, 2, device=DEV)
+    rows = torch.randn(12, 40, device=DEV)
+    torch.use_deterministic_algorithms(True)
+    try:
+        got = ps.experts_gather(x, places)
+        drows, _ = ps.experts_combine_backward(x, rows, places, weights)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    for t in (got, drows):
+        assert bool(t[free].isnan().all()) and bool(torch.isfinite(t[named]).all())
+    assert bool(torch.isfinite(ps.experts_combine(rows, places, weights)).all())

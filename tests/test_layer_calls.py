@@ -34,3 +34,73 @@ def test_a_refused_call_makes_no_workspace(monkeypatch, kind, capturing, held):
     for refusal in (ps.LS_ERR_INVALID_ARG, ps.LS_ERR_UNSUPPORTED):
         st, _ = ps._with_workspace(lambda *a: refusal, (1, 2), kind, 0, need)
         assert st == refusal and made == []
+
+
+@pytest.fixture
+def allocations(monkeypatch):
+    """Which way outputs are made: the quick one, or torch's own call, on the CPU."""
+    made, strided = [], torch.empty_strided
+
+    def quick(shape, stride, dtype):
+        made.append("quick")
+        return strided(shape, stride, dtype=dtype)
+
+    def own(shape, stride, *, dtype, device):
+        made.append("torch")
+        assert device == "cuda"
+        return strided(shape, stride, dtype=dtype)
+
+    monkeypatch.setattr(ps, "_quick_empty", quick)
+    monkeypatch.setattr(ps, "_quick_empty_holds", None)
+    monkeypatch.setattr(ps, "_is_as_asked", lambda t, *asked: (t.dtype, tuple(t.shape), t.stride()) == (asked[2], *asked[:2]))
+    monkeypatch.setattr(torch, "empty_strided", own)
+    return made
+
+
+def outputs():
+    return ps._vector_of(5, torch.int64), ps._matrix_of(3, 4, torch.float16), ps._rows_of((2, 3, 4), torch.float32)
+
+
+def test_outputs_are_made_the_quick_way(allocations):
+    for t, shape in zip(outputs(), ((5,), (3, 4), (2, 3, 4))):
+        assert t.shape == shape and t.is_contiguous()
+    assert "torch" not in allocations
+
+
+def test_outputs_follow_torch_where_it_fills_or_watches(allocations):
+    """Deterministic mode fills new tensors, and a dispatch mode sees them: neither is gone round."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Mode(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            return func(*args, **(kwargs or {}))
+
+    outputs()
+    del allocations[:]
+    torch.use_deterministic_algorithms(True)
+    try:
+        outputs()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert allocations == ["torch"] * 3
+    with Mode():
+        outputs()
+    assert allocations == ["torch"] * 6
+    outputs()
+    assert allocations == ["torch"] * 6 + ["quick"] * 3
+
+
+@pytest.mark.parametrize("changed", ["signature", "type", "order", "missing"])
+def test_outputs_without_the_quick_way(monkeypatch, allocations, changed):
+    """A torch build whose inner function is not there or not the same: torch's own call serves."""
+    strided = torch._C._VariableFunctions.empty_strided
+
+    def other(a, b, c):
+        if changed == "signature":
+            raise TypeError("_empty_strided_cuda(): incompatible arguments")
+        return strided(a, b, dtype=torch.float64) if changed == "type" else strided(a, tuple(reversed(b)), dtype=c)
+
+    monkeypatch.setattr(ps, "_quick_empty", None if changed == "missing" else other)
+    for t, (shape, dtype) in zip(outputs(), (((5,), torch.int64), ((3, 4), torch.float16), ((2, 3, 4), torch.float32))):
+        assert t.shape == shape and t.dtype is dtype and t.is_contiguous()
+    assert allocations == ["torch"] * 3
