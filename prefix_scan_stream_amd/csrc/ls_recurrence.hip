@@ -706,8 +706,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void recur_forward_kernel(RecurForwa
                 m.a[c] *= a[j][c];
             }
         }
-        if constexpr (CHAINED && !PACKED) {
-            // the state is here before the map goes out: the chain's end may write it in place
+        if constexpr (!PACKED) {
+            // the state is here before the map goes out: the chain's end, or the wave that walked to the end, may write
+            // it in place
 #pragma unroll
             for (int c = 0; c < CPL; ++c)
                 asm volatile("" : "+v"(carry[c]));
