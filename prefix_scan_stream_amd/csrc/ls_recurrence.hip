@@ -1131,7 +1131,7 @@ struct ChainPlan {
     int waves;
     int64_t chains, tiles;
 };
-static ChainPlan chain_plan(int64_t sequences, int64_t rows, int64_t channels, bool packed, int per_lane, int wave_rows, int most_waves,
+static constexpr ChainPlan chain_plan(int64_t sequences, int64_t rows, int64_t channels, bool packed, int per_lane, int wave_rows, int most_waves,
                             int least_waves)
 {
     const int64_t chains = (packed ? 1 : sequences) * ((channels + 64 * per_lane - 1) / (64 * per_lane));
@@ -1143,13 +1143,28 @@ static ChainPlan chain_plan(int64_t sequences, int64_t rows, int64_t channels, b
 }
 
 template <int CPL>
-static ChainPlan plan_of(bool backward, int64_t sequences, int64_t rows, int64_t channels, bool packed)
+static constexpr ChainPlan plan_of(bool backward, int64_t sequences, int64_t rows, int64_t channels, bool packed)
 {
     using F = ForwardShape<CPL>;
     using B = BackwardShape<CPL>;
     return backward ? chain_plan(sequences, rows, channels, packed, CPL, B::rows, B::waves, RC_PERIOD / B::rows)
                     : chain_plan(sequences, rows, channels, packed, CPL, F::rows, F::waves, 1);
 }
+
+// A block of fewer waves holds all rows in its one tile.  Of several tiles, each block has the link and a wave for
+// every map that it collects: Chain::compose waits for them without a limit of its own.
+template <int CPL>
+static constexpr bool tiles_have_collectors()
+{
+    for (int64_t rows = 0; rows <= 4 * RC_TILE; ++rows)
+        for (int which = 0; which < 4; ++which) {
+            const ChainPlan p = plan_of<CPL>(which % 2 != 0, 1, rows, 64, which / 2 != 0);
+            if (p.tiles > 1 && p.waves < RC_GROUP)
+                return false;
+        }
+    return true;
+}
+static_assert(tiles_have_collectors<1>() && tiles_have_collectors<2>(), "a group's maps need a wave each");
 
 template <int CPL>
 static size_t chain_bytes(int64_t sequences, int64_t rows, int64_t channels, bool packed)
