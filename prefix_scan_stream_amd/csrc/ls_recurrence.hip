@@ -553,7 +553,7 @@ struct Work {
     int64_t chain, c0;                        // sequence, first channel
     uint32_t here;                            // channels
     int64_t rows;                             // there are
-    int tiles, places;                        // tiles of the call, and those with rows
+    int places;                               // tiles with rows
 
     __device__ __forceinline__ Work(int rows_per_wave, int64_t sequences, int64_t call_rows, int64_t channels, const int64_t* offsets)
     {
@@ -575,7 +575,6 @@ struct Work {
             const int64_t live = offsets[sequences];
             rows = int64_t(uniform(uint64_t(live < 0 ? 0 : live < rows ? live : rows)));
         }
-        tiles = call_rows > 0 ? int((call_rows + tile_rows - 1) >> tile_shift) : 1;
         places = int((rows + tile_rows - 1) >> tile_shift);
     }
 };
