@@ -972,6 +972,7 @@ def pages_release(lens: torch.Tensor, finished: torch.Tensor, tables: torch.Tens
 
 
 # ------------------------------------------------------------ a layer's scans
+# Calls, not autograd: none records anything for it, also of tensors that require grad.
 
 def _element_code(t) -> int:
     code = LOGITS_CODES.get(t.dtype)

@@ -21,10 +21,14 @@
 // row, in 32 bits; the output h would cost as many bytes and is rounded.
 //
 // What bounds it: memory, three elements a token and channel forward and five backward, where blocks walk (64 sequences
-// of 512 tokens of 2048 bfloat16 channels: 74 us forward, 5.4 TB/s, 132 backward, 5.1); and where tiles are
+// of 512 tokens of 2048 bfloat16 channels: 74-76 us forward, 5.4 TB/s, 132-141 backward, 4.8-5.1); and where tiles are
 // blocks also the wait for the value in front, which holds a block's registers while nothing of it is
-// under way (1 x 65536 x 2048: 186 and 342 us, 4.3 and 3.9 TB/s; without the link, so with wrong values, 137 forward).
-// A CU holds two such blocks (three backward).  Tried there and not kept: blocks that stay and load the next tile while they
+// under way (1 x 65536 x 2048, log: 184-192 and 308 us, 4.3 TB/s both; without the link, so with wrong values, 137 forward).
+// Blocks of 8 waves that a CU holds, by their registers: forward with two channels a lane two (90-101 registers for tiles, 112-114
+// for blocks that walk), with one three or four (53-60, 76-78); backward with two channels two with a sigmoid (82-86; packed with
+// more than four chains 80: three), else three for more than four chains (78-80) and two for fewer (82-85), blocks that walk three or
+// four (62-77); with one three (67-75; 16 bits, a sigmoid and packed 83: two).
+// Tried for tiles and not kept: blocks that stay and load the next tile while they
 // wait (230 to 365 us forward: one block a CU), raw rows kept and the maps made again for three or four blocks a CU (185 to 193:
 // registers spill), one 16-bit channel a lane (backward 310, but 323 against 272 for 8 x 4096 x 4096).
 //
@@ -1112,6 +1116,10 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurForward q)
 // Blocks that walk keep the carry to themselves and load ahead; they take the call where the chains alone fill the
 // GPU, or where a chain is one tile.  From 256 chains on: 8 x 4096 x 4096 (256) forward 151 us against 166, but 6 x 4096 x
 // 8192 (384) 256 against 238, and backward slower in both; from 2048 on: 64 x 512 x 2048 (1024) 84 against 75.
+// 512 such blocks run at once forward, so just above it the second round is nearly empty, and tiles would be faster: of 4096
+// tokens of bfloat16, 512 chains walk in 289 and 526 us, 520 in 391 and 701 against 328 and 593 as tiles, 576 in 408 and 739
+// against 366 and 662, 704 in 464 and 812 against 449 and 809, 768 in 462 and 798 against 514 and 912, 900 in 596 and 1076 against
+// 575 and 1040, 1024 in 598 and 1103 against 669 and 1259, 2048 in 1228 and 2154 against 1348 and 2528.
 constexpr int64_t RC_WALKERS = 512;
 
 // Tokens per wave, and waves, of a tile.  1 x 65536 x 2048 forward with 8 tokens a wave 237 us against 183; backward of two
